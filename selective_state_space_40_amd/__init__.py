@@ -1,6 +1,7 @@
 """Selective state-space scan for AMD Instinct MI355X (gfx950).
 
-Python binding of the C ABI in include/mamba_scan.h. It only marshals
+Python binding of the C ABI in include/mamba_scan.h and
+include/mamba_layers.h. It only marshals
 arguments: it checks shapes and dtypes, allocates outputs and scratch with
 torch on the tensors' device, and passes raw device pointers and the current
 HIP stream to libmamba_scan.so, whose kernels do every step of the scan.
@@ -16,6 +17,11 @@ There is no other code path: without the built library every call raises.
     y, hL = ssd_fwd(x, dt, A_heads, B, C, D=None, z=None, h0=None)   # Mamba-2 dual form
     y, state = conv1d_fwd(x, weight, bias=None, state_in=None, silu=True)
     y = conv1d_update(state, x, weight, bias=None, silu=True)  # state updated in place
+    o, hL = linear_attn_fwd(q, k, v, log_decay, h0=None, lengths=None)
+    grads = linear_attn_bwd(q, k, v, log_decay, h0=None, do=do, dhL=None, lengths=None)
+    o = linear_attn_update(h, q, k, v, log_decay)              # h updated in place
+    y, mean, rstd = layer_norm_fwd(x, weight=None, bias=None, groups=1)
+    grads = layer_norm_bwd(x, weight, mean, rstd, dy=dy, groups=1)
 
 Shapes (row-major, contiguous): x, delta, z, y (batch, L, dim); B, C
 (batch, L, N); A (dim, N) fp32; D and delta_bias (dim,) fp32; h0, hL
@@ -24,6 +30,10 @@ softplus(delta + delta_bias) in place of delta. The short convolution takes
 x, y (batch, L, dim), weight (dim, W) fp32, bias (dim,) fp32 and a state of
 the last W inputs (batch, dim, W) in the dtype of x.
 x, delta, z, B and C share one dtype, float32 or bfloat16, and y has it too.
+Linear attention takes q, o (batch, L, heads, dk or dv), k, v (batch, L,
+kv_heads, dk or dv), log_decay (heads,) fp32, states (batch, heads, dk, dv) fp32
+and lengths (batch,) int32; layer norm x, y (..., dim), weight and bias (dim,)
+fp32, mean and rstd (..., groups) fp32.
 """
 import collections
 import ctypes
@@ -31,7 +41,9 @@ import os
 
 import torch
 
-__all__ = ["scan_fwd", "scan_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "scan_bwd", "ssd_fwd", "state_update", "conv1d_fwd", "conv1d_update", "workspace_size", "resolve_plan", "library_path",
+__all__ = ["scan_fwd", "scan_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "scan_bwd", "ssd_fwd", "state_update", "conv1d_fwd", "conv1d_update",
+           "linear_attn_fwd", "linear_attn_bwd", "linear_attn_update", "layer_norm_fwd",
+           "layer_norm_bwd", "workspace_size", "resolve_plan", "library_path",
            "load_library", "MambaScanError", "MAX_DSTATE", "ScanPlan", "ScanOptions", "Plan",
            "CARRY_AUTO", "CARRY_RERUN", "CARRY_REPAIR", "HALVES_AUTO", "HALVES_NONE"]
 
@@ -115,6 +127,23 @@ def load_library():
     lib.causal_conv1d_fwd.restype = i32
     lib.causal_conv1d_update.argtypes = [i64, i64, i32, i32] + [vp] * 5 + [i32, vp]
     lib.causal_conv1d_update.restype = i32
+    sz = ctypes.c_size_t
+    for fn in (lib.linear_attn_fwd_workspace_size, lib.linear_attn_bwd_workspace_size):
+        fn.argtypes = [i64] * 6 + [i32, i64, ctypes.POINTER(sz)]
+        fn.restype = i32
+    f32 = ctypes.c_float
+    lib.linear_attn_fwd.argtypes = [i64] * 6 + [i32] + [vp] * 6 + [f32] + [vp] * 2 + [i64, vp, sz, vp]
+    lib.linear_attn_fwd.restype = i32
+    lib.linear_attn_bwd.argtypes = [i64] * 6 + [i32] + [vp] * 6 + [f32] + [vp] * 7 + [i64, vp, sz, vp]
+    lib.linear_attn_bwd.restype = i32
+    lib.linear_attn_update.argtypes = [i64] * 5 + [i32] + [vp] * 5 + [f32, vp, vp]
+    lib.linear_attn_update.restype = i32
+    lib.layer_norm_fwd.argtypes = [i64] * 3 + [i32] + [vp] * 3 + [f32] + [vp] * 4
+    lib.layer_norm_fwd.restype = i32
+    lib.layer_norm_bwd_workspace_size.argtypes = [i64] * 3 + [i32, ctypes.POINTER(sz)]
+    lib.layer_norm_bwd_workspace_size.restype = i32
+    lib.layer_norm_bwd.argtypes = [i64] * 3 + [i32] + [vp] * 9 + [sz, vp]
+    lib.layer_norm_bwd.restype = i32
     lib.mamba_status_string.argtypes = [i32]
     lib.mamba_status_string.restype = ctypes.c_char_p
     _LIB = lib
@@ -499,3 +528,195 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, h0=None, *, dt_bias=None, dt_softplu
                          _stream(dev))
     _check(st, "ssd_fwd")
     return y, hL
+
+
+def _scratch(device, nbytes):
+    """Scratch of one call, from torch's allocator on the current stream: a
+    captured graph keeps its own, and calls on different streams share none."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _attn_shapes(q, k, v, log_decay, ndim):
+    """(batch, L, heads, kv_heads, dk, dv) of q, k and v, checked against each
+    other; L is 1 for single tokens (ndim 3)."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must be (batch, {'L, ' if ndim == 4 else ''}heads, size)")
+    lead = tuple(q.shape[:-2])
+    heads, dk = q.shape[-2:]
+    kv_heads, dv = v.shape[-2:]
+    if kv_heads == 0 and heads or kv_heads and heads % kv_heads:
+        raise ValueError(f"q has {heads} heads, not a multiple of the {kv_heads} of k and v")
+    dev, dt = q.device, q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported I/O dtype {dt}")
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    _need(q, "q", (*lead, heads, dk), dt, dev)
+    _need(k, "k", (*lead, kv_heads, dk), dt, dev)
+    _need(v, "v", (*lead, kv_heads, dv), dt, dev)
+    _need(log_decay, "log_decay", (heads,), torch.float32, dev)
+    return lead[0], (lead[1] if ndim == 4 else 1), heads, kv_heads, dk, dv
+
+
+def linear_attn_fwd(q, k, v, log_decay, h0=None, *, lengths=None, scale=None, return_state=True,
+                    out=None, state_out=None, segment_len=0):
+    """Linear attention with a decay exp(log_decay[h]) for each head over whole
+    sequences: S_t = decay S_(t-1) + k_t^T v_t, o_t = scale q_t S_t. q (batch, L,
+    heads, dk); k, v (batch, L, kv_heads, dk or dv), each shared by heads /
+    kv_heads heads; `lengths` (batch,) int32 the tokens of each row (None: L),
+    behind which o is zero; h0 (batch, heads, dk, dv) fp32; `scale` dk ** -0.5
+    by default. Returns (o, hL), hL (None when return_state is False) the state
+    after each row's last token; state_out may be h0. `segment_len` > 0 (a
+    multiple of 64) forces the parallel segments' length."""
+    lib = load_library()
+    batch, seqlen, heads, kv_heads, dk, dv = _attn_shapes(q, k, v, log_decay, 4)
+    dev, dt = q.device, q.dtype
+    _need(h0, "h0", (batch, heads, dk, dv), torch.float32, dev)
+    _need(lengths, "lengths", (batch,), torch.int32, dev)
+    o = out if out is not None else torch.empty(batch, seqlen, heads, dv, dtype=dt, device=dev)
+    _need(o, "out", (batch, seqlen, heads, dv), dt, dev)
+    hL = None
+    if return_state:
+        hL = state_out if state_out is not None else torch.empty(batch, heads, dk, dv,
+                                                                 dtype=torch.float32, device=dev)
+        _need(hL, "state_out", (batch, heads, dk, dv), torch.float32, dev)
+    with torch.cuda.device(dev):
+        nbytes = ctypes.c_size_t(0)
+        _check(lib.linear_attn_fwd_workspace_size(batch, seqlen, heads, kv_heads, dk, dv,
+                                                  _DTYPES[dt], segment_len, ctypes.byref(nbytes)),
+               "linear_attn_fwd_workspace_size")
+        ws = _scratch(dev, nbytes.value)
+        st = lib.linear_attn_fwd(batch, seqlen, heads, kv_heads, dk, dv, _DTYPES[dt], _ptr(q),
+                                 _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(h0),
+                                 dk ** -0.5 if scale is None else scale, _ptr(o), _ptr(hL),
+                                 segment_len, _ptr(ws), nbytes.value, _stream(dev))
+    _check(st, "linear_attn_fwd")
+    return o, hL
+
+
+def linear_attn_bwd(q, k, v, log_decay, h0=None, *, do, dhL=None, lengths=None, scale=None,
+                    want_dlog_decay=True, want_dh0=True, segment_len=0):
+    """Gradients of sum(do * o) + sum(dhL * hL) for the linear_attn_fwd call
+    with the same inputs. Returns a dict: dq, dk, dv (like q, k, v; zero behind
+    a row's length); dlog_decay (heads,) fp32 and dh0 (batch, heads, dk, dv)
+    fp32, None when not wanted."""
+    lib = load_library()
+    batch, seqlen, heads, kv_heads, dk, dv = _attn_shapes(q, k, v, log_decay, 4)
+    dev, dt = q.device, q.dtype
+    _need(h0, "h0", (batch, heads, dk, dv), torch.float32, dev)
+    _need(lengths, "lengths", (batch,), torch.int32, dev)
+    if do is None:
+        raise ValueError("do (the gradient at the output) is required")
+    _need(do, "do", (batch, seqlen, heads, dv), dt, dev)
+    _need(dhL, "dhL", (batch, heads, dk, dv), torch.float32, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+             dlog_decay=torch.empty(heads, **f32) if want_dlog_decay else None,
+             dh0=torch.empty(batch, heads, dk, dv, **f32) if want_dh0 else None)
+    with torch.cuda.device(dev):
+        nbytes = ctypes.c_size_t(0)
+        _check(lib.linear_attn_bwd_workspace_size(batch, seqlen, heads, kv_heads, dk, dv,
+                                                  _DTYPES[dt], segment_len, ctypes.byref(nbytes)),
+               "linear_attn_bwd_workspace_size")
+        ws = _scratch(dev, nbytes.value)
+        st = lib.linear_attn_bwd(batch, seqlen, heads, kv_heads, dk, dv, _DTYPES[dt], _ptr(q),
+                                 _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(h0),
+                                 dk ** -0.5 if scale is None else scale, _ptr(do), _ptr(dhL),
+                                 _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
+                                 _ptr(g["dlog_decay"]), _ptr(g["dh0"]), segment_len, _ptr(ws),
+                                 nbytes.value, _stream(dev))
+    _check(st, "linear_attn_bwd")
+    return g
+
+
+def linear_attn_update(h, q, k, v, log_decay, *, scale=None, out=None):
+    """One token of linear attention: h (batch, heads, dk, dv) fp32 is updated
+    in place; q (batch, heads, dk), k, v (batch, kv_heads, dk or dv); returns o
+    (batch, heads, dv)."""
+    lib = load_library()
+    batch, _, heads, kv_heads, dk, dv = _attn_shapes(q, k, v, log_decay, 3)
+    dev, dt = q.device, q.dtype
+    if h is None:
+        raise ValueError("h (the state) is required")
+    _need(h, "h", (batch, heads, dk, dv), torch.float32, dev)
+    o = out if out is not None else torch.empty(batch, heads, dv, dtype=dt, device=dev)
+    _need(o, "out", (batch, heads, dv), dt, dev)
+    with torch.cuda.device(dev):
+        st = lib.linear_attn_update(batch, heads, kv_heads, dk, dv, _DTYPES[dt], _ptr(h), _ptr(q),
+                                    _ptr(k), _ptr(v), _ptr(log_decay),
+                                    dk ** -0.5 if scale is None else scale, _ptr(o), _stream(dev))
+    _check(st, "linear_attn_update")
+    return o
+
+
+def _norm_shapes(x, weight, groups):
+    """(rows, dim) of x, checked with the parameters."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() < 1:
+        raise ValueError("x must be (..., dim)")
+    dim = x.shape[-1]
+    if groups < 1 or dim % groups:
+        raise ValueError(f"{dim} channels do not split into {groups} groups")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported I/O dtype {x.dtype}")
+    if x.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    _need(x, "x", x.shape, x.dtype, x.device)
+    _need(weight, "weight", (dim,), torch.float32, x.device)
+    return x.numel() // dim if dim else 0, dim
+
+
+def layer_norm_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out=None):
+    """Layer norm over each of the `groups` equal parts of the last dimension:
+    y = (x - mean) * rstd * weight + bias with rstd = (var + eps) ** -0.5.
+    weight and bias (dim,) fp32. Returns (y, mean, rstd), mean and rstd
+    (..., groups) fp32, which layer_norm_bwd takes; out may be x."""
+    lib = load_library()
+    rows, dim = _norm_shapes(x, weight, groups)
+    dev, dt = x.device, x.dtype
+    _need(bias, "bias", (dim,), torch.float32, dev)
+    y = out if out is not None else torch.empty_like(x)
+    _need(y, "out", x.shape, dt, dev)
+    mean = torch.empty(*x.shape[:-1], groups, dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    with torch.cuda.device(dev):
+        st = lib.layer_norm_fwd(rows, dim, groups, _DTYPES[dt], _ptr(x), _ptr(weight), _ptr(bias),
+                                eps, _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev))
+    _check(st, "layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x, weight, mean, rstd, *, dy, groups=1, want_dbias=True, out=None):
+    """Gradients of sum(dy * y) for the layer_norm_fwd call with the same x and
+    weight, mean and rstd from it. Returns a dict: dx (like x; out may be dy),
+    dweight (dim,) fp32 (None without a weight) and dbias (dim,) fp32 (None
+    when not wanted)."""
+    lib = load_library()
+    rows, dim = _norm_shapes(x, weight, groups)
+    dev, dt = x.device, x.dtype
+    for t, name in ((mean, "mean"), (rstd, "rstd"), (dy, "dy")):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    _need(mean, "mean", (*x.shape[:-1], groups), torch.float32, dev)
+    _need(rstd, "rstd", (*x.shape[:-1], groups), torch.float32, dev)
+    _need(dy, "dy", x.shape, dt, dev)
+    dx = out if out is not None else torch.empty_like(x)
+    _need(dx, "out", x.shape, dt, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    g = dict(dx=dx, dweight=None if weight is None else torch.empty(dim, **f32),
+             dbias=torch.empty(dim, **f32) if want_dbias else None)
+    with torch.cuda.device(dev):
+        nbytes = ctypes.c_size_t(0)
+        _check(lib.layer_norm_bwd_workspace_size(rows, dim, groups, _DTYPES[dt],
+                                                 ctypes.byref(nbytes)),
+               "layer_norm_bwd_workspace_size")
+        ws = _scratch(dev, nbytes.value)
+        st = lib.layer_norm_bwd(rows, dim, groups, _DTYPES[dt], _ptr(x), _ptr(weight), _ptr(mean),
+                                _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(g["dweight"]),
+                                _ptr(g["dbias"]), _ptr(ws), nbytes.value, _stream(dev))
+    _check(st, "layer_norm_bwd")
+    return g

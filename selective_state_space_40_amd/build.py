@@ -24,7 +24,12 @@ UNITS = [("api", "api.cpp", ()), ("noalloc", "noalloc.hip", ()), ("launch", "lau
          ("scan_bwd", "scan_bwd.hip", ()), ("ssd", "ssd.hip", ())] + [
     (f"scan_io{io}_sp{sp}_n{part}", "scan_variant.hip",
      (f"-DMAMBA_VARIANT_IO={io}", f"-DMAMBA_VARIANT_SP={sp}", f"-DMAMBA_VARIANT_PART={part}"))
-    for io in (0, 1) for sp in (0, 1) for part in (0, 1)]
+    for io in (0, 1) for sp in (0, 1) for part in (0, 1)] + [
+    ("api_layers", "api_layers.cpp", ()), ("linear_attn", "linear_attn.hip", ()),
+    ("layer_norm", "layer_norm.hip", ())] + [
+    (f"linear_attn_io{io}_m{mode}", "linear_attn_variant.hip",
+     (f"-DMAMBA_VARIANT_IO={io}", f"-DMAMBA_VARIANT_MODE={mode}"))
+    for io in (0, 1) for mode in (0, 1, 2)]
 
 
 def hipcc():

@@ -25,6 +25,10 @@ static_assert(mamba::kConvMaxWidth == MAMBA_CONV_MAX_WIDTH, "convolution width l
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_cu_count[kMaxDevices];  // 0 = not queried yet
 
+}  // namespace
+
+namespace mamba {
+
 // Compute units of the current device (cached per device).
 int current_cu_count(int* cu) {
     int dev = 0;
@@ -43,6 +47,12 @@ int current_cu_count(int* cu) {
     *cu = n;
     return MAMBA_OK;
 }
+
+}  // namespace mamba
+
+namespace {
+
+using mamba::current_cu_count;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

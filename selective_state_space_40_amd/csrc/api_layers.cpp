@@ -1,0 +1,331 @@
+// C ABI of linear attention and layer norm (mamba_layers.h): argument checks,
+// the automatic plans and error mapping around linear_attn.hip,
+// linear_attn_variant.hip and layer_norm.hip. Every check runs on the host
+// before any launch; the compute-unit query of the automatic plans is the
+// only HIP call made before the arguments are known to be good.
+#include <hip/hip_runtime_api.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "mamba_layers.h"
+
+namespace {
+
+using mamba::LinearAttnCall;
+using mamba::LinPlan;
+
+static_assert(mamba::kLinMaxDim == MAMBA_LINATTN_MAX_DIM, "head width limit");
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool known_dtype(int dtype) { return dtype == MAMBA_DTYPE_F32 || dtype == MAMBA_DTYPE_BF16; }
+
+int io_of(int dtype) { return dtype == MAMBA_DTYPE_F32 ? mamba::kIoF32 : mamba::kIoBF16; }
+
+template <int N>
+int check_aligned(const void* const (&ptrs)[N]) {
+    for (const void* p : ptrs)
+        if (p != nullptr && !aligned16(p)) return MAMBA_ERR_MISALIGNED;
+    return MAMBA_OK;
+}
+
+// Tokens per chunk of the widest-chunked kernel: segments are whole chunks of it.
+constexpr int64_t kSegUnit = 64;
+// Workgroups a launch holds at most, and elements of a tensor.
+constexpr int64_t kMaxBlocks = int64_t(1) << 30;
+constexpr int64_t kMaxElems = int64_t(1) << 48;
+
+int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, int64_t dk, int64_t dv,
+               int dtype, int64_t segment_len) {
+    if (batch < 0 || seqlen < 0 || heads < 0 || kv_heads < 0 || dk < 1 || dv < 1 || segment_len < 0)
+        return MAMBA_ERR_INVALID_ARG;
+    if (!known_dtype(dtype) || segment_len % kSegUnit != 0) return MAMBA_ERR_INVALID_ARG;
+    if (heads > 0 ? (kv_heads == 0 || heads % kv_heads != 0) : kv_heads != 0) return MAMBA_ERR_INVALID_ARG;
+    if (dk > MAMBA_LINATTN_MAX_DIM || dv > MAMBA_LINATTN_MAX_DIM || dk % MAMBA_LINATTN_DIM_UNIT != 0 ||
+        dv % MAMBA_LINATTN_DIM_UNIT != 0 || heads > MAMBA_LINATTN_MAX_HEADS)
+        return MAMBA_ERR_UNSUPPORTED;
+    if (batch > (int64_t(1) << 24) || seqlen > kMaxElems / (MAMBA_LINATTN_MAX_HEADS * MAMBA_LINATTN_MAX_DIM))
+        return MAMBA_ERR_UNSUPPORTED;
+    if (batch > 0 && seqlen > 0 &&
+        seqlen > kMaxElems / (int64_t(MAMBA_LINATTN_MAX_HEADS) * MAMBA_LINATTN_MAX_DIM) / batch)
+        return MAMBA_ERR_UNSUPPORTED;
+    return MAMBA_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a call is divided. `passes` workgroups run per (row, head, segment,
+// column block): one forward, three backward, whose widest head decides.
+int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, LinPlan* p) {
+    const int64_t wide = passes == 1 ? c.dv : (c.dk > c.dv ? c.dk : c.dv);
+    const int64_t deep = passes == 1 ? c.dk : wide;
+    p->block_cols = wide > 64 && deep <= 128 ? 128 : 64;
+    p->seg_len = c.seqlen > 0 ? c.seqlen : 1;
+    p->nseg = 1;
+    if (c.batch == 0 || c.heads == 0 || c.seqlen == 0) return MAMBA_OK;
+    int64_t seg = segment_len;
+    if (seg == 0) {
+        int cu = 0;
+        const int st = mamba::current_cu_count(&cu);
+        if (st != MAMBA_OK) return st;
+        const int64_t units = c.batch * c.heads * ceil_div(wide, p->block_cols) * passes;
+        int64_t n = (2 * int64_t(cu)) / units;
+        const int64_t most = c.seqlen / 256;
+        if (n > most) n = most;
+        seg = n >= 2 ? ceil_div(ceil_div(c.seqlen, n), kSegUnit) * kSegUnit : c.seqlen;
+    }
+    if (seg < c.seqlen) {
+        const int64_t n = ceil_div(c.seqlen, seg);
+        if (n > (int64_t(1) << 16)) return MAMBA_ERR_UNSUPPORTED;
+        p->seg_len = seg;
+        p->nseg = static_cast<int>(n);
+    }
+    const int64_t blocks = c.batch * c.heads * p->nseg;
+    if (blocks > kMaxBlocks / (passes * ceil_div(wide, p->block_cols))) return MAMBA_ERR_UNSUPPORTED;
+    // and a block per window of the decay's gradient
+    if (passes > 1 && c.batch * c.heads > kMaxBlocks / (c.seqlen / mamba::kLinWindow + p->nseg + 1))
+        return MAMBA_ERR_UNSUPPORTED;
+    // the join's launch holds (row, head) in a 16-bit grid dimension
+    if (p->nseg > 1 && c.batch * c.heads > 65535) {
+        if (segment_len != 0) return MAMBA_ERR_UNSUPPORTED;
+        p->nseg = 1;
+        p->seg_len = c.seqlen;
+    }
+    return MAMBA_OK;
+}
+
+LinearAttnCall attn_call(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, int64_t dk,
+                         int64_t dv, int dtype) {
+    LinearAttnCall c = {};
+    c.batch = batch;
+    c.seqlen = seqlen;
+    c.heads = static_cast<int>(heads);
+    c.kv_heads = static_cast<int>(kv_heads);
+    c.dk = static_cast<int>(dk);
+    c.dv = static_cast<int>(dv);
+    c.io = io_of(dtype);
+    return c;
+}
+
+int attn_workspace(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, int64_t dk, int64_t dv,
+                   int dtype, int64_t segment_len, int passes, size_t* bytes) {
+    if (bytes == nullptr) return MAMBA_ERR_INVALID_ARG;
+    int st = check_attn(batch, seqlen, heads, kv_heads, dk, dv, dtype, segment_len);
+    if (st != MAMBA_OK) return st;
+    const LinearAttnCall c = attn_call(batch, seqlen, heads, kv_heads, dk, dv, dtype);
+    LinPlan p;
+    st = make_attn_plan(c, passes, segment_len, &p);
+    if (st != MAMBA_OK) return st;
+    *bytes = mamba::linear_attn_workspace_bytes(c, p, passes > 1);
+    return MAMBA_OK;
+}
+
+int check_norm(int64_t rows, int64_t dim, int64_t groups, int dtype) {
+    if (rows < 0 || dim < 0 || groups < 1 || !known_dtype(dtype) || dim % groups != 0)
+        return MAMBA_ERR_INVALID_ARG;
+    if (dim / groups > MAMBA_NORM_MAX_DIM) return MAMBA_ERR_UNSUPPORTED;
+    if (dim > (int64_t(1) << 30) || (dim > 0 && rows > kMaxElems / dim) ||
+        rows > kMaxBlocks / groups)
+        return MAMBA_ERR_UNSUPPORTED;
+    return MAMBA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
+                                   int64_t dk, int64_t dv, int dtype, int64_t segment_len,
+                                   size_t* bytes) {
+    return attn_workspace(batch, seqlen, heads, kv_heads, dk, dv, dtype, segment_len, 1, bytes);
+}
+
+int linear_attn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
+                                   int64_t dk, int64_t dv, int dtype, int64_t segment_len,
+                                   size_t* bytes) {
+    return attn_workspace(batch, seqlen, heads, kv_heads, dk, dv, dtype, segment_len, 3, bytes);
+}
+
+int linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, int64_t dk,
+                    int64_t dv, int dtype, const void* q, const void* k, const void* v,
+                    const float* log_decay, const int32_t* lengths, const float* h0, float scale,
+                    void* o, float* hL, int64_t segment_len, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+    int st = check_attn(batch, seqlen, heads, kv_heads, dk, dv, dtype, segment_len);
+    if (st != MAMBA_OK) return st;
+    if (batch == 0 || heads == 0) return MAMBA_OK;
+    if (log_decay == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (seqlen > 0 && (q == nullptr || k == nullptr || v == nullptr || o == nullptr))
+        return MAMBA_ERR_INVALID_ARG;
+    const void* const ptrs[] = {q, k, v, log_decay, lengths, h0, o, hL, workspace};
+    st = check_aligned(ptrs);
+    if (st != MAMBA_OK) return st;
+    if (seqlen == 0 && hL == nullptr) return MAMBA_OK;
+    LinearAttnCall c = attn_call(batch, seqlen, heads, kv_heads, dk, dv, dtype);
+    LinPlan p;
+    st = make_attn_plan(c, 1, segment_len, &p);
+    if (st != MAMBA_OK) return st;
+    const size_t need = mamba::linear_attn_workspace_bytes(c, p, false);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+    c.scale = scale;
+    c.q = q;
+    c.k = k;
+    c.v = v;
+    c.log_decay = log_decay;
+    c.lengths = lengths;
+    c.h0 = h0;
+    c.o = o;
+    c.hL = hL;
+    return mamba::launch_linear_attn_fwd(c, p, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+int linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, int64_t dk,
+                    int64_t dv, int dtype, const void* q, const void* k, const void* v,
+                    const float* log_decay, const int32_t* lengths, const float* h0, float scale,
+                    const void* d_o, const float* dhL, void* dq, void* d_k, void* d_v,
+                    float* dlog_decay, float* dh0, int64_t segment_len, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+    int st = check_attn(batch, seqlen, heads, kv_heads, dk, dv, dtype, segment_len);
+    if (st != MAMBA_OK) return st;
+    if (heads == 0) return MAMBA_OK;
+    if (log_decay == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (batch > 0 && seqlen > 0 &&
+        (q == nullptr || k == nullptr || v == nullptr || d_o == nullptr || dq == nullptr || d_k == nullptr ||
+         d_v == nullptr))
+        return MAMBA_ERR_INVALID_ARG;
+    const void* const ptrs[] = {q, k, v, log_decay, lengths, h0, d_o, dhL, dq, d_k, d_v, dlog_decay, dh0,
+                                workspace};
+    st = check_aligned(ptrs);
+    if (st != MAMBA_OK) return st;
+    LinearAttnCall c = attn_call(batch, seqlen, heads, kv_heads, dk, dv, dtype);
+    LinPlan p;
+    st = make_attn_plan(c, 3, segment_len, &p);
+    if (st != MAMBA_OK) return st;
+    const size_t need = mamba::linear_attn_workspace_bytes(c, p, true);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+    c.scale = scale;
+    c.q = q;
+    c.k = k;
+    c.v = v;
+    c.log_decay = log_decay;
+    c.lengths = lengths;
+    c.h0 = h0;
+    c.d_o = d_o;
+    c.dhL = dhL;
+    c.dq = dq;
+    c.d_k = d_k;
+    c.d_v = d_v;
+    c.dlog_decay = dlog_decay;
+    c.dh0 = dh0;
+    return mamba::launch_linear_attn_bwd(c, p, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+int linear_attn_update(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dk, int64_t dv,
+                       int dtype, float* h, const void* q, const void* k, const void* v,
+                       const float* log_decay, float scale, void* o, hipStream_t stream) {
+    int st = check_attn(batch, 1, heads, kv_heads, dk, dv, dtype, 0);
+    if (st != MAMBA_OK) return st;
+    if (batch == 0 || heads == 0) return MAMBA_OK;
+    if (h == nullptr || q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || o == nullptr)
+        return MAMBA_ERR_INVALID_ARG;
+    const void* const ptrs[] = {h, q, k, v, log_decay, o};
+    st = check_aligned(ptrs);
+    if (st != MAMBA_OK) return st;
+    if (batch * heads > kMaxBlocks / (MAMBA_LINATTN_MAX_DIM / 64)) return MAMBA_ERR_UNSUPPORTED;
+    mamba::LinUpdateArgs a = {};
+    a.batch = batch;
+    a.heads = static_cast<int>(heads);
+    a.kv_heads = static_cast<int>(kv_heads);
+    a.dk = static_cast<int>(dk);
+    a.dv = static_cast<int>(dv);
+    a.io = io_of(dtype);
+    a.scale = scale;
+    a.h = h;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.log_decay = log_decay;
+    a.o = o;
+    return mamba::launch_linear_attn_update(a, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+int layer_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int dtype, const void* x,
+                   const float* weight, const float* bias, float eps, void* y, float* mean,
+                   float* rstd, hipStream_t stream) {
+    int st = check_norm(rows, dim, groups, dtype);
+    if (st != MAMBA_OK) return st;
+    if (!(eps >= 0.0f) || !isfinite(eps)) return MAMBA_ERR_INVALID_ARG;
+    if (rows == 0 || dim == 0) return MAMBA_OK;
+    if (x == nullptr || y == nullptr) return MAMBA_ERR_INVALID_ARG;
+    const void* const ptrs[] = {x, weight, bias, y, mean, rstd};
+    st = check_aligned(ptrs);
+    if (st != MAMBA_OK) return st;
+    mamba::NormArgs a = {};
+    a.rows = rows;
+    a.dim = dim;
+    a.groups = groups;
+    a.io = io_of(dtype);
+    a.eps = eps;
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    return mamba::launch_layer_norm_fwd(a, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+int layer_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t groups, int dtype,
+                                  size_t* bytes) {
+    if (bytes == nullptr) return MAMBA_ERR_INVALID_ARG;
+    int st = check_norm(rows, dim, groups, dtype);
+    if (st != MAMBA_OK) return st;
+    *bytes = 0;
+    if (rows == 0 || dim == 0) return MAMBA_OK;
+    int cu = 0;
+    st = mamba::current_cu_count(&cu);
+    if (st != MAMBA_OK) return st;
+    *bytes = mamba::layer_norm_bwd_workspace_bytes(rows, dim, groups, cu);
+    return MAMBA_OK;
+}
+
+int layer_norm_bwd(int64_t rows, int64_t dim, int64_t groups, int dtype, const void* x,
+                   const float* weight, const float* mean, const float* rstd, const void* dy,
+                   void* dx, float* dweight, float* dbias, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+    int st = check_norm(rows, dim, groups, dtype);
+    if (st != MAMBA_OK) return st;
+    if (dim == 0) return MAMBA_OK;
+    if (rows > 0 && (x == nullptr || mean == nullptr || rstd == nullptr || dy == nullptr || dx == nullptr))
+        return MAMBA_ERR_INVALID_ARG;
+    const void* const ptrs[] = {x, weight, mean, rstd, dy, dx, dweight, dbias, workspace};
+    st = check_aligned(ptrs);
+    if (st != MAMBA_OK) return st;
+    int cu = 1;
+    if (rows > 0) {
+        st = mamba::current_cu_count(&cu);
+        if (st != MAMBA_OK) return st;
+        const size_t need = mamba::layer_norm_bwd_workspace_bytes(rows, dim, groups, cu);
+        if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+    } else if (dweight == nullptr && dbias == nullptr) {
+        return MAMBA_OK;
+    }
+    mamba::NormArgs a = {};
+    a.rows = rows;
+    a.dim = dim;
+    a.groups = groups;
+    a.io = io_of(dtype);
+    a.x = x;
+    a.weight = weight;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.dy = dy;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    return mamba::launch_layer_norm_bwd(a, cu, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+}
+
+}  // extern "C"

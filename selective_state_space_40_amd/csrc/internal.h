@@ -161,6 +161,122 @@ struct SsdArgs {
 
 hipError_t launch_ssd_fwd(const SsdArgs& a, hipStream_t stream);
 
+// Linear attention with a decay for each head (linear_attn_kernel.h).
+constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
+constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;   // passes of the backward launch
+constexpr int kLinMaxDim = 256;   // widest head
+// Tokens of a chunk: fp32 takes half in the same LDS.
+constexpr int kLinChunkBF16 = 64, kLinChunkF32 = 32;
+// Tokens of a window of the decay's gradient: a state and an adjoint of dk x
+// dv values are kept per window (8% of the backward's traffic at 128 x 128).
+constexpr int kLinWindow = 1024;
+
+// One pass (q, k, v) -> out over the sequences; see the kernel's header.
+struct LinPass {
+    const void* q;          // (batch, seqlen, hq, dc)
+    const void* k;          // (batch, seqlen, hk, dc)
+    const void* v;          // (batch, seqlen, hv, dout)
+    const void* x;          // (batch, seqlen, hx, dout) or nullptr: for the decay's gradient
+    void* out;              // (batch, seqlen, ho, dout)
+    const float* s_in;      // state the walk starts from, or nullptr (zeros)
+    float* s_out;           // receives the state the walk ends with, or nullptr
+    float* marks;           // (batch, heads, nseg, nmark, dk, dv) or nullptr: receives the state
+                            // (adjoint) between a segment's windows of kLinWindow tokens
+    float* seg_in;          // (batch, heads, nseg, dk, dv): state entering each segment
+    int64_t sn, sp;         // strides of a state's rows (dc) and columns (dout)
+    int hq, hk, hv, hx, ho; // heads of each tensor, divisors of the number of heads
+    int dc, dout;
+    float out_scale;        // factor of q S
+    float state_scale;      // factor of the tokens' share of the state
+    int rev;                // walks from the last token to the first
+    int out32;              // out is fp32
+    int dg_pairs;           // adds the pairs of one chunk to the decay's gradient
+};
+
+struct LinArgs {
+    int64_t batch, seqlen, seg_len;
+    int heads, nseg, nblk, npass;
+    int nmark;                // windows less one of a segment
+    int exact;                // kLinState: the states serve the decay's gradient
+    const int32_t* lengths;   // (batch) or nullptr
+    const float* log_decay;   // (heads)
+    float scale;
+    double* dg;               // (heads, batch, nseg, 2, nblk) terms of the decay's gradient, or nullptr
+    const float* dhL;
+    const float* adj_in;      // the adjoints' seg_in
+    LinPass pass[3];
+};
+
+template <int IO, int MODE>
+hipError_t launch_linear_attn_variant(const LinArgs& a, int dc_pad, int block_cols, hipStream_t s);
+
+// A call of linear attention; the backward's outputs are set for its
+// launches only.
+struct LinearAttnCall {
+    int64_t batch, seqlen;
+    int heads, kv_heads, dk, dv, io;
+    float scale;
+    const void *q, *k, *v;
+    const float* log_decay;
+    const int32_t* lengths;
+    const float* h0;
+    void* o;
+    float* hL;
+    const void* d_o;
+    const float* dhL;
+    void *dq, *d_k, *d_v;
+    float *dlog_decay, *dh0;
+};
+
+// Division of a call over the GPU: segments of seg_len tokens (nseg == 1:
+// none) and output columns per workgroup.
+struct LinPlan {
+    int64_t seg_len = 0;
+    int nseg = 1;
+    int block_cols = 64;
+    size_t workspace_bytes = 0;
+};
+
+size_t linear_attn_workspace_bytes(const LinearAttnCall& c, const LinPlan& p, bool bwd);
+hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s);
+hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s);
+
+struct LinUpdateArgs {
+    int64_t batch;
+    int heads, kv_heads, dk, dv, io;
+    float scale;
+    float* h;
+    const void *q, *k, *v;
+    const float* log_decay;
+    void* o;
+};
+
+hipError_t launch_linear_attn_update(const LinUpdateArgs& a, hipStream_t s);
+
+// Layer norm over each of the `groups` equal parts of a row.
+struct NormArgs {
+    int64_t rows, dim, groups;
+    int io;
+    float eps;
+    const void* x;
+    const float* weight;
+    const float* bias;
+    void* y;
+    float* mean;         // (rows, groups), read by the backward pass
+    float* rstd;
+    const void* dy;
+    void* dx;
+    float* dweight;
+    float* dbias;
+};
+
+hipError_t launch_layer_norm_fwd(const NormArgs& a, hipStream_t s);
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups, int cu);
+hipError_t launch_layer_norm_bwd(const NormArgs& a, int cu, void* ws, hipStream_t s);
+
+// Compute units of the current device, cached per device; a mamba_status.
+int current_cu_count(int* cu);
+
 // Workspace layout for nchunks > 1: three fp32 arrays of
 // nchunks * batch * dim * dstate elements each: the state entering each
 // chunk, each chunk's end state from a zero start, and each chunk's decay

@@ -1,0 +1,422 @@
+// Layer norm over each of the `groups` equal parts of a row, and its
+// gradients:
+//     xh = (x - mean) rstd,  y = xh w + b
+//     dx = rstd (w dy - mean(w dy) - xh mean(w dy xh))
+//     dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Both are bound by memory: one read of x (and dy), one write of y (dx). A
+// part of n = dim / groups values is held by a team of 16, 64, 256 or 512
+// lanes, 8 to 32 values per lane in registers, so the mean, the centred sum
+// of squares and the output take one pass over memory; the variance is the
+// mean square of the centred values, not a difference of sums.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "internal.h"
+
+namespace mamba {
+namespace {
+
+// Sum over the lanes of a team; `slot` is LDS for one value per wave and
+// value, and the team spans whole waves when it is wider than one.
+template <int TEAM, int NV>
+__device__ __forceinline__ void team_sum(float (&v)[NV], float* slot) {
+    constexpr int LANES = TEAM < kWave ? TEAM : kWave;
+#pragma unroll
+    for (int m = 1; m < LANES; m *= 2)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] += __shfl_xor(v[i], m);
+    if constexpr (TEAM > kWave) {
+        constexpr int W = TEAM / kWave;
+        const int wave = threadIdx.x / kWave;
+        if (threadIdx.x % kWave == 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) slot[wave * NV + i] = v[i];
+        }
+        __syncthreads();
+        const float* t = slot + wave / W * W * NV;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float s = 0.0f;
+#pragma unroll
+            for (int u = 0; u < W; ++u) s += t[u * NV + i];
+            v[i] = s;
+        }
+    }
+}
+
+// A lane's CH x 8 values of a part of n. With VEC a lane holds runs of 8
+// consecutive values (the part is then a multiple of 8 values and starts on
+// 16 bytes); otherwise single values TEAM apart, for odd widths.
+template <int IO, int TEAM, int CH, bool VEC>
+struct Part {
+    static constexpr int kWords = VEC ? (IO == kIoF32 ? 2 : 1) : 0;
+    uint4 q[VEC ? CH * kWords : 1];
+    uint32_t r[VEC ? 1 : CH * 8];
+
+    static __device__ __forceinline__ int index(int lane, int u, int e) {
+        return VEC ? (lane + TEAM * u) * 8 + e : lane + TEAM * (8 * u + e);
+    }
+    __device__ __forceinline__ void load(const void* p, int64_t at, int n, int lane) {
+        if constexpr (VEC) {
+            const char* base = static_cast<const char*>(p) + at * (IO == kIoF32 ? 4 : 2);
+#pragma unroll
+            for (int u = 0; u < CH; ++u) {
+                const bool in = (lane + TEAM * u) * 8 < n;
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                    q[u * kWords + k] = in ? reinterpret_cast<const uint4*>(base)[(lane + TEAM * u) * kWords + k]
+                                           : make_uint4(0, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < CH; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = index(lane, u, e);
+                    r[u * 8 + e] = i < n ? load_raw<IO>(p, at + i) : 0u;
+                }
+        }
+    }
+    __device__ __forceinline__ float get(int u, int e) const {
+        if constexpr (VEC && IO == kIoF32) {
+            const uint4& t = q[u * 2 + e / 4];
+            return __uint_as_float(e % 4 == 0 ? t.x : e % 4 == 1 ? t.y : e % 4 == 2 ? t.z : t.w);
+        } else if constexpr (VEC) {
+            const uint4& t = q[u];
+            const uint32_t x = e / 2 == 0 ? t.x : e / 2 == 1 ? t.y : e / 2 == 2 ? t.z : t.w;
+            return __uint_as_float(e % 2 ? x & 0xffff0000u : x << 16);
+        } else {
+            return raw_to_f32<IO>(r[u * 8 + e]);
+        }
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t at, int n, int lane,
+                                                 const float (&v)[CH * 8]) {
+        if constexpr (VEC) {
+            char* base = static_cast<char*>(p) + at * (IO == kIoF32 ? 4 : 2);
+#pragma unroll
+            for (int u = 0; u < CH; ++u) {
+                if ((lane + TEAM * u) * 8 >= n) continue;
+                const float* s = v + 8 * u;
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (IO == kIoF32) {
+                        o[e] = __float_as_uint(s[e]);
+                    } else {
+                        const uint32_t h = __builtin_bit_cast(uint16_t, static_cast<__bf16>(s[e]));
+                        if (e % 2) o[e / 2] |= h << 16;
+                        else o[e / 2] = h;
+                    }
+                }
+                uint4* d = reinterpret_cast<uint4*>(base) + (lane + TEAM * u) * kWords;
+                d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                if constexpr (IO == kIoF32) d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < CH; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = index(lane, u, e);
+                    if (i < n) store_io<IO>(p, at + i, v[u * 8 + e]);
+                }
+        }
+    }
+};
+
+// The parameters of a lane's values.
+template <int TEAM, int CH, bool VEC>
+__device__ __forceinline__ void load_params(const float* p, int64_t at, int n, int lane, float none,
+                                            float (&v)[CH * 8]) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < CH * 8; ++i) v[i] = none;
+        return;
+    }
+    Part<kIoF32, TEAM, CH, VEC> t;
+    t.load(p, at, n, lane);
+#pragma unroll
+    for (int u = 0; u < CH; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u * 8 + e] = t.get(u, e);
+}
+
+template <int IO, int TEAM, int CH, bool VEC>
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_fwd_kernel(NormArgs a) {
+    constexpr int THREADS = TEAM > 256 ? TEAM : 256;
+    constexpr int TEAMS = THREADS / TEAM;
+    __shared__ float slots[2][THREADS / kWave];
+    const int lane = threadIdx.x % TEAM;
+    const int n = static_cast<int>(a.dim / a.groups);
+    const int64_t parts = a.rows * a.groups;
+    const int64_t part = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
+    const bool in = part < parts;
+    const int64_t at = in ? part * n : 0;
+    const int m = in ? n : 0;
+    Part<IO, TEAM, CH, VEC> x;
+    x.load(a.x, at, m, lane);
+    float v[CH * 8];
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int u = 0; u < CH; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[u * 8 + e] = x.get(u, e);
+            sum[0] += v[u * 8 + e];
+        }
+    team_sum<TEAM>(sum, slots[0]);
+    const float mean = sum[0] / static_cast<float>(n);
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int u = 0; u < CH; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool have = Part<IO, TEAM, CH, VEC>::index(lane, u, e) < n;
+            float& t = v[u * 8 + e];
+            t = have ? t - mean : 0.0f;
+            sq[0] = fmaf(t, t, sq[0]);
+        }
+    team_sum<TEAM>(sq, slots[1]);
+    const float rstd = 1.0f / sqrtf(sq[0] / static_cast<float>(n) + a.eps);
+    const int64_t col = part % a.groups * n;
+    float wt[CH * 8], bs[CH * 8];
+    load_params<TEAM, CH, VEC>(a.weight, col, m, lane, 1.0f, wt);
+    load_params<TEAM, CH, VEC>(a.bias, col, m, lane, 0.0f, bs);
+#pragma unroll
+    for (int i = 0; i < CH * 8; ++i) v[i] = fmaf(v[i] * rstd, wt[i], bs[i]);
+    Part<IO, TEAM, CH, VEC>::store(a.y, at, m, lane, v);
+    if (in && lane == 0) {
+        if (a.mean != nullptr) a.mean[part] = mean;
+        if (a.rstd != nullptr) a.rstd[part] = rstd;
+    }
+}
+
+// The backward pass. A workgroup stays with one group of columns and walks
+// rows blockrow, blockrow + slots, ...: its lanes keep their columns' sums of
+// dw and db in registers, its teams' sums meet in LDS at the end, and one
+// (slot, column) pair per workgroup goes to `partial` (2, slots, dim), from
+// which layer_norm_columns_kernel adds the slots in order.
+constexpr int kNormBwdThreads = 512;
+
+template <int IO, int TEAM, int CH, bool VEC>
+__global__ __launch_bounds__(kNormBwdThreads) void layer_norm_bwd_kernel(NormArgs a, int slots,
+                                                                         float* partial) {
+    __shared__ float red[2][2 * kNormBwdThreads / kWave];
+    __shared__ float cols[TEAM > 256 ? 1 : CH * 8 * kNormBwdThreads];
+    typedef Part<IO, TEAM, CH, VEC> P;
+    const int lane = threadIdx.x % TEAM;
+    const int team = threadIdx.x / TEAM, teams = blockDim.x / TEAM;
+    const int n = static_cast<int>(a.dim / a.groups);
+    const int64_t grp = blockIdx.x % a.groups;
+    const int64_t slot = blockIdx.x / a.groups;
+    const float inv = 1.0f / static_cast<float>(n);
+    float wt[CH * 8], dw[CH * 8], db[CH * 8];
+    load_params<TEAM, CH, VEC>(a.weight, grp * n, n, lane, 1.0f, wt);
+#pragma unroll
+    for (int i = 0; i < CH * 8; ++i) dw[i] = db[i] = 0.0f;
+    const int64_t step = static_cast<int64_t>(slots) * teams;
+    P x, dy;
+    float mean = 0.0f, rstd = 0.0f;
+    auto fetch = [&](int64_t row) {
+        const bool in = row < a.rows;
+        const int64_t part = in ? row * a.groups + grp : 0;
+        x.load(a.x, part * n, in ? n : 0, lane);
+        dy.load(a.dy, part * n, in ? n : 0, lane);
+        mean = in ? a.mean[part] : 0.0f;
+        rstd = in ? a.rstd[part] : 0.0f;
+    };
+    int odd = 0;
+    fetch(slot * teams + team);
+    // every team of the workgroup takes the same number of turns
+    for (int64_t r0 = slot * teams; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + team;
+        float xh[CH * 8], wdy[CH * 8];
+        float s[2] = {0.0f, 0.0f};
+        const float mu = mean, rs = rstd;
+#pragma unroll
+        for (int u = 0; u < CH; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = u * 8 + e;
+                const bool have = P::index(lane, u, e) < n;
+                xh[i] = have ? (x.get(u, e) - mu) * rs : 0.0f;
+                const float d = dy.get(u, e);
+                dw[i] = fmaf(d, xh[i], dw[i]);
+                db[i] += d;
+                wdy[i] = d * wt[i];
+                s[0] += wdy[i];
+                s[1] = fmaf(wdy[i], xh[i], s[1]);
+            }
+        fetch(row + step);
+        team_sum<TEAM>(s, red[odd]);
+        odd ^= 1;   // the other buffer: a wave may still read this one
+        const float c1 = s[0] * inv, c2 = s[1] * inv;
+#pragma unroll
+        for (int i = 0; i < CH * 8; ++i) wdy[i] = rs * (wdy[i] - c1 - xh[i] * c2);
+        P::store(a.dx, (row < a.rows ? row * a.groups + grp : 0) * n, row < a.rows ? n : 0, lane, wdy);
+    }
+    if (a.dweight == nullptr && a.dbias == nullptr) return;
+    float* pw = partial + slot * a.dim + grp * n;
+    float* pb = pw + static_cast<int64_t>(slots) * a.dim;
+    if (slots == 1) {
+        pw = a.dweight + grp * n;
+        pb = a.dbias + grp * n;
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float (&d)[CH * 8] = which ? db : dw;
+        const bool wanted = (which ? a.dbias : a.dweight) != nullptr;
+        float* out = which ? pb : pw;
+        if constexpr (TEAM <= 256) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < CH * 8; ++i) cols[(team * CH * 8 + i) * TEAM + lane] = d[i];
+            __syncthreads();
+            for (int j = threadIdx.x; j < TEAM * CH * 8; j += blockDim.x) {
+                float t = 0.0f;
+                for (int k = 0; k < teams; ++k) t += cols[k * CH * 8 * TEAM + j];
+                const int i = P::index(j % TEAM, j / TEAM / 8, j / TEAM % 8);
+                if (wanted && i < n) out[i] = t;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < CH; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = P::index(lane, u, e);
+                    if (wanted && i < n) out[i] = d[u * 8 + e];
+                }
+        }
+    }
+}
+
+// Column sums over the slots: 64 columns per workgroup, its 4 waves a quarter
+// of the slots each.
+__global__ __launch_bounds__(256) void layer_norm_columns_kernel(int64_t dim, int slots,
+                                                                 const float* partial, float* dweight,
+                                                                 float* dbias) {
+    __shared__ float red[4][kWave];
+    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * kWave + lane;
+    float* out = blockIdx.y ? dbias : dweight;
+    if (out == nullptr) return;
+    const float* p = partial + static_cast<int64_t>(blockIdx.y) * slots * dim;
+    float s = 0.0f;
+    if (col < dim)
+        for (int k = w; k < slots; k += 4) s += p[static_cast<int64_t>(k) * dim + col];
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && col < dim) out[col] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+__global__ __launch_bounds__(256) void layer_norm_zero_kernel(int64_t dim, float* dweight, float* dbias) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= dim) return;
+    if (dweight != nullptr) dweight[i] = 0.0f;
+    if (dbias != nullptr) dbias[i] = 0.0f;
+}
+
+// Lanes and 8-value runs per lane for parts of n values.
+struct Team {
+    int lanes, runs;
+};
+
+Team team_for(int64_t n) {
+    const int lanes = n <= 384 ? 16 : (n <= 1536 ? 64 : (n <= 6144 ? 256 : 512));
+    return {lanes, static_cast<int>((n + 8 * lanes - 1) / (8 * lanes))};
+}
+
+// Threads per workgroup of the backward pass and slots (workgroups per group
+// of columns): about one workgroup of 512 per compute unit when there are
+// rows enough, smaller workgroups when there are not.
+struct BwdGrid {
+    int threads, slots;
+};
+
+BwdGrid bwd_grid(int64_t rows, int64_t groups, int lanes, int cu) {
+    int threads = kNormBwdThreads;
+    while (threads > 256 && threads > lanes && rows * groups * lanes / threads < cu) threads /= 2;
+    if (threads < lanes) threads = lanes;
+    const int64_t teams = threads / lanes;
+    const int64_t most = (rows + teams - 1) / teams;
+    const int64_t per_cu = kNormBwdThreads / threads;
+    int64_t slots = (per_cu * cu + groups - 1) / groups;
+    if (slots > most) slots = most;
+    return {threads, static_cast<int>(slots < 1 ? 1 : slots)};
+}
+
+template <int IO, int TEAM, int CH, bool VEC>
+hipError_t launch_norm(const NormArgs& a, bool bwd, int threads, int slots, float* partial, hipStream_t s) {
+    if (!bwd) {
+        constexpr int TEAMS = (TEAM > 256 ? TEAM : 256) / TEAM;
+        const int64_t blocks = (a.rows * a.groups + TEAMS - 1) / TEAMS;
+        hipLaunchKernelGGL((layer_norm_fwd_kernel<IO, TEAM, CH, VEC>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(TEAM > 256 ? TEAM : 256), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((layer_norm_bwd_kernel<IO, TEAM, CH, VEC>),
+                           dim3(static_cast<unsigned>(slots * a.groups)), dim3(threads), 0, s, a, slots, partial);
+    }
+    return hipGetLastError();
+}
+
+template <int IO, bool VEC>
+hipError_t launch_norm_team(const NormArgs& a, Team t, bool bwd, int threads, int slots, float* partial,
+                            hipStream_t s) {
+    switch (t.lanes * 8 + t.runs) {
+        case 16 * 8 + 1: return launch_norm<IO, 16, 1, VEC>(a, bwd, threads, slots, partial, s);
+        case 16 * 8 + 2: return launch_norm<IO, 16, 2, VEC>(a, bwd, threads, slots, partial, s);
+        case 16 * 8 + 3: return launch_norm<IO, 16, 3, VEC>(a, bwd, threads, slots, partial, s);
+        case 64 * 8 + 1: return launch_norm<IO, 64, 1, VEC>(a, bwd, threads, slots, partial, s);
+        case 64 * 8 + 2: return launch_norm<IO, 64, 2, VEC>(a, bwd, threads, slots, partial, s);
+        case 64 * 8 + 3: return launch_norm<IO, 64, 3, VEC>(a, bwd, threads, slots, partial, s);
+        case 256 * 8 + 1: return launch_norm<IO, 256, 1, VEC>(a, bwd, threads, slots, partial, s);
+        case 256 * 8 + 2: return launch_norm<IO, 256, 2, VEC>(a, bwd, threads, slots, partial, s);
+        case 256 * 8 + 3: return launch_norm<IO, 256, 3, VEC>(a, bwd, threads, slots, partial, s);
+        case 512 * 8 + 2: return launch_norm<IO, 512, 2, VEC>(a, bwd, threads, slots, partial, s);
+        case 512 * 8 + 3: return launch_norm<IO, 512, 3, VEC>(a, bwd, threads, slots, partial, s);
+        case 512 * 8 + 4: return launch_norm<IO, 512, 4, VEC>(a, bwd, threads, slots, partial, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_norm_any(const NormArgs& a, bool bwd, int threads, int slots, float* partial, hipStream_t s) {
+    const int64_t n = a.dim / a.groups;
+    const Team t = team_for(n);
+    const bool vec = n % 8 == 0;
+    if (a.io == kIoF32)
+        return vec ? launch_norm_team<kIoF32, true>(a, t, bwd, threads, slots, partial, s)
+                   : launch_norm_team<kIoF32, false>(a, t, bwd, threads, slots, partial, s);
+    return vec ? launch_norm_team<kIoBF16, true>(a, t, bwd, threads, slots, partial, s)
+               : launch_norm_team<kIoBF16, false>(a, t, bwd, threads, slots, partial, s);
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm_fwd(const NormArgs& a, hipStream_t s) {
+    return launch_norm_any(a, false, 0, 0, nullptr, s);
+}
+
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups, int cu) {
+    if (rows == 0 || dim == 0) return 0;
+    const BwdGrid g = bwd_grid(rows, groups, team_for(dim / groups).lanes, cu);
+    return g.slots > 1 ? static_cast<size_t>(g.slots) * dim * 2 * sizeof(float) : 0;
+}
+
+hipError_t launch_layer_norm_bwd(const NormArgs& a, int cu, void* ws, hipStream_t s) {
+    if (a.rows == 0) {
+        hipLaunchKernelGGL(layer_norm_zero_kernel, dim3(static_cast<unsigned>((a.dim + 255) / 256)), dim3(256),
+                           0, s, a.dim, a.dweight, a.dbias);
+        return hipGetLastError();
+    }
+    const BwdGrid g = bwd_grid(a.rows, a.groups, team_for(a.dim / a.groups).lanes, cu);
+    float* partial = static_cast<float*>(ws);
+    const hipError_t e = launch_norm_any(a, true, g.threads, g.slots, partial, s);
+    if (e != hipSuccess || g.slots == 1 || (a.dweight == nullptr && a.dbias == nullptr)) return e;
+    hipLaunchKernelGGL(layer_norm_columns_kernel, dim3(static_cast<unsigned>((a.dim + kWave - 1) / kWave), 2),
+                       dim3(256), 0, s, a.dim, g.slots, partial, a.dweight, a.dbias);
+    return hipGetLastError();
+}
+
+}  // namespace mamba

@@ -1,0 +1,699 @@
+// Linear attention with a decay for each head, chunk by chunk on the matrix
+// cores. One kernel serves the forward pass and the three products of the
+// backward pass: each is a pass (q, k, v) -> out over a sequence,
+//     out_i = sum_{j <= i} lam^(i-j) (q_i . k_j) v_j  +  decayed state,
+// with an fp32 state S (sum of k_j^T v_j, decayed) carried from chunk to
+// chunk. For a chunk of C tokens entered with state S, local tokens i, j:
+//     P[i,j]  = scale lam^(i-j) (q_i . k_j)  for j <= i, else 0     (C x C)
+//     out_i   = sum_j P[i,j] v_j + out_scale lam^(i+1-r) q_i S
+//     S      <- lam^cnt S + sum_j state_scale lam^(cnt-1-j+r) k_j^T v_j
+// r is 0 for the forward direction. The backward products of k and v run
+// through time from the end (token order reversed as rows are loaded) and
+// carry the adjoint of the state, which token i reads before its own decay
+// and not after it: r is 1 there.
+//     forward    (q, k, v) -> o,   state S
+//     gradients  (do, v, k) -> dq, state S^T
+//                (k, q, do) -> dv, adjoint dS, reversed
+//                (v, do, q) -> dk, adjoint dS^T, reversed
+//
+// Work mapping. A workgroup of 4 waves walks the chunks of one (row, head,
+// segment) for a block of 4 PW output columns; wave w owns PW of them. The
+// state's columns belong to the same wave, so its S (all DC rows, PW columns)
+// stays in the accumulators for the whole walk, and the accumulator of two
+// 16 x 16 blocks is, up to a fixed order of the rows, the operand of the
+// product q S: the state passes through neither LDS nor another wave. The
+// chunk's q, k and v rows are staged in LDS; the next chunk's are loaded into
+// registers meanwhile. The C x C matrix P is split over the waves by 16 x 16
+// blocks (only those on and below the diagonal) and exchanged through LDS.
+//
+// bf16 operands. q, k and v enter the products exactly. P is rounded to bf16
+// (its effect on a bf16 output is that of the output's own rounding). What
+// reaches fp32 results goes in as a sum of bf16 terms, each the rounding of
+// what the ones before leave: two for the state (2^-16 of a term at most),
+// three where the gradient of the decay is formed, since it weighs rounding
+// errors with a token's place in its segment. The product q S that only an
+// output sees needs one. fp32 I/O uses the fp32 matrix instruction and no
+// rounding.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "internal.h"
+
+namespace mamba {
+namespace {
+
+typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8;
+typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kLinThreads = 256;
+constexpr int kLinWaves = kLinThreads / kWave;
+
+struct F32x8 {
+    float v[8];
+};
+
+// A fragment holds, in lane (c, g) = (lane % 16, lane / 16), 8 of the 32
+// values that one row or column c of an operand contributes to a product:
+// nat() the values 8 g + e, perm() 4 g + e and 16 + 4 g + (e - 4), the order
+// in which two accumulator blocks hold them. Both operands of a product use
+// the same order. The fp32 instruction contracts 4 values at a time, value e
+// of the four lane groups in step e.
+template <int IO>
+struct LinOps;
+
+template <>
+struct LinOps<kIoBF16> {
+    typedef __bf16 T;
+    typedef bf16x8 Frag;
+    static constexpr bool kSplit = true;    // fp32 values enter as bf16 terms
+    static constexpr int kChunk = kLinChunkBF16;
+    static constexpr int kPad = 8;          // LDS row padding (elements)
+
+    static __device__ __forceinline__ Frag nat(const T* row, int g) {
+        return *reinterpret_cast<const bf16x8*>(row + 8 * g);
+    }
+    static __device__ __forceinline__ Frag perm(const T* row, int g) {
+        const bf16x4 a = *reinterpret_cast<const bf16x4*>(row + 4 * g);
+        const bf16x4 b = *reinterpret_cast<const bf16x4*>(row + 16 + 4 * g);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // 8 rows r0 + 8 g + e of column c0 + c of a row-major tile: the LDS
+    // transpose read (ds_read_b64_tr_b16). Within each group of 16 lanes,
+    // lane r receives as element e the element (r mod 4) of the 8 bytes that
+    // lane 4 e + r / 4 of its group addresses, so lane s of the group
+    // addresses row s / 4, columns 4 (s mod 4) .. + 3 of a 4 x 16 block.
+    template <int RS>
+    static __device__ __forceinline__ Frag tr(const T* tile, int r0, int c0, int c, int g) {
+        const T* p = tile + (r0 + 8 * g + (c >> 2)) * RS + c0 + 4 * (c & 3);
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(const_cast<T*>(p)));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(const_cast<T*>(p + 4 * RS)));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 acc) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float get(const Frag& f, int e) {
+        return static_cast<float>(f[e]);
+    }
+    // The next term of fp32 values: x rounded, and x becomes what is left.
+    static __device__ __forceinline__ Frag term(float (&x)[8]) {
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = static_cast<__bf16>(x[e]);
+            x[e] -= static_cast<float>(f[e]);
+        }
+        return f;
+    }
+    // four consecutive elements as fp32
+    static __device__ __forceinline__ f32x4 ld4(const T* p) {
+        const bf16x4 a = *reinterpret_cast<const bf16x4*>(p);
+        return f32x4{static_cast<float>(a[0]), static_cast<float>(a[1]), static_cast<float>(a[2]),
+                     static_cast<float>(a[3])};
+    }
+    static __device__ __forceinline__ void st4(T* p, f32x4 v) {
+        bf16x4 a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = static_cast<__bf16>(v[e]);
+        *reinterpret_cast<bf16x4*>(p) = a;
+    }
+};
+
+template <>
+struct LinOps<kIoF32> {
+    typedef float T;
+    typedef F32x8 Frag;
+    static constexpr bool kSplit = false;
+    static constexpr int kChunk = kLinChunkF32;
+    static constexpr int kPad = 4;
+
+    static __device__ __forceinline__ Frag pair(const float* a, const float* b) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(a), y = *reinterpret_cast<const f32x4*>(b);
+        return F32x8{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
+    }
+    static __device__ __forceinline__ Frag nat(const T* row, int g) {
+        return pair(row + 8 * g, row + 8 * g + 4);
+    }
+    static __device__ __forceinline__ Frag perm(const T* row, int g) {
+        return pair(row + 4 * g, row + 16 + 4 * g);
+    }
+    template <int RS>
+    static __device__ __forceinline__ Frag tr(const T* tile, int r0, int c0, int c, int g) {
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e] = tile[(r0 + 8 * g + e) * RS + c0 + c];
+        return f;
+    }
+    static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 acc) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], acc, 0, 0, 0);
+        return acc;
+    }
+    static __device__ __forceinline__ float get(const Frag& f, int e) { return f.v[e]; }
+    static __device__ __forceinline__ Frag term(float (&x)[8]) {
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e] = x[e];
+        return f;
+    }
+    static __device__ __forceinline__ f32x4 ld4(const T* p) {
+        return *reinterpret_cast<const f32x4*>(p);
+    }
+    static __device__ __forceinline__ void st4(T* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+};
+
+// Buffer resource over `bytes` bytes from p (raw addressing, gfx9 word 3):
+// loads at or past the end return zeros and stores there are dropped, so
+// neither ragged chunks nor narrow heads need a branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_rsrc(const void* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+// An offset past the end of every resource.
+constexpr int kPastEnd = static_cast<int>(0x80000000u);
+
+// The rows of one head's chunk in a (batch, seqlen, heads, dim) tensor.
+template <typename T>
+struct HeadRows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    int stride;   // bytes from token to token
+
+    __device__ __forceinline__ HeadRows(const void* p, int64_t row0, int heads, int head, int dim,
+                                        int cnt)
+        : rsrc(lin_rsrc(static_cast<const T*>(p) + (row0 * heads + head) * dim,
+                        cnt > 0 ? ((cnt - 1) * heads * dim + dim) * static_cast<int>(sizeof(T)) : 0)),
+          stride(heads * dim * static_cast<int>(sizeof(T))) {}
+};
+
+// One tile's share of a thread: COUNT vectors of 16 bytes. Vector e covers
+// row e / VPR and the 16-byte column e % VPR of the padded width.
+template <int IO, int COLS>
+struct Tile {
+    typedef typename LinOps<IO>::T T;
+    static constexpr int kC = LinOps<IO>::kChunk;
+    static constexpr int kRow = COLS + LinOps<IO>::kPad;   // LDS row pitch
+    static constexpr int kVec = 16 / sizeof(T);
+    static constexpr int VPR = COLS / kVec;
+    static constexpr int COUNT = kC * VPR / kLinThreads;
+    static_assert(kC * VPR % kLinThreads == 0, "whole vectors per thread");
+
+    uint4 r[COUNT];
+
+    // Columns col0 .. col0 + COLS of the chunk's rows, of which `dim` exist;
+    // `rev` turns the token order round.
+    __device__ __forceinline__ void load(const HeadRows<T>& h, int col0, int dim, int cnt, bool rev) {
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) {
+            const int e = threadIdx.x + u * kLinThreads;
+            const int i = e / VPR, col = col0 + (e % VPR) * kVec;
+            const int row = rev ? cnt - 1 - i : i;
+            const int off = (i < cnt && col < dim) ? row * h.stride + col * static_cast<int>(sizeof(T))
+                                                   : kPastEnd;
+            r[u] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(h.rsrc, off, 0, 0));
+        }
+    }
+    __device__ __forceinline__ void stage(T* lds) const {
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) {
+            const int e = threadIdx.x + u * kLinThreads;
+            *reinterpret_cast<uint4*>(lds + (e / VPR) * kRow + (e % VPR) * kVec) = r[u];
+        }
+    }
+};
+
+template <int IO, int DC, int PW, int MODE>
+struct LinLds {
+    typedef typename LinOps<IO>::T T;
+    static constexpr int kC = LinOps<IO>::kChunk;
+    static constexpr int kRowP = kC + LinOps<IO>::kPad;
+    alignas(16) T K[kC * Tile<IO, DC>::kRow];
+    alignas(16) T V[kC * Tile<IO, kLinWaves * PW>::kRow];
+    alignas(16) T Q[MODE == kLinState ? 8 : kC * Tile<IO, DC>::kRow];
+    alignas(16) T X[MODE == kLinBwd ? kC * Tile<IO, kLinWaves * PW>::kRow : 8];
+    alignas(16) T P[MODE == kLinState ? 8 : kC * kRowP];
+    alignas(16) float W[kC];      // weight of token j in the state update
+    float pow[kC + 1];            // lam^n
+    double red[kLinWaves];
+};
+
+// The gradient of the log decay is the sum over pairs (t, j) of steps t - j
+// times the pair's term lam^(t-j) scale (q_t . k_j) (do_t . v_j), the entering
+// state counting as a token before the first and the gradient of the final
+// state as one at the last. Pairs of one chunk are added as they are. For the
+// others, with x_t = q_t . (dq_t through the state) and z_j = k_j . (dk_j
+// through the adjoint), both cut at the same chunks, and places counted in a
+// window of W tokens (that starts afresh in every segment),
+//     sum_t (t + 1) x_t - sum_j (j + 1) z_j + W <adjoint, state at its end>
+// gives every pair its steps. The three cancel down to a memory's length from
+// a window's, so their rounding (fp32 throughout) is amplified by W over that
+// length: W is kLinWindow, and a head that forgets within a chunk (lam^C below
+// e^-25) counts inside chunks instead, t + 1 from a chunk's start and C - 1 - j
+// to its end; what crosses a whole chunk is nothing there.
+__device__ __forceinline__ bool decay_is_strong(float g, int chunk) {
+    return g * static_cast<float>(chunk) <= -25.0f;
+}
+
+// lam^n = exp(g n), the product's rounding error put back.
+__device__ __forceinline__ float decay_power(float g, int n) {
+    if (n == 0) return 1.0f;   // also for g = -inf, a head that forgets at once
+    const float p = g * static_cast<float>(n);
+    const float e = fmaf(g, static_cast<float>(n), -p);
+    const float x = expf(p);
+    return (x > 0.0f && x < __builtin_inff()) ? fmaf(x, e, x) : x;
+}
+
+template <int IO, int DC, int PW, int MODE>
+__global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) {
+    typedef LinOps<IO> O;
+    typedef typename O::T T;
+    typedef typename O::Frag Frag;
+    constexpr int C = O::kChunk;
+    constexpr int NT = C / 16;            // blocks of 16 tokens
+    constexpr int NS = C / 32;            // product steps over tokens
+    constexpr int NN = DC / 16;           // blocks of 16 state rows
+    constexpr int NP = PW / 16;           // blocks of 16 columns per wave
+    constexpr int DOB = kLinWaves * PW;   // columns per workgroup
+    constexpr int RD = Tile<IO, DC>::kRow, RO = Tile<IO, DOB>::kRow;
+    constexpr bool kState = MODE == kLinState, kBwd = MODE == kLinBwd;
+    typedef LinLds<IO, DC, PW, MODE> Lds;
+    __shared__ Lds lds;
+
+    const int tid = threadIdx.x;
+    const int lane = tid & (kWave - 1);
+    const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int c = lane & 15, g = lane >> 4;
+
+    // which (row, head, segment, pass, column block); neighbours in this
+    // order read the same rows and share an XCD's L2
+    int64_t id = xcd_contiguous_block(blockIdx.x, gridDim.x);
+    const int blk = static_cast<int>(id % a.nblk);
+    id /= a.nblk;
+    const int ip = static_cast<int>(id % a.npass);
+    id /= a.npass;
+    const int nsegs = kState ? a.nseg - 1 : a.nseg;
+    int seg = static_cast<int>(id % nsegs);
+    id /= nsegs;
+    const int hd = static_cast<int>(id % a.heads);
+    const int64_t b = id / a.heads;
+    const LinPass& ps = a.pass[ip];
+    const bool rev = ps.rev != 0;
+    const bool exact = kState ? a.exact != 0 : ps.x != nullptr;   // three terms, for the decay's gradient
+    if (kState && rev) seg += 1;   // the reversed walk's last segment is the first
+    const int p0 = blk * DOB;
+    const int dc = ps.dc, dout = ps.dout;
+    // this workgroup's term of the decay's gradient
+    double* dg_out = nullptr;
+    if constexpr (kBwd) {
+        if (a.dg != nullptr && ip != kLinPassDv)
+            dg_out = a.dg + (((static_cast<int64_t>(hd) * a.batch + b) * a.nseg + seg) * 2 +
+                             (ip == kLinPassDq ? 0 : 1)) * a.nblk + blk;
+    }
+    if (p0 >= dout) {   // fewer blocks than another pass of the launch
+        if (kBwd && dg_out != nullptr && tid == 0) *dg_out = 0.0;
+        return;
+    }
+
+    const int64_t L = a.seqlen;
+    int64_t len = L;
+    if (a.lengths != nullptr) {
+        const int64_t n = a.lengths[b];
+        len = n < 0 ? 0 : (n < L ? n : L);
+    }
+    const int64_t seg0 = static_cast<int64_t>(seg) * a.seg_len;
+    const int64_t seg1 = seg == a.nseg - 1 ? L : seg0 + a.seg_len;
+    const int64_t end = len < seg1 ? len : seg1;         // valid tokens: seg0 .. end
+    const int64_t ntok = end > seg0 ? end - seg0 : 0;
+
+    const float g1 = a.log_decay[hd];
+    const bool strong = decay_is_strong(g1, C);
+    if (tid <= C) lds.pow[tid] = decay_power(g1, tid);
+    // P's blocks above the diagonal are read beside those on it and never
+    // written again
+    if constexpr (!kState)
+        for (int e = tid; e < C * Lds::kRowP; e += kLinThreads) lds.P[e] = static_cast<T>(0.0f);
+    __syncthreads();
+    const int r = rev ? 1 : 0;
+
+    // S: block (nt, pt) holds rows n = 16 nt + 4 g + v of column p0 + PW w + 16 pt + c
+    const int pc = p0 + PW * w + c;
+    const int64_t state_elems = static_cast<int64_t>(dc) * dout;
+    const int64_t bh = b * a.heads + hd;
+    const float* sin = ps.s_in != nullptr ? ps.s_in + bh * state_elems : nullptr;
+    if (a.nseg > 1) sin = ps.seg_in + (bh * a.nseg + seg) * state_elems;
+    if (kState) sin = nullptr;
+    f32x4 S[NN][NP];
+#pragma unroll
+    for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+        for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int n = 16 * nt + 4 * g + v, p = pc + 16 * pt;
+                S[nt][pt][v] = (sin != nullptr && n < dc && p < dout)
+                                   ? sin[static_cast<int64_t>(n) * ps.sn + static_cast<int64_t>(p) * ps.sp]
+                                   : 0.0f;
+            }
+
+    // factors of P for the blocks d = it - jt below the diagonal, and of q S
+    // for token 16 it + c: the same for every chunk
+    float fac[NT][4], eo[NT];
+    if constexpr (!kState) {
+#pragma unroll
+        for (int d = 0; d < NT; ++d)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int n = 16 * d + c - 4 * g - v;
+                fac[d][v] = n >= 0 ? a.scale * lds.pow[n] : 0.0f;
+            }
+#pragma unroll
+        for (int it = 0; it < NT; ++it) eo[it] = ps.out_scale * lds.pow[16 * it + c + 1 - r];
+    }
+
+    const int hq = hd / (a.heads / ps.hq), hk = hd / (a.heads / ps.hk);
+    const int hv = hd / (a.heads / ps.hv), hx = kBwd ? hd / (a.heads / ps.hx) : 0;
+    const int64_t nchunks = (ntok + C - 1) / C;
+    // chunk ch of the walk: its first token and count (0 past the end). Both
+    // directions cut at the same tokens, as the decay's gradient adds what one
+    // direction forms inside a chunk to what both form across chunks.
+    auto chunk_at = [&](int64_t ch, int64_t& t0, int& cnt) {
+        const int64_t first = (rev ? nchunks - 1 - ch : ch) * C;
+        const int64_t left = ch < nchunks ? ntok - first : 0;
+        cnt = left >= C ? C : static_cast<int>(left);
+        t0 = seg0 + first;
+    };
+    Tile<IO, DC> tq, tk;
+    Tile<IO, DOB> tv, tx;
+    auto fetch = [&](int64_t ch) {
+        int64_t t0;
+        int cnt;
+        chunk_at(ch, t0, cnt);
+        const int64_t row0 = b * L + t0;
+        tk.load(HeadRows<T>(ps.k, row0, ps.hk, hk, dc, cnt), 0, dc, cnt, rev);
+        tv.load(HeadRows<T>(ps.v, row0, ps.hv, hv, dout, cnt), p0, dout, cnt, rev);
+        if constexpr (!kState) tq.load(HeadRows<T>(ps.q, row0, ps.hq, hq, dc, cnt), 0, dc, cnt, rev);
+        if constexpr (kBwd)
+            tx.load(HeadRows<T>(ps.x, row0, ps.hx, hx, dout, ps.x != nullptr ? cnt : 0), p0, dout, cnt, rev);
+    };
+    const float em_full = g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(C));
+    double dg = 0.0;
+    // the adjoint at the segment's end against S, this thread's part
+    auto adjoint_dot = [&]() -> double {
+        const float* adj = a.nseg > 1 ? a.adj_in + (bh * a.nseg + seg) * state_elems
+                                      : (a.dhL != nullptr ? a.dhL + bh * state_elems : nullptr);
+        if (adj == nullptr) return 0.0;
+        float sum = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * nt + 4 * g + v, p = pc + 16 * pt;
+                    if (n < dc && p < dout)
+                        sum = fmaf(S[nt][pt][v],
+                                   adj[static_cast<int64_t>(n) * ps.sn + static_cast<int64_t>(p) * ps.sp], sum);
+                }
+        return static_cast<double>(sum);
+    };
+    auto store_state = [&](float* to) {
+#pragma unroll
+        for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * nt + 4 * g + v, p = pc + 16 * pt;
+                    if (n < dc && p < dout)
+                        to[static_cast<int64_t>(n) * ps.sn + static_cast<int64_t>(p) * ps.sp] = S[nt][pt][v];
+                }
+    };
+
+    fetch(0);
+    for (int64_t ch = 0; ch < nchunks; ++ch) {
+        int64_t t0;
+        int cnt;
+        chunk_at(ch, t0, cnt);
+        tk.stage(lds.K);
+        tv.stage(lds.V);
+        if constexpr (!kState) tq.stage(lds.Q);
+        if constexpr (kBwd) tx.stage(lds.X);
+        if (tid < C) lds.W[tid] = tid < cnt ? ps.state_scale * lds.pow[cnt - 1 - tid + r] : 0.0f;
+        __syncthreads();
+        fetch(ch + 1);
+
+        f32x4 Y[NP][NT];
+        if constexpr (!kState) {
+            // P, block by block of the lower triangle
+            constexpr int NB = NT * (NT + 1) / 2;
+            float dgi = 0.0f;
+#pragma unroll
+            for (int u = 0; u < (NB + kLinWaves - 1) / kLinWaves; ++u) {
+                const int bi = u * kLinWaves + w;
+                if (bi < NB) {
+                    int it = 0;
+                    while ((it + 1) * (it + 2) / 2 <= bi) ++it;
+                    const int jt = bi - it * (it + 1) / 2;
+                    const T* krow = lds.K + (16 * jt + c) * RD;
+                    const T* qrow = lds.Q + (16 * it + c) * RD;
+                    f32x4 G = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < DC; k += 32)
+                        G = O::mma(O::nat(krow + k, g), O::nat(qrow + k, g), G);
+                    f32x4 pv;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        float f = fac[0][v];
+#pragma unroll
+                        for (int d = 1; d < NT; ++d) f = it - jt == d ? fac[d][v] : f;
+                        // above the diagonal a product may be non-finite: select, not multiply
+                        pv[v] = (it > jt || c >= 4 * g + v) ? G[v] * f : 0.0f;
+                    }
+                    O::st4(lds.P + (16 * it + c) * Lds::kRowP + 16 * jt + 4 * g, pv);
+                    if constexpr (kBwd) {
+                        if (ps.dg_pairs) {
+                            // this column block's share of x_i . v_j
+                            const T* vrow = lds.V + (16 * jt + c) * RO;
+                            const T* xrow = lds.X + (16 * it + c) * RO;
+                            f32x4 A = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int k = 0; k < DOB; k += 32)
+                                A = O::mma(O::nat(vrow + k, g), O::nat(xrow + k, g), A);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const int n = 16 * (it - jt) + c - 4 * g - v;
+                                dgi += n > 0 ? static_cast<float>(n) * pv[v] * A[v] : 0.0f;
+                            }
+                        }
+                    }
+                }
+            }
+
+            // q S from the accumulators
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                for (int it = 0; it < NT; ++it) Y[pt][it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < NN / 2; ++k) {
+                Frag q[NT];
+#pragma unroll
+                for (int it = 0; it < NT; ++it) q[it] = O::perm(lds.Q + (16 * it + c) * RD + 32 * k, g);
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = S[2 * k][pt][e];
+                        x[e + 4] = S[2 * k + 1][pt][e];
+                    }
+                    const Frag s0 = O::term(x);
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) Y[pt][it] = O::mma(s0, q[it], Y[pt][it]);
+                    if constexpr (kBwd && O::kSplit) {
+                        if (exact) {
+                            const Frag s1 = O::term(x), s2 = O::term(x);
+#pragma unroll
+                            for (int it = 0; it < NT; ++it) {
+                                Y[pt][it] = O::mma(s1, q[it], Y[pt][it]);
+                                Y[pt][it] = O::mma(s2, q[it], Y[pt][it]);
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                for (int it = 0; it < NT; ++it) Y[pt][it] *= eo[it];
+            if constexpr (kBwd) {
+                if (ps.x != nullptr) {
+                    // the decay's gradient through the state: x_i . (this part
+                    // of the output), by the token's place in the segment
+                    float sum = dgi;
+                    const int win = static_cast<int>((t0 - seg0) % kLinWindow);
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) {
+                        const int i = 16 * it + c;
+                        float d = 0.0f;
+#pragma unroll
+                        for (int pt = 0; pt < NP; ++pt) {
+                            const f32x4 x = O::ld4(lds.X + i * RO + PW * w + 16 * pt + 4 * g);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) d = fmaf(x[v], Y[pt][it][v], d);
+                        }
+                        const int at = rev ? cnt - 1 - i : i;   // token t0 + at
+                        int place = win + at + 1;
+                        if (strong) place = rev ? at + 1 - cnt : at + 1;
+                        sum = fmaf(static_cast<float>(rev ? -place : place), d, sum);
+                    }
+                    dg += static_cast<double>(sum);
+                    // the last chunk of a head that counts inside chunks may be short
+                    if (strong && ps.dg_pairs && ch == nchunks - 1)
+                        dg += adjoint_dot() * static_cast<double>(static_cast<float>(cnt) * lds.pow[cnt]);
+                }
+            }
+            __syncthreads();
+        }
+
+        // v as the products over tokens read it, and those products
+        Frag vf[NP][NS];
+#pragma unroll
+        for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                vf[pt][s] = O::template tr<RO>(lds.V, 32 * s, PW * w + 16 * pt, c, g);
+        if constexpr (!kState) {
+#pragma unroll
+            for (int it = 0; it < NT; ++it)
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    if (32 * s < 16 * (it + 1)) {
+                        const Frag p = O::nat(lds.P + (16 * it + c) * Lds::kRowP + 32 * s, g);
+#pragma unroll
+                        for (int pt = 0; pt < NP; ++pt) Y[pt][it] = O::mma(vf[pt][s], p, Y[pt][it]);
+                    }
+            // out rows 16 it + c, columns 16 pt + 4 g .. + 3 of the wave's
+            const int osz = ps.out32 ? 4 : static_cast<int>(sizeof(T));
+            const int ho = hd / (a.heads / ps.ho);
+            const int64_t first = ((b * L + t0) * ps.ho + ho) * dout;
+            const __amdgpu_buffer_rsrc_t ro = lin_rsrc(static_cast<char*>(ps.out) + first * osz,
+                                                       ((cnt - 1) * ps.ho * dout + dout) * osz);
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+                const int i = 16 * it + c;
+                const int row = rev ? cnt - 1 - i : i;
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt) {
+                    const int p = p0 + PW * w + 16 * pt + 4 * g;
+                    const int off = i < cnt && p < dout ? (row * ps.ho * dout + p) * osz : kPastEnd;
+                    typedef __attribute__((__vector_size__(16))) uint32_t u32x4;
+                    typedef __attribute__((__vector_size__(8))) uint32_t u32x2;
+                    if (sizeof(T) == 4 || ps.out32) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[pt][it]), ro, off, 0, 0);
+                    } else {
+                        bf16x4 o;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[pt][it][v]);
+                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ro, off, 0, 0);
+                    }
+                }
+            }
+        }
+
+        // the state: S + (lam^cnt - 1) S, which rounds only the change (a
+        // factor next to 1 applied chunk after chunk would drift by its own
+        // rounding), then the chunk's tokens
+        const float em = cnt == C ? em_full : (g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(cnt)));
+#pragma unroll
+        for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) S[nt][pt][v] = fmaf(S[nt][pt][v], em, S[nt][pt][v]);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            Frag v0[NP], v1[NP], v2[NP];
+            const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds.W[32 * s + 8 * g]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds.W[32 * s + 8 * g + 4]);
+#pragma unroll
+            for (int pt = 0; pt < NP; ++pt) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = O::get(vf[pt][s], e) * (e < 4 ? w0[e] : w1[e - 4]);
+                v0[pt] = O::term(x);
+                if constexpr (O::kSplit) v1[pt] = O::term(x);
+                if constexpr (O::kSplit && MODE != kLinFwd) v2[pt] = O::term(x);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt) {
+                const Frag kf = O::template tr<RD>(lds.K, 32 * s, 16 * nt, c, g);
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt) {
+                    S[nt][pt] = O::mma(kf, v0[pt], S[nt][pt]);
+                    if constexpr (O::kSplit) S[nt][pt] = O::mma(kf, v1[pt], S[nt][pt]);
+                    if constexpr (O::kSplit && MODE != kLinFwd) {
+                        if (exact) S[nt][pt] = O::mma(kf, v2[pt], S[nt][pt]);
+                    }
+                }
+            }
+        }
+        if constexpr (kBwd) {
+            // where two windows meet, the state and the adjoint are kept for
+            // linear_attn_marks_kernel
+            if (ps.marks != nullptr && !strong) {
+                const int64_t at = (rev ? t0 : t0 + cnt) - seg0;
+                if (at % kLinWindow == 0 && at > 0 && at < ntok)
+                    store_state(ps.marks + ((bh * a.nseg + seg) * a.nmark + at / kLinWindow - 1) * state_elems);
+            }
+        }
+        __syncthreads();
+    }
+
+    // the walk's end: the state leaves for the caller, or (kLinState) for the
+    // join of the segments
+    float* sout = nullptr;
+    if constexpr (kState) {
+        sout = ps.seg_in + (bh * a.nseg + seg) * state_elems;
+    } else {
+        const bool last = seg == (rev ? 0 : a.nseg - 1);
+        if (last && ps.s_out != nullptr) sout = ps.s_out + bh * state_elems;
+    }
+    if (sout != nullptr) store_state(sout);
+    if constexpr (!kState) {
+        // rows behind the sequence's end: zeros
+        const int64_t z0 = end > seg0 ? end : seg0;
+        const int ho = hd / (a.heads / ps.ho);
+        const int cols = dout - p0 < DOB ? dout - p0 : DOB;
+        const int64_t count = (seg1 - z0) * cols;
+        for (int64_t e = tid; e < count; e += kLinThreads) {
+            const int64_t at = ((b * L + z0 + e / cols) * ps.ho + ho) * dout + p0 + e % cols;
+            if (sizeof(T) == 4 || ps.out32) static_cast<float*>(ps.out)[at] = 0.0f;
+            else static_cast<__bf16*>(ps.out)[at] = static_cast<__bf16>(0.0f);
+        }
+    }
+    if constexpr (kBwd) {
+        if (dg_out != nullptr) {
+            if (ps.dg_pairs && ntok > 0 && !strong)
+                dg += adjoint_dot() * static_cast<double>((ntok - 1) % kLinWindow + 1);
+#pragma unroll
+            for (int m = 1; m < kWave; m *= 2) dg += __shfl_xor(dg, m);
+            if (lane == 0) lds.red[w] = dg;
+            __syncthreads();
+            if (tid == 0) {
+                double sum = 0.0;
+                for (int u = 0; u < kLinWaves; ++u) sum += lds.red[u];
+                *dg_out = sum;
+            }
+        }
+    }
+}
+
+}  // namespace
+}  // namespace mamba

@@ -1,0 +1,205 @@
+"""Layer norm forward and backward on the GPU against 64 bits.
+
+Tolerances. In fp32 a sum of up to 16384 values rounds at most about 48 times
+along any path (a lane's 8 to 32 terms in turn, then a tree), 48 * 2^-24 =
+3e-6 (SUMS) of the sum of its absolute values. So mean is off by SUMS *
+mean|x|, the centred value and with it xh = (x - mean) rstd by SUMS * (|xh| +
+rstd mean|x|) - the mean's error does not shrink with x - mean - and rstd by
+SUMS of itself and of rstd mean|x|. y = xh w + b adds its own roundings; dx is
+a difference of three terms, each off by SUMS of its size where xh counts as
+|xh| + rstd mean|x|. A bf16 output adds 2^-8 of the value. dweight and dbias
+add the rows: SUMS of the sum of |terms| per column, xh counting likewise.
+"""
+import sys
+
+import pytest
+import torch
+
+import layers_ref as ref
+import selective_state_space_40_amd as ms
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, F32 = torch.bfloat16, torch.float32
+SUMS = 3e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ms.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def _say(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+def _within(got, want, bound, dtype, what):
+    g, w = got.double().cpu(), want.double()
+    assert g.shape == w.shape, what
+    if w.numel() == 0:
+        return
+    if dtype == BF:
+        bound = bound + 2.0 ** -8 * w.abs()
+    worst = ((g - w).abs() - bound).max().item()
+    assert worst <= 0, f"{what}: {worst:.3e} beyond the bound"
+
+
+def _make(rows, dim, dtype, seed, affine=True, offset=0.5):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, dim, generator=g) + offset * torch.randn(dim, generator=g)).to(dtype)
+    dy = torch.randn(rows, dim, generator=g).to(dtype)
+    w, b = 1 + 0.2 * torch.randn(dim, generator=g), torch.randn(dim, generator=g)
+    return tuple(None if t is None else t.to(DEV) for t in (x, dy, w if affine else None, b if affine else None))
+
+
+def _check(x, dy, w, b, groups, what, eps=1e-5):
+    dt = x.dtype
+    y, mean, rstd = ms.layer_norm_fwd(x, w, b, groups=groups, eps=eps)
+    grads = ms.layer_norm_bwd(x, w, mean, rstd, dy=dy, groups=groups)
+    torch.cuda.synchronize()
+    yr, mr, rr = ref.norm(x, w, b, groups, eps)
+    rows, dim = x.shape
+    split = lambda t: t.reshape(rows, groups, -1)   # noqa: E731
+    size = split(x.double().cpu()).abs().mean(-1)               # mean |x| of a part
+    xh = ref.norm(x, None, None, groups, eps)[0]
+    xs = (split(xh.abs()) + (rr * size)[..., None]).reshape(rows, dim)   # |xh| as it rounds
+    wd = torch.ones(dim, dtype=torch.float64) if w is None else w.double().cpu()
+    bd = torch.zeros(dim, dtype=torch.float64) if b is None else b.double().cpu()
+    dyd = dy.double().cpu()
+    _within(y, yr, SUMS * (wd.abs() * xs + bd.abs()), dt, f"{what} y")
+    _within(mean, mr, SUMS * size, F32, f"{what} mean")
+    _within(rstd, rr, SUMS * rr * (1 + rr * size), F32, f"{what} rstd")
+    dx, dw, db = ref.norm_grads(x, w, dy, groups, eps)
+    up = (dyd * wd).abs()
+    terms = split(up) + split(up).mean(-1, keepdim=True) + split(xs) * split(up * xs).mean(-1, keepdim=True)
+    _within(grads["dx"], dx, SUMS * (rr[..., None] * terms).reshape(rows, dim), dt, f"{what} dx")
+    for got, want, terms in ((grads["dweight"], dw, dyd.abs() * xs), (grads["dbias"], db, dyd.abs())):
+        if got is not None:
+            _within(got, want, SUMS * terms.sum(0), F32, f"{what} column sums")
+
+
+# widths at the edges of every team of lanes, odd ones, one value
+WIDTHS = [1, 2, 7, 8, 64, 120, 128, 129, 256, 384, 385, 392, 512, 1000, 1024, 1531, 1536, 1537, 1544,
+          2048, 4095, 4096, 5120, 6144, 6145, 6152, 8192, 10001, 12288, 16383, 16384]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dim", WIDTHS)
+def test_widths(dim, dtype):
+    for rows in (1, 5, 67):
+        _say(f"case {rows} x {dim} {dtype}")
+        _check(*_make(rows, dim, dtype, dim + rows), 1, f"{rows} x {dim} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", [(33, 1024, 16), (7, 24, 8), (130, 37 * 3, 3), (300, 4096, 2), (9, 12, 12),
+                                  (2000, 640, 5), (5, 16384 * 3, 3)], ids=lambda c: "x".join(map(str, c)))
+def test_groups(case, dtype):
+    rows, dim, groups = case
+    _say(f"case groups {case} {dtype}")
+    _check(*_make(rows, dim, dtype, sum(case)), groups, f"groups {case} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_many_rows(dtype):
+    # every workgroup takes several turns, the last ones of different length
+    for rows, dim in ((20011, 64), (5003, 520), (3001, 2050)):
+        _say(f"case rows {rows} x {dim} {dtype}")
+        _check(*_make(rows, dim, dtype, rows), 1, f"rows {rows} x {dim} {dtype}")
+
+
+def test_without_parameters_and_wanted_outputs():
+    x, dy, _, _ = _make(40, 96, F32, 1, affine=False)
+    _check(x, dy, None, None, 1, "plain")
+    y, mean, rstd = ms.layer_norm_fwd(x)
+    full = ms.layer_norm_bwd(x, None, mean, rstd, dy=dy)
+    part = ms.layer_norm_bwd(x, None, mean, rstd, dy=dy, want_dbias=False)
+    assert full["dweight"] is None and part["dbias"] is None
+    assert torch.equal(full["dx"], part["dx"])
+
+
+def test_offset_far_above_the_spread():
+    # the variance is that of centred values: an offset of 1000 spreads costs
+    # what the inputs' own rounding costs and no more. fp32 inputs 1000 + N(0,1)
+    # are exact in the reference too, so only mean's rounding (2^-24 * 1000 *
+    # few) enters the centred values: 4 * 6e-5 of a spread
+    g = torch.Generator().manual_seed(2)
+    x = (1000.0 + torch.randn(50, 777, generator=g)).to(DEV)
+    y, mean, rstd = ms.layer_norm_fwd(x)
+    yr, mr, rr = ref.norm(x)
+    assert (y.double().cpu() - yr).abs().max() <= 2.5e-4
+    assert (rstd.double().cpu() - rr).abs().max() <= 1e-5
+
+
+def test_constant_rows_and_special_values():
+    x = torch.full((3, 64), 2.0, device=DEV)
+    w, b = torch.randn(64, device=DEV), torch.randn(64, device=DEV)
+    y, mean, rstd = ms.layer_norm_fwd(x, w, b)
+    assert torch.equal(y, b.expand_as(y)) and (mean == 2.0).all()
+    assert ((rstd.double() - 1e-5 ** -0.5).abs() <= 1e-4).all()
+    x = torch.randn(4, 300, device=DEV)
+    x[1, 7] = float("nan")
+    x[2, 9] = float("inf")
+    y, mean, rstd = ms.layer_norm_fwd(x)
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2]).any()
+    assert torch.isfinite(y[0]).all() and torch.isfinite(y[3]).all()
+
+
+def test_in_place_and_shapes():
+    x, dy, w, b = _make(24, 200, BF, 3)
+    y, mean, rstd = ms.layer_norm_fwd(x, w, b)
+    g = ms.layer_norm_bwd(x, w, mean, rstd, dy=dy)
+    x3 = x.view(2, 12, 200)
+    y3, m3, r3 = ms.layer_norm_fwd(x3, w, b)
+    assert torch.equal(y3.view_as(y), y) and m3.shape == (2, 12, 1)
+    keep = x.clone()
+    assert ms.layer_norm_fwd(keep, w, b, out=keep)[0] is keep and torch.equal(keep, y)
+    d = dy.clone()
+    g2 = ms.layer_norm_bwd(x, w, mean, rstd, dy=d, out=d)
+    assert torch.equal(d, g["dx"]) and torch.equal(g2["dweight"], g["dweight"])
+    y0, m0, _ = ms.layer_norm_fwd(x[:0], w, b)
+    assert y0.shape == (0, 200)
+    g0 = ms.layer_norm_bwd(x[:0], w, m0, m0, dy=dy[:0])
+    assert (g0["dweight"] == 0).all() and (g0["dbias"] == 0).all()
+
+
+def test_gradients_against_differences():
+    # central differences of the 64-bit forward pass: error O(step^2)
+    x, dy, w, b = _make(5, 40, F32, 4)
+    y, mean, rstd = ms.layer_norm_fwd(x, w, b, groups=2)
+    g = ms.layer_norm_bwd(x, w, mean, rstd, dy=dy, groups=2)
+    gen = torch.Generator().manual_seed(5)
+    loss = lambda x, w, b: (ref.norm(x, w, b, 2)[0] * dy.double().cpu()).sum().item()   # noqa: E731
+    args = dict(x=x.double(), w=w.double(), b=b.double())
+    for name, key in (("x", "dx"), ("w", "dweight"), ("b", "dbias")):
+        d = torch.randn(args[name].shape, generator=gen, dtype=torch.float64).to(DEV)
+        up = loss(**{**args, name: args[name] + 1e-4 * d})
+        down = loss(**{**args, name: args[name] - 1e-4 * d})
+        want = (g[key].double() * d).sum().item()
+        size = (g[key].double().norm() * d.norm()).item()
+        assert abs((up - down) / 2e-4 - want) <= 1e-5 * size, name
+
+
+def test_captured_calls_replay():
+    x, dy, w, b = _make(700, 1000, BF, 6)
+    y, mean, rstd = ms.layer_norm_fwd(x, w, b)
+    want = [y, mean, rstd, *ms.layer_norm_bwd(x, w, mean, rstd, dy=dy).values()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gy, gm, gr = ms.layer_norm_fwd(x, w, b)
+        got = [gy, gm, gr, *ms.layer_norm_bwd(x, w, gm, gr, dy=dy).values()]
+    for r in range(4):
+        for t in got:
+            t.fill_(float("nan"))
+        torch.randn(1 << 16, device=DEV).sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, e in zip(got, want):
+            assert torch.equal(a, e), f"replay {r}"
