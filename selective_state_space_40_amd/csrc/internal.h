@@ -177,14 +177,14 @@ struct LinPass {
     const void* k;          // (batch, seqlen, hk, dc)
     const void* v;          // (batch, seqlen, hv, dout)
     const void* x;          // (batch, seqlen, hx, dout) or nullptr: for the decay's gradient
-    void* out;              // (batch, seqlen, ho, dout)
+    void* out;              // (batch, seqlen, heads, dout)
     const float* s_in;      // state the walk starts from, or nullptr (zeros)
     float* s_out;           // receives the state the walk ends with, or nullptr
     float* marks;           // (batch, heads, nseg, nmark, dk, dv) or nullptr: receives the state
                             // (adjoint) between a segment's windows of kLinWindow tokens
     float* seg_in;          // (batch, heads, nseg, dk, dv): state entering each segment
-    int64_t sn, sp;         // strides of a state's rows (dc) and columns (dout)
-    int hq, hk, hv, hx, ho; // heads of each tensor, divisors of the number of heads
+    int sn, sp;             // strides of a state's rows (dc) and columns (dout)
+    int hq, hk, hv, hx;     // heads of each tensor: the call's heads, or those of its keys
     int dc, dout;
     float out_scale;        // factor of q S
     float state_scale;      // factor of the tokens' share of the state
@@ -195,7 +195,8 @@ struct LinPass {
 
 struct LinArgs {
     int64_t batch, seqlen, seg_len;
-    int heads, nseg, nblk, npass;
+    int heads, rep;           // heads, and how many share a head of keys and values
+    int nseg, nblk, npass;
     int nmark;                // windows less one of a segment
     int exact;                // kLinState: the states serve the decay's gradient
     const int32_t* lengths;   // (batch) or nullptr

@@ -263,6 +263,7 @@ LinArgs base_args(const LinearAttnCall& c, const LinPlan& p) {
     a.seqlen = c.seqlen;
     a.seg_len = p.seg_len;
     a.heads = c.heads;
+    a.rep = c.heads / c.kv_heads;
     a.nseg = p.nseg;
     a.npass = 1;
     a.lengths = c.lengths;
@@ -281,7 +282,7 @@ LinPass forward_pass(const LinearAttnCall& c) {
     s.s_out = c.hL;
     s.sn = c.dv;
     s.sp = 1;
-    s.hq = s.hx = s.ho = c.heads;
+    s.hq = s.hx = c.heads;
     s.hk = s.hv = c.kv_heads;
     s.dc = c.dk;
     s.dout = c.dv;
@@ -380,7 +381,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         adj.sn = c.dv;
         adj.sp = 1;
         adj.hq = c.kv_heads;
-        adj.hk = adj.hv = adj.hx = adj.ho = c.heads;
+        adj.hk = adj.hv = adj.hx = c.heads;
         adj.dc = c.dk;
         adj.dout = c.dv;
         adj.out_scale = 1.0f;

@@ -53,6 +53,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kLinThreads = 256;
 constexpr int kLinWaves = kLinThreads / kWave;
 
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
+
 struct F32x8 {
     float v[8];
 };
@@ -269,6 +274,13 @@ __device__ __forceinline__ float decay_power(float g, int n) {
     return (x > 0.0f && x < __builtin_inff()) ? fmaf(x, e, x) : x;
 }
 
+// xcd_contiguous_block in 32 bits.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
+    constexpr uint32_t X = kXcds;
+    const uint32_t q = nblocks / X, r = nblocks % X, xcd = bid % X, k = bid / X;
+    return xcd * q + (xcd < r ? xcd : r) + k;
+}
+
 template <int IO, int DC, int PW, int MODE>
 __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) {
     typedef LinOps<IO> O;
@@ -292,16 +304,21 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
 
     // which (row, head, segment, pass, column block); neighbours in this
     // order read the same rows and share an XCD's L2
-    int64_t id = xcd_contiguous_block(blockIdx.x, gridDim.x);
-    const int blk = static_cast<int>(id % a.nblk);
-    id /= a.nblk;
-    const int ip = static_cast<int>(id % a.npass);
-    id /= a.npass;
-    const int nsegs = kState ? a.nseg - 1 : a.nseg;
-    int seg = static_cast<int>(id % nsegs);
-    id /= nsegs;
-    const int hd = static_cast<int>(id % a.heads);
-    const int64_t b = id / a.heads;
+    const uint32_t nsegs = kState ? a.nseg - 1 : a.nseg;
+    uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+    uint32_t up = id / a.nblk;
+    const int blk = static_cast<int>(id - up * a.nblk);
+    id = up;
+    up = id / a.npass;
+    const int ip = static_cast<int>(id - up * a.npass);
+    id = up;
+    up = id / nsegs;
+    int seg = static_cast<int>(id - up * nsegs);
+    id = up;
+    const int64_t bh = id;                       // row * heads + head
+    const uint32_t row = id / a.heads;
+    const int hd = static_cast<int>(id - row * a.heads);
+    const int64_t b = row;
     const LinPass& ps = a.pass[ip];
     const bool rev = ps.rev != 0;
     const bool exact = kState ? a.exact != 0 : ps.x != nullptr;   // three terms, for the decay's gradient
@@ -344,22 +361,48 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
     // S: block (nt, pt) holds rows n = 16 nt + 4 g + v of column p0 + PW w + 16 pt + c
     const int pc = p0 + PW * w + c;
     const int64_t state_elems = static_cast<int64_t>(dc) * dout;
-    const int64_t bh = b * a.heads + hd;
+    const int state_bytes = dc * dout * 4;
+    // a state in memory, read or written by buffer offsets: rows and columns
+    // past dc x dout fall outside
+    typedef __attribute__((__vector_size__(16))) uint32_t u32x4;
+    typedef __attribute__((__vector_size__(8))) uint32_t u32x2;
+    const int sn = ps.sn, sp = ps.sp;
+    const bool runs = kBwd && sn == 1;   // a block's 4 rows lie together (transposed state)
+    auto state_offset = [&](int nt, int pt) {
+        const int n = 16 * nt + 4 * g, p = pc + 16 * pt;
+        const int off = (n * sn + p * sp) * 4;
+        return (n < dc) & (p < dout) ? off : kPastEnd;
+    };
+    // f(nt, pt, block) over a state in memory; dc is a multiple of 4, so a
+    // block's 4 rows are all in or all out
+    auto load_state = [&](const float* from, auto f) {
+        const __amdgpu_buffer_rsrc_t rs = lin_rsrc(from, from != nullptr ? state_bytes : 0);
+        if (runs) {
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt)
+                    f(nt, pt, __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                            rs, state_offset(nt, pt), 0, 0)));
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt) {
+                    f32x4 x;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        x[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                            rs, state_offset(nt, pt), v * sn * 4, 0));
+                    f(nt, pt, x);
+                }
+        }
+    };
     const float* sin = ps.s_in != nullptr ? ps.s_in + bh * state_elems : nullptr;
     if (a.nseg > 1) sin = ps.seg_in + (bh * a.nseg + seg) * state_elems;
     if (kState) sin = nullptr;
     f32x4 S[NN][NP];
-#pragma unroll
-    for (int nt = 0; nt < NN; ++nt)
-#pragma unroll
-        for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int n = 16 * nt + 4 * g + v, p = pc + 16 * pt;
-                S[nt][pt][v] = (sin != nullptr && n < dc && p < dout)
-                                   ? sin[static_cast<int64_t>(n) * ps.sn + static_cast<int64_t>(p) * ps.sp]
-                                   : 0.0f;
-            }
+    load_state(sin, [&](int nt, int pt, f32x4 x) { S[nt][pt] = x; });
 
     // factors of P for the blocks d = it - jt below the diagonal, and of q S
     // for token 16 it + c: the same for every chunk
@@ -376,8 +419,9 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
         for (int it = 0; it < NT; ++it) eo[it] = ps.out_scale * lds.pow[16 * it + c + 1 - r];
     }
 
-    const int hq = hd / (a.heads / ps.hq), hk = hd / (a.heads / ps.hk);
-    const int hv = hd / (a.heads / ps.hv), hx = kBwd ? hd / (a.heads / ps.hx) : 0;
+    const int shared = hd / a.rep;   // the head of keys and values
+    const int hq = ps.hq == a.heads ? hd : shared, hk = ps.hk == a.heads ? hd : shared;
+    const int hv = ps.hv == a.heads ? hd : shared, hx = ps.hx == a.heads ? hd : shared;
     const int64_t nchunks = (ntok + C - 1) / C;
     // chunk ch of the walk: its first token and count (0 past the end). Both
     // directions cut at the same tokens, as the decay's gradient adds what one
@@ -401,7 +445,23 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
         if constexpr (kBwd)
             tx.load(HeadRows<T>(ps.x, row0, ps.hx, hx, dout, ps.x != nullptr ? cnt : 0), p0, dout, cnt, rev);
     };
+    // lam^cnt - 1 of whole chunks and of a short last one
+    const int short_cnt = static_cast<int>(ntok % C);
     const float em_full = g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(C));
+    const float em_short = g1 == 0.0f || short_cnt == 0 ? 0.0f : expm1f(g1 * static_cast<float>(short_cnt));
+    // this wave's blocks of P's lower triangle
+    constexpr int NB = NT * (NT + 1) / 2, BPW = (NB + kLinWaves - 1) / kLinWaves;
+    int bit[BPW], bjt[BPW];
+#pragma unroll
+    for (int u = 0; u < BPW; ++u) {
+        const int bi = u * kLinWaves + w;
+        int it = 0;
+#pragma unroll
+        for (int t = 1; t < NT; ++t)
+            if (bi >= t * (t + 1) / 2) it = t;
+        bit[u] = it;
+        bjt[u] = bi - it * (it + 1) / 2;
+    }
     double dg = 0.0;
     // the adjoint at the segment's end against S, this thread's part
     auto adjoint_dot = [&]() -> double {
@@ -409,30 +469,31 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
                                       : (a.dhL != nullptr ? a.dhL + bh * state_elems : nullptr);
         if (adj == nullptr) return 0.0;
         float sum = 0.0f;
+        load_state(adj, [&](int nt, int pt, f32x4 x) {   // zeros outside the state
 #pragma unroll
-        for (int nt = 0; nt < NN; ++nt)
-#pragma unroll
-            for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = 16 * nt + 4 * g + v, p = pc + 16 * pt;
-                    if (n < dc && p < dout)
-                        sum = fmaf(S[nt][pt][v],
-                                   adj[static_cast<int64_t>(n) * ps.sn + static_cast<int64_t>(p) * ps.sp], sum);
-                }
+            for (int v = 0; v < 4; ++v) sum = fmaf(S[nt][pt][v], x[v], sum);
+        });
         return static_cast<double>(sum);
     };
     auto store_state = [&](float* to) {
+        const __amdgpu_buffer_rsrc_t rs = lin_rsrc(to, state_bytes);
+        if (runs) {
 #pragma unroll
-        for (int nt = 0; nt < NN; ++nt)
+            for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
-            for (int pt = 0; pt < NP; ++pt)
+                for (int pt = 0; pt < NP; ++pt)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nt][pt]), rs,
+                                                           state_offset(nt, pt), 0, 0);
+        } else {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = 16 * nt + 4 * g + v, p = pc + 16 * pt;
-                    if (n < dc && p < dout)
-                        to[static_cast<int64_t>(n) * ps.sn + static_cast<int64_t>(p) * ps.sp] = S[nt][pt][v];
-                }
+            for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+                for (int pt = 0; pt < NP; ++pt)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[nt][pt][v]), rs,
+                                                              state_offset(nt, pt), v * sn * 4, 0);
+        }
     };
 
     fetch(0);
@@ -451,15 +512,11 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
         f32x4 Y[NP][NT];
         if constexpr (!kState) {
             // P, block by block of the lower triangle
-            constexpr int NB = NT * (NT + 1) / 2;
             float dgi = 0.0f;
 #pragma unroll
-            for (int u = 0; u < (NB + kLinWaves - 1) / kLinWaves; ++u) {
-                const int bi = u * kLinWaves + w;
-                if (bi < NB) {
-                    int it = 0;
-                    while ((it + 1) * (it + 2) / 2 <= bi) ++it;
-                    const int jt = bi - it * (it + 1) / 2;
+            for (int u = 0; u < BPW; ++u) {
+                if (u * kLinWaves + w < NB) {
+                    const int it = bit[u], jt = bjt[u];
                     const T* krow = lds.K + (16 * jt + c) * RD;
                     const T* qrow = lds.Q + (16 * it + c) * RD;
                     f32x4 G = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -580,37 +637,40 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
                         for (int pt = 0; pt < NP; ++pt) Y[pt][it] = O::mma(vf[pt][s], p, Y[pt][it]);
                     }
             // out rows 16 it + c, columns 16 pt + 4 g .. + 3 of the wave's
-            const int osz = ps.out32 ? 4 : static_cast<int>(sizeof(T));
-            const int ho = hd / (a.heads / ps.ho);
-            const int64_t first = ((b * L + t0) * ps.ho + ho) * dout;
-            const __amdgpu_buffer_rsrc_t ro = lin_rsrc(static_cast<char*>(ps.out) + first * osz,
-                                                       ((cnt - 1) * ps.ho * dout + dout) * osz);
+            auto put = [&](auto wide) {
+                constexpr bool kWide = decltype(wide)::value;   // fp32 values
+                constexpr int kSize = kWide ? 4 : 2;
+                const int64_t first = ((b * L + t0) * a.heads + hd) * dout;
+                const __amdgpu_buffer_rsrc_t ro = lin_rsrc(static_cast<char*>(ps.out) + first * kSize,
+                                                           ((cnt - 1) * a.heads * dout + dout) * kSize);
 #pragma unroll
-            for (int it = 0; it < NT; ++it) {
-                const int i = 16 * it + c;
-                const int row = rev ? cnt - 1 - i : i;
+                for (int it = 0; it < NT; ++it) {
+                    const int i = 16 * it + c;
+                    const int at = (rev ? cnt - 1 - i : i) * a.heads * dout;
 #pragma unroll
-                for (int pt = 0; pt < NP; ++pt) {
-                    const int p = p0 + PW * w + 16 * pt + 4 * g;
-                    const int off = i < cnt && p < dout ? (row * ps.ho * dout + p) * osz : kPastEnd;
-                    typedef __attribute__((__vector_size__(16))) uint32_t u32x4;
-                    typedef __attribute__((__vector_size__(8))) uint32_t u32x2;
-                    if (sizeof(T) == 4 || ps.out32) {
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[pt][it]), ro, off, 0, 0);
-                    } else {
-                        bf16x4 o;
+                    for (int pt = 0; pt < NP; ++pt) {
+                        const int p = p0 + PW * w + 16 * pt + 4 * g;
+                        const int off = (i < cnt) & (p < dout) ? (at + p) * kSize : kPastEnd;
+                        if constexpr (kWide) {
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[pt][it]), ro, off, 0, 0);
+                        } else {
+                            bf16x4 o;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[pt][it][v]);
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ro, off, 0, 0);
+                            for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[pt][it][v]);
+                            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ro, off, 0, 0);
+                        }
                     }
                 }
-            }
+            };
+            if constexpr (IO == kIoF32) put(Flag<true>{});
+            else if (kBwd && ps.out32) put(Flag<true>{});
+            else put(Flag<false>{});
         }
 
         // the state: S + (lam^cnt - 1) S, which rounds only the change (a
         // factor next to 1 applied chunk after chunk would drift by its own
         // rounding), then the chunk's tokens
-        const float em = cnt == C ? em_full : (g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(cnt)));
+        const float em = cnt == C ? em_full : em_short;
 #pragma unroll
         for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
@@ -669,11 +729,10 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
     if constexpr (!kState) {
         // rows behind the sequence's end: zeros
         const int64_t z0 = end > seg0 ? end : seg0;
-        const int ho = hd / (a.heads / ps.ho);
         const int cols = dout - p0 < DOB ? dout - p0 : DOB;
         const int64_t count = (seg1 - z0) * cols;
         for (int64_t e = tid; e < count; e += kLinThreads) {
-            const int64_t at = ((b * L + z0 + e / cols) * ps.ho + ho) * dout + p0 + e % cols;
+            const int64_t at = ((b * L + z0 + e / cols) * a.heads + hd) * dout + p0 + e % cols;
             if (sizeof(T) == 4 || ps.out32) static_cast<float*>(ps.out)[at] = 0.0f;
             else static_cast<__bf16*>(ps.out)[at] = static_cast<__bf16>(0.0f);
         }
