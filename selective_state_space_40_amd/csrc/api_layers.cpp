@@ -6,6 +6,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <math.h>
+#include <stdlib.h>
 #include <stdint.h>
 
 #include "internal.h"
@@ -61,7 +62,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, LinPlan* p) {
     const int64_t wide = passes == 1 ? c.dv : (c.dk > c.dv ? c.dk : c.dv);
     const int64_t deep = passes == 1 ? c.dk : wide;
-    p->block_cols = wide > 64 && deep <= 128 ? 128 : 64;
+    p->block_cols = wide > 64 ? 128 : 64;
+    if(getenv("LIN_COLS"))p->block_cols=atoi(getenv("LIN_COLS"));
     p->seg_len = c.seqlen > 0 ? c.seqlen : 1;
     p->nseg = 1;
     if (c.batch == 0 || c.heads == 0 || c.seqlen == 0) return MAMBA_OK;

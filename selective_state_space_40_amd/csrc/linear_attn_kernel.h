@@ -16,15 +16,15 @@
 //                (k, q, do) -> dv, adjoint dS, reversed
 //                (v, do, q) -> dk, adjoint dS^T, reversed
 //
-// Work mapping. A workgroup of 4 waves walks the chunks of one (row, head,
-// segment) for a block of 4 PW output columns; wave w owns PW of them. The
-// state's columns belong to the same wave, so its S (all DC rows, PW columns)
+// Work mapping. A workgroup of 4 or 8 waves walks the chunks of one (row, head,
+// segment) for a block of 64 or 128 output columns; wave w owns 16 of them. The
+// state's columns belong to the same wave, so its S (all DC rows, 16 columns)
 // stays in the accumulators for the whole walk, and the accumulator of two
 // 16 x 16 blocks is, up to a fixed order of the rows, the operand of the
 // product q S: the state passes through neither LDS nor another wave. The
 // chunk's q, k and v rows are staged in LDS; the next chunk's are loaded into
 // registers meanwhile. The C x C matrix P is split over the waves by 16 x 16
-// blocks (only those on and below the diagonal) and exchanged through LDS.
+// blocks and exchanged through LDS.
 //
 // bf16 operands. q, k and v enter the products exactly. P is rounded to bf16
 // (its effect on a bf16 output is that of the output's own rounding). What
@@ -50,13 +50,7 @@ typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLinThreads = 256;
-constexpr int kLinWaves = kLinThreads / kWave;
-
-template <bool V>
-struct Flag {
-    static constexpr bool value = V;
-};
+constexpr int kLinCols = 16;   // output columns of a wave
 
 struct F32x8 {
     float v[8];
@@ -77,15 +71,30 @@ struct LinOps<kIoBF16> {
     typedef bf16x8 Frag;
     static constexpr bool kSplit = true;    // fp32 values enter as bf16 terms
     static constexpr int kChunk = kLinChunkBF16;
-    static constexpr int kPad = 8;          // LDS row padding (elements)
+    // LDS row padding (elements). Cycles of a CU per wave's read, measured:
+    // whole fragments of 16 rows (nat) 4 with 32 bytes, 8 with 16 and 32
+    // without; the transpose read 4 with either. P's rows, written 8 bytes a
+    // lane and read whole, take 8 and 8 with 16 bytes, 16 and 4 with 32.
+    static constexpr int kPad = 16, kPadP = 8;
 
     static __device__ __forceinline__ Frag nat(const T* row, int g) {
         return *reinterpret_cast<const bf16x8*>(row + 8 * g);
     }
-    static __device__ __forceinline__ Frag perm(const T* row, int g) {
-        const bf16x4 a = *reinterpret_cast<const bf16x4*>(row + 4 * g);
-        const bf16x4 b = *reinterpret_cast<const bf16x4*>(row + 16 + 4 * g);
+    // The two halves are read on their own, from addresses that the compiler
+    // does not see to be 32 bytes apart: one ds_read2_b64 for both takes 32
+    // cycles where these take 4 each.
+    static __device__ __forceinline__ Frag perm(const T* lo, const T* hi) {
+        const bf16x4 a = *reinterpret_cast<const bf16x4*>(lo);
+        const bf16x4 b = *reinterpret_cast<const bf16x4*>(hi);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // perm() from a tile staged in that order: a thread's 16 bytes, 8 values at
+    // 8 m of a row, go as two halves to where their fragments have them
+    static __device__ __forceinline__ Frag packed(const T* row, int g) { return nat(row, g); }
+    static __device__ __forceinline__ void pack(T* row, int m, uint4 x) {
+        T* p = row + 32 * (m >> 2) + 16 * (m & 1) + 4 * ((m >> 1) & 1);
+        *reinterpret_cast<uint2*>(p) = make_uint2(x.x, x.y);
+        *reinterpret_cast<uint2*>(p + 8) = make_uint2(x.z, x.w);
     }
     // 8 rows r0 + 8 g + e of column c0 + c of a row-major tile: the LDS
     // transpose read (ds_read_b64_tr_b16). Within each group of 16 lanes,
@@ -137,7 +146,7 @@ struct LinOps<kIoF32> {
     typedef F32x8 Frag;
     static constexpr bool kSplit = false;
     static constexpr int kChunk = kLinChunkF32;
-    static constexpr int kPad = 4;
+    static constexpr int kPad = 4, kPadP = 4;
 
     static __device__ __forceinline__ Frag pair(const float* a, const float* b) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(a), y = *reinterpret_cast<const f32x4*>(b);
@@ -146,8 +155,13 @@ struct LinOps<kIoF32> {
     static __device__ __forceinline__ Frag nat(const T* row, int g) {
         return pair(row + 8 * g, row + 8 * g + 4);
     }
-    static __device__ __forceinline__ Frag perm(const T* row, int g) {
+    static __device__ __forceinline__ Frag perm(const T* lo, const T* hi) { return pair(lo, hi); }
+    // fp32 halves of a fragment are 16 bytes in any order
+    static __device__ __forceinline__ Frag packed(const T* row, int g) {
         return pair(row + 4 * g, row + 16 + 4 * g);
+    }
+    static __device__ __forceinline__ void pack(T* row, int m, uint4 x) {
+        *reinterpret_cast<uint4*>(row + 4 * m) = x;
     }
     template <int RS>
     static __device__ __forceinline__ Frag tr(const T* tile, int r0, int c0, int c, int g) {
@@ -184,68 +198,83 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_rsrc(const void* p, int by
 // An offset past the end of every resource.
 constexpr int kPastEnd = static_cast<int>(0x80000000u);
 
-// The rows of one head's chunk in a (batch, seqlen, heads, dim) tensor.
-template <typename T>
+// One head's rows of a (batch, seqlen, heads, dim) tensor from a segment's
+// first token on. A chunk's resource ends with its last valid token, so rows
+// past it (and, walked backwards, rows before the chunk's first, whose
+// offsets are negative) need no test.
 struct HeadRows {
-    __amdgpu_buffer_rsrc_t rsrc;
+    const char* base;
     int stride;   // bytes from token to token
+    int width;    // bytes of a row
 
-    __device__ __forceinline__ HeadRows(const void* p, int64_t row0, int heads, int head, int dim,
-                                        int cnt)
-        : rsrc(lin_rsrc(static_cast<const T*>(p) + (row0 * heads + head) * dim,
-                        cnt > 0 ? ((cnt - 1) * heads * dim + dim) * static_cast<int>(sizeof(T)) : 0)),
-          stride(heads * dim * static_cast<int>(sizeof(T))) {}
+    __device__ __forceinline__ HeadRows(const void* p, int64_t row0, int heads, int head, int dim, int size)
+        : base(static_cast<const char*>(p) + (row0 * heads + head) * dim * size),
+          stride(heads * dim * size), width(dim * size) {}
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int64_t first, int cnt) const {
+        return lin_rsrc(base + first * stride, cnt > 0 ? (cnt - 1) * stride + width : 0);
+    }
 };
 
-// One tile's share of a thread: COUNT vectors of 16 bytes. Vector e covers
-// row e / VPR and the 16-byte column e % VPR of the padded width.
-template <int IO, int COLS>
+// One tile's share of a thread: COUNT vectors of 16 bytes in the same column,
+// ROWS rows apart.
+template <int IO, int THREADS, int COLS, int PAD>
 struct Tile {
     typedef typename LinOps<IO>::T T;
     static constexpr int kC = LinOps<IO>::kChunk;
-    static constexpr int kRow = COLS + LinOps<IO>::kPad;   // LDS row pitch
+    static constexpr int kRow = COLS + PAD;   // LDS row pitch
     static constexpr int kVec = 16 / sizeof(T);
     static constexpr int VPR = COLS / kVec;
-    static constexpr int COUNT = kC * VPR / kLinThreads;
-    static_assert(kC * VPR % kLinThreads == 0, "whole vectors per thread");
+    static constexpr int ROWS = THREADS / VPR;
+    static constexpr int COUNT = kC / ROWS;
+    static_assert(THREADS % VPR == 0 && kC % ROWS == 0, "whole vectors per thread");
 
     uint4 r[COUNT];
 
-    // Columns col0 .. col0 + COLS of the chunk's rows, of which `dim` exist;
-    // `rev` turns the token order round.
-    __device__ __forceinline__ void load(const HeadRows<T>& h, int col0, int dim, int cnt, bool rev) {
+    // This thread's offset from a chunk's first token (walked backwards: from
+    // its last), columns col0 on.
+    static __device__ __forceinline__ int offset(const HeadRows& h, int col0, bool rev) {
+        const int i = threadIdx.x / VPR, col = (col0 + threadIdx.x % VPR * kVec) * static_cast<int>(sizeof(T));
+        return col < h.width ? (rev ? -i : i) * h.stride + col : kPastEnd;
+    }
+    __device__ __forceinline__ void load(const HeadRows& h, int off, int64_t first, int cnt, bool rev) {
+        const __amdgpu_buffer_rsrc_t rs = h.chunk(first, cnt);
+        const int start = rev ? (cnt - 1) * h.stride : 0, step = (rev ? -ROWS : ROWS) * h.stride;
 #pragma unroll
-        for (int u = 0; u < COUNT; ++u) {
-            const int e = threadIdx.x + u * kLinThreads;
-            const int i = e / VPR, col = col0 + (e % VPR) * kVec;
-            const int row = rev ? cnt - 1 - i : i;
-            const int off = (i < cnt && col < dim) ? row * h.stride + col * static_cast<int>(sizeof(T))
-                                                   : kPastEnd;
-            r[u] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(h.rsrc, off, 0, 0));
-        }
+        for (int u = 0; u < COUNT; ++u)
+            r[u] = __builtin_bit_cast(
+                uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + (start + u * step), 0, 0));
     }
     __device__ __forceinline__ void stage(T* lds) const {
+        T* p = lds + threadIdx.x / VPR * kRow + threadIdx.x % VPR * kVec;
 #pragma unroll
-        for (int u = 0; u < COUNT; ++u) {
-            const int e = threadIdx.x + u * kLinThreads;
-            *reinterpret_cast<uint4*>(lds + (e / VPR) * kRow + (e % VPR) * kVec) = r[u];
-        }
+        for (int u = 0; u < COUNT; ++u) *reinterpret_cast<uint4*>(p + u * ROWS * kRow) = r[u];
+    }
+    // in the order of packed()
+    __device__ __forceinline__ void stage_packed(T* lds) const {
+        T* p = lds + threadIdx.x / VPR * kRow;
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) LinOps<IO>::pack(p + u * ROWS * kRow, threadIdx.x % VPR, r[u]);
     }
 };
 
-template <int IO, int DC, int PW, int MODE>
+template <int IO, int DC, int WAVES, int MODE>
 struct LinLds {
     typedef typename LinOps<IO>::T T;
     static constexpr int kC = LinOps<IO>::kChunk;
-    static constexpr int kRowP = kC + LinOps<IO>::kPad;
-    alignas(16) T K[kC * Tile<IO, DC>::kRow];
-    alignas(16) T V[kC * Tile<IO, kLinWaves * PW>::kRow];
-    alignas(16) T Q[MODE == kLinState ? 8 : kC * Tile<IO, DC>::kRow];
-    alignas(16) T X[MODE == kLinBwd ? kC * Tile<IO, kLinWaves * PW>::kRow : 8];
+    static constexpr int kRowP = kC + LinOps<IO>::kPadP;
+    static constexpr int kThreads = WAVES * kWave, kCols = WAVES * kLinCols;
+    typedef Tile<IO, kThreads, DC, LinOps<IO>::kPad> TileK;
+    typedef Tile<IO, kThreads, kCols, LinOps<IO>::kPad> TileV;
+    typedef Tile<IO, kThreads, DC, LinOps<IO>::kPad> TileQ;
+    typedef Tile<IO, kThreads, kCols, LinOps<IO>::kPad> TileX;
+    alignas(16) T K[kC * TileK::kRow];
+    alignas(16) T V[kC * TileV::kRow];
+    alignas(16) T Q[MODE == kLinState ? 8 : kC * TileQ::kRow];
+    alignas(16) T X[MODE == kLinBwd ? kC * TileX::kRow : 8];
     alignas(16) T P[MODE == kLinState ? 8 : kC * kRowP];
     alignas(16) float W[kC];      // weight of token j in the state update
     float pow[kC + 1];            // lam^n
-    double red[kLinWaves];
+    double red[WAVES];
 };
 
 // The gradient of the log decay is the sum over pairs (t, j) of steps t - j
@@ -281,8 +310,8 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
     return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
-template <int IO, int DC, int PW, int MODE>
-__global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) {
+template <int IO, int DC, int WAVES, int MODE>
+__global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a) {
     typedef LinOps<IO> O;
     typedef typename O::T T;
     typedef typename O::Frag Frag;
@@ -290,11 +319,11 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
     constexpr int NT = C / 16;            // blocks of 16 tokens
     constexpr int NS = C / 32;            // product steps over tokens
     constexpr int NN = DC / 16;           // blocks of 16 state rows
-    constexpr int NP = PW / 16;           // blocks of 16 columns per wave
-    constexpr int DOB = kLinWaves * PW;   // columns per workgroup
-    constexpr int RD = Tile<IO, DC>::kRow, RO = Tile<IO, DOB>::kRow;
+    constexpr int DOB = WAVES * kLinCols; // columns per workgroup
+    constexpr int THREADS = WAVES * kWave;
     constexpr bool kState = MODE == kLinState, kBwd = MODE == kLinBwd;
-    typedef LinLds<IO, DC, PW, MODE> Lds;
+    typedef LinLds<IO, DC, WAVES, MODE> Lds;
+    constexpr int RK = Lds::TileK::kRow, RV = Lds::TileV::kRow, RQ = Lds::TileQ::kRow, RX = Lds::TileX::kRow;
     __shared__ Lds lds;
 
     const int tid = threadIdx.x;
@@ -350,16 +379,50 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
 
     const float g1 = a.log_decay[hd];
     const bool strong = decay_is_strong(g1, C);
-    if (tid <= C) lds.pow[tid] = decay_power(g1, tid);
-    // P's blocks above the diagonal are read beside those on it and never
-    // written again
-    if constexpr (!kState)
-        for (int e = tid; e < C * Lds::kRowP; e += kLinThreads) lds.P[e] = static_cast<T>(0.0f);
-    __syncthreads();
     const int r = rev ? 1 : 0;
 
-    // S: block (nt, pt) holds rows n = 16 nt + 4 g + v of column p0 + PW w + 16 pt + c
-    const int pc = p0 + PW * w + c;
+    // the inputs' rows and this thread's place in them; the first chunk's
+    // loads go out before anything else
+    const int shared = hd / a.rep;   // the head of keys and values
+    const int64_t row0 = b * L + seg0;
+    const HeadRows rk(ps.k, row0, ps.hk, ps.hk == a.heads ? hd : shared, dc, sizeof(T));
+    const HeadRows rv(ps.v, row0, ps.hv, ps.hv == a.heads ? hd : shared, dout, sizeof(T));
+    const HeadRows rq(ps.q, row0, ps.hq, ps.hq == a.heads ? hd : shared, dc, sizeof(T));
+    const HeadRows rx(ps.x, row0, ps.hx, ps.hx == a.heads ? hd : shared, dout, sizeof(T));
+    const int ok = Lds::TileK::offset(rk, 0, rev), ov = Lds::TileV::offset(rv, p0, rev);
+    const int oq = Lds::TileQ::offset(rq, 0, rev), ox = Lds::TileX::offset(rx, p0, rev);
+    const int64_t nchunks = (ntok + C - 1) / C;
+    // chunk ch of the walk: its first token in the segment and count (0 past
+    // the end). Both directions cut at the same tokens, as the decay's gradient
+    // adds what one direction forms inside a chunk to what both form across
+    // chunks.
+    auto chunk_at = [&](int64_t ch, int64_t& first, int& cnt) {
+        first = (rev ? nchunks - 1 - ch : ch) * C;
+        const int64_t left = ch < nchunks ? ntok - first : 0;
+        cnt = left >= C ? C : static_cast<int>(left);
+    };
+    typename Lds::TileK tk;
+    typename Lds::TileV tv;
+    typename Lds::TileQ tq;
+    typename Lds::TileX tx;
+    auto fetch_kq = [&](int64_t first, int cnt) {
+        tk.load(rk, ok, first, cnt, rev);
+        if constexpr (!kState) tq.load(rq, oq, first, cnt, rev);
+    };
+    auto fetch_vx = [&](int64_t first, int cnt) {
+        tv.load(rv, ov, first, cnt, rev);
+        if constexpr (kBwd) tx.load(rx, ox, first, ps.x != nullptr ? cnt : 0, rev);
+    };
+    {
+        int64_t first;
+        int cnt;
+        chunk_at(0, first, cnt);
+        fetch_kq(first, cnt);
+        fetch_vx(first, cnt);
+    }
+
+    // S: block nt holds rows n = 16 nt + 4 g + v of column p0 + 16 w + c
+    const int pc = p0 + kLinCols * w + c;
     const int64_t state_elems = static_cast<int64_t>(dc) * dout;
     const int state_bytes = dc * dout * 4;
     // a state in memory, read or written by buffer offsets: rows and columns
@@ -368,100 +431,74 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
     typedef __attribute__((__vector_size__(8))) uint32_t u32x2;
     const int sn = ps.sn, sp = ps.sp;
     const bool runs = kBwd && sn == 1;   // a block's 4 rows lie together (transposed state)
-    auto state_offset = [&](int nt, int pt) {
-        const int n = 16 * nt + 4 * g, p = pc + 16 * pt;
-        const int off = (n * sn + p * sp) * 4;
-        return (n < dc) & (p < dout) ? off : kPastEnd;
+    // dc is a multiple of 4: a block's 4 rows are all in or all out
+    auto state_offset = [&](int nt) {
+        const int n = 16 * nt + 4 * g;
+        const int off = (n * sn + pc * sp) * 4;
+        return (n < dc) & (pc < dout) ? off : kPastEnd;
     };
-    // f(nt, pt, block) over a state in memory; dc is a multiple of 4, so a
-    // block's 4 rows are all in or all out
+    // f(nt, block) over a state in memory, zeros outside it
     auto load_state = [&](const float* from, auto f) {
         const __amdgpu_buffer_rsrc_t rs = lin_rsrc(from, from != nullptr ? state_bytes : 0);
         if (runs) {
 #pragma unroll
             for (int nt = 0; nt < NN; ++nt)
-#pragma unroll
-                for (int pt = 0; pt < NP; ++pt)
-                    f(nt, pt, __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                            rs, state_offset(nt, pt), 0, 0)));
+                f(nt, __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, state_offset(nt), 0, 0)));
         } else {
 #pragma unroll
-            for (int nt = 0; nt < NN; ++nt)
+            for (int nt = 0; nt < NN; ++nt) {
+                f32x4 x;
 #pragma unroll
-                for (int pt = 0; pt < NP; ++pt) {
-                    f32x4 x;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        x[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                            rs, state_offset(nt, pt), v * sn * 4, 0));
-                    f(nt, pt, x);
-                }
+                for (int v = 0; v < 4; ++v)
+                    x[v] = __uint_as_float(
+                        __builtin_amdgcn_raw_buffer_load_b32(rs, state_offset(nt) + v * sn * 4, 0, 0));
+                f(nt, x);
+            }
         }
     };
     const float* sin = ps.s_in != nullptr ? ps.s_in + bh * state_elems : nullptr;
     if (a.nseg > 1) sin = ps.seg_in + (bh * a.nseg + seg) * state_elems;
     if (kState) sin = nullptr;
-    f32x4 S[NN][NP];
-    load_state(sin, [&](int nt, int pt, f32x4 x) { S[nt][pt] = x; });
+    f32x4 S[NN];
+    load_state(sin, [&](int nt, f32x4 x) { S[nt] = x; });
 
-    // factors of P for the blocks d = it - jt below the diagonal, and of q S
-    // for token 16 it + c: the same for every chunk
-    float fac[NT][4], eo[NT];
+    if (tid <= C) lds.pow[tid] = decay_power(g1, tid);
+    __syncthreads();
+
+    // P's 16 x 16 blocks: this wave forms those of the columns (tokens j) of
+    // block jt, for the rows it = grp + GR u; blocks above the diagonal come out
+    // as zeros, which the product P v reads beside those on it. The blocks'
+    // factors and those of q S for token 16 it + c are the same for every chunk.
+    constexpr int GR = WAVES / NT, OWN = NT > GR ? NT / GR : 1;
+    const int jt = w % NT, grp = w / NT;
+    const bool forms = grp < NT;
+    const T* klo = lds.K + (16 * jt + c) * RK + 4 * g;
+    int apart = 16;
+    asm volatile("" : "+v"(apart));
+    const T* khi = klo + apart;
+    float fac[OWN][4], eo[NT];
     if constexpr (!kState) {
 #pragma unroll
-        for (int d = 0; d < NT; ++d)
+        for (int u = 0; u < OWN; ++u)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int n = 16 * d + c - 4 * g - v;
-                fac[d][v] = n >= 0 ? a.scale * lds.pow[n] : 0.0f;
+                const int n = 16 * (grp + GR * u - jt) + c - 4 * g - v;
+                fac[u][v] = n >= 0 && n < C ? a.scale * lds.pow[n] : 0.0f;
             }
 #pragma unroll
         for (int it = 0; it < NT; ++it) eo[it] = ps.out_scale * lds.pow[16 * it + c + 1 - r];
     }
-
-    const int shared = hd / a.rep;   // the head of keys and values
-    const int hq = ps.hq == a.heads ? hd : shared, hk = ps.hk == a.heads ? hd : shared;
-    const int hv = ps.hv == a.heads ? hd : shared, hx = ps.hx == a.heads ? hd : shared;
-    const int64_t nchunks = (ntok + C - 1) / C;
-    // chunk ch of the walk: its first token and count (0 past the end). Both
-    // directions cut at the same tokens, as the decay's gradient adds what one
-    // direction forms inside a chunk to what both form across chunks.
-    auto chunk_at = [&](int64_t ch, int64_t& t0, int& cnt) {
-        const int64_t first = (rev ? nchunks - 1 - ch : ch) * C;
-        const int64_t left = ch < nchunks ? ntok - first : 0;
-        cnt = left >= C ? C : static_cast<int>(left);
-        t0 = seg0 + first;
-    };
-    Tile<IO, DC> tq, tk;
-    Tile<IO, DOB> tv, tx;
-    auto fetch = [&](int64_t ch) {
-        int64_t t0;
-        int cnt;
-        chunk_at(ch, t0, cnt);
-        const int64_t row0 = b * L + t0;
-        tk.load(HeadRows<T>(ps.k, row0, ps.hk, hk, dc, cnt), 0, dc, cnt, rev);
-        tv.load(HeadRows<T>(ps.v, row0, ps.hv, hv, dout, cnt), p0, dout, cnt, rev);
-        if constexpr (!kState) tq.load(HeadRows<T>(ps.q, row0, ps.hq, hq, dc, cnt), 0, dc, cnt, rev);
-        if constexpr (kBwd)
-            tx.load(HeadRows<T>(ps.x, row0, ps.hx, hx, dout, ps.x != nullptr ? cnt : 0), p0, dout, cnt, rev);
-    };
-    // lam^cnt - 1 of whole chunks and of a short last one
+    // lam^cnt - 1 of whole chunks and of a short one
     const int short_cnt = static_cast<int>(ntok % C);
     const float em_full = g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(C));
     const float em_short = g1 == 0.0f || short_cnt == 0 ? 0.0f : expm1f(g1 * static_cast<float>(short_cnt));
-    // this wave's blocks of P's lower triangle
-    constexpr int NB = NT * (NT + 1) / 2, BPW = (NB + kLinWaves - 1) / kLinWaves;
-    int bit[BPW], bjt[BPW];
-#pragma unroll
-    for (int u = 0; u < BPW; ++u) {
-        const int bi = u * kLinWaves + w;
-        int it = 0;
-#pragma unroll
-        for (int t = 1; t < NT; ++t)
-            if (bi >= t * (t + 1) / 2) it = t;
-        bit[u] = it;
-        bjt[u] = bi - it * (it + 1) / 2;
-    }
+    // where this lane's outputs go: token 16 it + c, columns 4 g .. + 3 of the
+    // wave's
+    const bool wide = IO == kIoF32 || (kBwd && ps.out32);
+    const int osize = wide ? 4 : 2;
+    const HeadRows ro(ps.out, row0, a.heads, hd, dout, osize);
+    const int po = p0 + kLinCols * w + 4 * g;
+    const int oo = po < dout ? (rev ? -c : c) * ro.stride + po * osize : kPastEnd;
     double dg = 0.0;
     // the adjoint at the segment's end against S, this thread's part
     auto adjoint_dot = [&]() -> double {
@@ -469,9 +506,9 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
                                       : (a.dhL != nullptr ? a.dhL + bh * state_elems : nullptr);
         if (adj == nullptr) return 0.0;
         float sum = 0.0f;
-        load_state(adj, [&](int nt, int pt, f32x4 x) {   // zeros outside the state
+        load_state(adj, [&](int nt, f32x4 x) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sum = fmaf(S[nt][pt][v], x[v], sum);
+            for (int v = 0; v < 4; ++v) sum = fmaf(S[nt][v], x[v], sum);
         });
         return static_cast<double>(sum);
     };
@@ -480,64 +517,107 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
         if (runs) {
 #pragma unroll
             for (int nt = 0; nt < NN; ++nt)
-#pragma unroll
-                for (int pt = 0; pt < NP; ++pt)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nt][pt]), rs,
-                                                           state_offset(nt, pt), 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nt]), rs, state_offset(nt), 0, 0);
         } else {
 #pragma unroll
             for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
-                for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[nt][pt][v]), rs,
-                                                              state_offset(nt, pt), v * sn * 4, 0);
+                for (int v = 0; v < 4; ++v)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[nt][v]), rs,
+                                                          state_offset(nt) + v * sn * 4, 0, 0);
         }
     };
 
-    fetch(0);
+    if constexpr (!kState) {
+        // as many stores before the first chunk as a chunk issues (dropped, past
+        // the end of an empty range): the waits for a chunk's loads then
+        // count the stores behind them and need not wait for those
+        const __amdgpu_buffer_rsrc_t none = lin_rsrc(ps.out, 0);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            if (wide) __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, none, 16 * u, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b64(u32x2{0, 0}, none, 16 * u, 0, 0);
+        }
+    }
     for (int64_t ch = 0; ch < nchunks; ++ch) {
-        int64_t t0;
+        int64_t first;
         int cnt;
-        chunk_at(ch, t0, cnt);
+        chunk_at(ch, first, cnt);
+        // (1) stage. The tiles' last readers passed the barrier before P V.
         tk.stage(lds.K);
+        if constexpr (!kState) tq.stage_packed(lds.Q);
         tv.stage(lds.V);
-        if constexpr (!kState) tq.stage(lds.Q);
         if constexpr (kBwd) tx.stage(lds.X);
         if (tid < C) lds.W[tid] = tid < cnt ? ps.state_scale * lds.pow[cnt - 1 - tid + r] : 0.0f;
         __syncthreads();
-        fetch(ch + 1);
+        // the next chunk's loads go out in two groups, as the units that
+        // address them take as long as a chunk's products
+        int64_t next;
+        int next_cnt;
+        chunk_at(ch + 1, next, next_cnt);
+        fetch_kq(next, next_cnt);
 
-        f32x4 Y[NP][NT];
+        f32x4 Y[NT];
         if constexpr (!kState) {
-            // P, block by block of the lower triangle
+            // (2) q k^T and q S (from the accumulators), which share q's fragments
+            f32x4 G[OWN];
+#pragma unroll
+            for (int u = 0; u < OWN; ++u) G[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int it = 0; it < NT; ++it) Y[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < NN / 2; ++k) {
+                Frag q[NT];
+#pragma unroll
+                for (int it = 0; it < NT; ++it) q[it] = O::packed(lds.Q + (16 * it + c) * RQ + 32 * k, g);
+                if constexpr (GR == 1) {
+                    const Frag kf = O::perm(klo + 32 * k, khi + 32 * k);
+#pragma unroll
+                    for (int u = 0; u < OWN; ++u) G[u] = O::mma(kf, q[u], G[u]);
+                }
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = S[2 * k][e];
+                    x[e + 4] = S[2 * k + 1][e];
+                }
+                const Frag s0 = O::term(x);
+#pragma unroll
+                for (int it = 0; it < NT; ++it) Y[it] = O::mma(s0, q[it], Y[it]);
+                if constexpr (kBwd && O::kSplit) {
+                    if (exact) {
+                        const Frag s1 = O::term(x), s2 = O::term(x);
+#pragma unroll
+                        for (int it = 0; it < NT; ++it) Y[it] = O::mma(s1, q[it], Y[it]);
+#pragma unroll
+                        for (int it = 0; it < NT; ++it) Y[it] = O::mma(s2, q[it], Y[it]);
+                    }
+                }
+            }
             float dgi = 0.0f;
+            if (forms) {
+                if constexpr (GR > 1) {
 #pragma unroll
-            for (int u = 0; u < BPW; ++u) {
-                if (u * kLinWaves + w < NB) {
-                    const int it = bit[u], jt = bjt[u];
-                    const T* krow = lds.K + (16 * jt + c) * RD;
-                    const T* qrow = lds.Q + (16 * it + c) * RD;
-                    f32x4 G = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int k = 0; k < DC; k += 32) {
+                        const Frag kf = O::perm(klo + k, khi + k);
 #pragma unroll
-                    for (int k = 0; k < DC; k += 32)
-                        G = O::mma(O::nat(krow + k, g), O::nat(qrow + k, g), G);
+                        for (int u = 0; u < OWN; ++u)
+                            G[u] = O::mma(kf, O::packed(lds.Q + (16 * (grp + GR * u) + c) * RQ + k, g), G[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < OWN; ++u) {
+                    const int it = grp + GR * u;
                     f32x4 pv;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        float f = fac[0][v];
-#pragma unroll
-                        for (int d = 1; d < NT; ++d) f = it - jt == d ? fac[d][v] : f;
-                        // above the diagonal a product may be non-finite: select, not multiply
-                        pv[v] = (it > jt || c >= 4 * g + v) ? G[v] * f : 0.0f;
-                    }
+                    for (int v = 0; v < 4; ++v)   // a product above the diagonal may be non-finite: select
+                        pv[v] = 16 * (it - jt) + c >= 4 * g + v ? G[u][v] * fac[u][v] : 0.0f;
                     O::st4(lds.P + (16 * it + c) * Lds::kRowP + 16 * jt + 4 * g, pv);
                     if constexpr (kBwd) {
-                        if (ps.dg_pairs) {
+                        if (ps.dg_pairs && it >= jt) {
                             // this column block's share of x_i . v_j
-                            const T* vrow = lds.V + (16 * jt + c) * RO;
-                            const T* xrow = lds.X + (16 * it + c) * RO;
+                            const T* vrow = lds.V + (16 * jt + c) * RV;
+                            const T* xrow = lds.X + (16 * it + c) * RX;
                             f32x4 A = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                             for (int k = 0; k < DOB; k += 32)
@@ -551,61 +631,22 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
                     }
                 }
             }
-
-            // q S from the accumulators
 #pragma unroll
-            for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-                for (int it = 0; it < NT; ++it) Y[pt][it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < NN / 2; ++k) {
-                Frag q[NT];
-#pragma unroll
-                for (int it = 0; it < NT; ++it) q[it] = O::perm(lds.Q + (16 * it + c) * RD + 32 * k, g);
-#pragma unroll
-                for (int pt = 0; pt < NP; ++pt) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = S[2 * k][pt][e];
-                        x[e + 4] = S[2 * k + 1][pt][e];
-                    }
-                    const Frag s0 = O::term(x);
-#pragma unroll
-                    for (int it = 0; it < NT; ++it) Y[pt][it] = O::mma(s0, q[it], Y[pt][it]);
-                    if constexpr (kBwd && O::kSplit) {
-                        if (exact) {
-                            const Frag s1 = O::term(x), s2 = O::term(x);
-#pragma unroll
-                            for (int it = 0; it < NT; ++it) {
-                                Y[pt][it] = O::mma(s1, q[it], Y[pt][it]);
-                                Y[pt][it] = O::mma(s2, q[it], Y[pt][it]);
-                            }
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-                for (int it = 0; it < NT; ++it) Y[pt][it] *= eo[it];
+            for (int it = 0; it < NT; ++it) Y[it] *= eo[it];
             if constexpr (kBwd) {
                 if (ps.x != nullptr) {
                     // the decay's gradient through the state: x_i . (this part
-                    // of the output), by the token's place in the segment
+                    // of the output), by the token's place in its window
                     float sum = dgi;
-                    const int win = static_cast<int>((t0 - seg0) % kLinWindow);
+                    const int win = static_cast<int>(first % kLinWindow);
 #pragma unroll
                     for (int it = 0; it < NT; ++it) {
                         const int i = 16 * it + c;
                         float d = 0.0f;
+                        const f32x4 x = O::ld4(lds.X + i * RX + kLinCols * w + 4 * g);
 #pragma unroll
-                        for (int pt = 0; pt < NP; ++pt) {
-                            const f32x4 x = O::ld4(lds.X + i * RO + PW * w + 16 * pt + 4 * g);
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) d = fmaf(x[v], Y[pt][it][v], d);
-                        }
-                        const int at = rev ? cnt - 1 - i : i;   // token t0 + at
+                        for (int v = 0; v < 4; ++v) d = fmaf(x[v], Y[it][v], d);
+                        const int at = rev ? cnt - 1 - i : i;   // the token's place in the chunk
                         int place = win + at + 1;
                         if (strong) place = rev ? at + 1 - cnt : at + 1;
                         sum = fmaf(static_cast<float>(rev ? -place : place), d, sum);
@@ -616,91 +657,47 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
                         dg += adjoint_dot() * static_cast<double>(static_cast<float>(cnt) * lds.pow[cnt]);
                 }
             }
-            __syncthreads();
         }
 
-        // v as the products over tokens read it, and those products
-        Frag vf[NP][NS];
+        fetch_vx(next, next_cnt);
+        // v as the products over tokens read it
+        Frag vf[NS];
 #pragma unroll
-        for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-            for (int s = 0; s < NS; ++s)
-                vf[pt][s] = O::template tr<RO>(lds.V, 32 * s, PW * w + 16 * pt, c, g);
-        if constexpr (!kState) {
-#pragma unroll
-            for (int it = 0; it < NT; ++it)
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-                    if (32 * s < 16 * (it + 1)) {
-                        const Frag p = O::nat(lds.P + (16 * it + c) * Lds::kRowP + 32 * s, g);
-#pragma unroll
-                        for (int pt = 0; pt < NP; ++pt) Y[pt][it] = O::mma(vf[pt][s], p, Y[pt][it]);
-                    }
-            // out rows 16 it + c, columns 16 pt + 4 g .. + 3 of the wave's
-            auto put = [&](auto wide) {
-                constexpr bool kWide = decltype(wide)::value;   // fp32 values
-                constexpr int kSize = kWide ? 4 : 2;
-                const int64_t first = ((b * L + t0) * a.heads + hd) * dout;
-                const __amdgpu_buffer_rsrc_t ro = lin_rsrc(static_cast<char*>(ps.out) + first * kSize,
-                                                           ((cnt - 1) * a.heads * dout + dout) * kSize);
-#pragma unroll
-                for (int it = 0; it < NT; ++it) {
-                    const int i = 16 * it + c;
-                    const int at = (rev ? cnt - 1 - i : i) * a.heads * dout;
-#pragma unroll
-                    for (int pt = 0; pt < NP; ++pt) {
-                        const int p = p0 + PW * w + 16 * pt + 4 * g;
-                        const int off = (i < cnt) & (p < dout) ? (at + p) * kSize : kPastEnd;
-                        if constexpr (kWide) {
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[pt][it]), ro, off, 0, 0);
-                        } else {
-                            bf16x4 o;
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[pt][it][v]);
-                            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), ro, off, 0, 0);
-                        }
-                    }
-                }
-            };
-            if constexpr (IO == kIoF32) put(Flag<true>{});
-            else if (kBwd && ps.out32) put(Flag<true>{});
-            else put(Flag<false>{});
-        }
+        for (int s = 0; s < NS; ++s) vf[s] = O::template tr<RV>(lds.V, 32 * s, kLinCols * w, c, g);
 
-        // the state: S + (lam^cnt - 1) S, which rounds only the change (a
+        // (4) the state: S + (lam^cnt - 1) S, which rounds only the change (a
         // factor next to 1 applied chunk after chunk would drift by its own
         // rounding), then the chunk's tokens
         const float em = cnt == C ? em_full : em_short;
 #pragma unroll
         for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
-            for (int pt = 0; pt < NP; ++pt)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) S[nt][pt][v] = fmaf(S[nt][pt][v], em, S[nt][pt][v]);
+            for (int v = 0; v < 4; ++v) S[nt][v] = fmaf(S[nt][v], em, S[nt][v]);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            Frag v0[NP], v1[NP], v2[NP];
             const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds.W[32 * s + 8 * g]);
             const f32x4 w1 = *reinterpret_cast<const f32x4*>(&lds.W[32 * s + 8 * g + 4]);
+            float x[8];
 #pragma unroll
-            for (int pt = 0; pt < NP; ++pt) {
-                float x[8];
+            for (int e = 0; e < 8; ++e) x[e] = O::get(vf[s], e) * (e < 4 ? w0[e] : w1[e - 4]);
+            Frag v0 = O::term(x), v1, v2;
+            if constexpr (O::kSplit) v1 = O::term(x);
+            if constexpr (O::kSplit && MODE != kLinFwd) v2 = O::term(x);
+            constexpr int U = 4;   // independent blocks between the terms of one
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = O::get(vf[pt][s], e) * (e < 4 ? w0[e] : w1[e - 4]);
-                v0[pt] = O::term(x);
-                if constexpr (O::kSplit) v1[pt] = O::term(x);
-                if constexpr (O::kSplit && MODE != kLinFwd) v2[pt] = O::term(x);
-            }
+            for (int n0 = 0; n0 < NN; n0 += U) {
+                Frag kf[U];
 #pragma unroll
-            for (int nt = 0; nt < NN; ++nt) {
-                const Frag kf = O::template tr<RD>(lds.K, 32 * s, 16 * nt, c, g);
+                for (int u = 0; u < U; ++u) kf[u] = O::template tr<RK>(lds.K, 32 * s, 16 * (n0 + u), c, g);
 #pragma unroll
-                for (int pt = 0; pt < NP; ++pt) {
-                    S[nt][pt] = O::mma(kf, v0[pt], S[nt][pt]);
-                    if constexpr (O::kSplit) S[nt][pt] = O::mma(kf, v1[pt], S[nt][pt]);
-                    if constexpr (O::kSplit && MODE != kLinFwd) {
-                        if (exact) S[nt][pt] = O::mma(kf, v2[pt], S[nt][pt]);
-                    }
+                for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v0, S[n0 + u]);
+                if constexpr (O::kSplit)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v1, S[n0 + u]);
+                if constexpr (O::kSplit && MODE != kLinFwd) {
+                    if (exact)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v2, S[n0 + u]);
                 }
             }
         }
@@ -708,12 +705,42 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
             // where two windows meet, the state and the adjoint are kept for
             // linear_attn_marks_kernel
             if (ps.marks != nullptr && !strong) {
-                const int64_t at = (rev ? t0 : t0 + cnt) - seg0;
+                const int64_t at = rev ? first : first + cnt;
                 if (at % kLinWindow == 0 && at > 0 && at < ntok)
                     store_state(ps.marks + ((bh * a.nseg + seg) * a.nmark + at / kLinWindow - 1) * state_elems);
             }
         }
         __syncthreads();
+
+        // (5) P v onto q S, and out; the next chunk's tiles may be staged by
+        // other waves meanwhile
+        if constexpr (!kState) {
+#pragma unroll
+            for (int it = 0; it < NT; ++it)
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    if (32 * s < 16 * (it + 1)) {
+                        const Frag p = O::nat(lds.P + (16 * it + c) * Lds::kRowP + 32 * s, g);
+                        Y[it] = O::mma(vf[s], p, Y[it]);
+                    }
+            const __amdgpu_buffer_rsrc_t rs = ro.chunk(first, cnt);
+            const int start = rev ? (cnt - 1) * ro.stride : 0, step = (rev ? -16 : 16) * ro.stride;
+            if (wide) {
+#pragma unroll
+                for (int it = 0; it < NT; ++it)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[it]), rs,
+                                                           oo + (start + it * step), 0, 0);
+            } else {
+#pragma unroll
+                for (int it = 0; it < NT; ++it) {
+                    bf16x4 o;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[it][v]);
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), rs,
+                                                          oo + (start + it * step), 0, 0);
+                }
+            }
+        }
     }
 
     // the walk's end: the state leaves for the caller, or (kLinState) for the
@@ -731,9 +758,9 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
         const int64_t z0 = end > seg0 ? end : seg0;
         const int cols = dout - p0 < DOB ? dout - p0 : DOB;
         const int64_t count = (seg1 - z0) * cols;
-        for (int64_t e = tid; e < count; e += kLinThreads) {
+        for (int64_t e = tid; e < count; e += THREADS) {
             const int64_t at = ((b * L + z0 + e / cols) * a.heads + hd) * dout + p0 + e % cols;
-            if (sizeof(T) == 4 || ps.out32) static_cast<float*>(ps.out)[at] = 0.0f;
+            if (wide) static_cast<float*>(ps.out)[at] = 0.0f;
             else static_cast<__bf16*>(ps.out)[at] = static_cast<__bf16>(0.0f);
         }
     }
@@ -747,7 +774,7 @@ __global__ __launch_bounds__(kLinThreads, 2) void linear_attn_kernel(LinArgs a) 
             __syncthreads();
             if (tid == 0) {
                 double sum = 0.0;
-                for (int u = 0; u < kLinWaves; ++u) sum += lds.red[u];
+                for (int u = 0; u < WAVES; ++u) sum += lds.red[u];
                 *dg_out = sum;
             }
         }
