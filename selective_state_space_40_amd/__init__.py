@@ -37,6 +37,7 @@ fp32, mean and rstd (..., groups) fp32.
 """
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -530,35 +531,88 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, h0=None, *, dt_bias=None, dt_softplu
     return y, hL
 
 
-def _scratch(device, nbytes):
+def _fits(t, shape, dtype, index):
+    """Whether t is a contiguous tensor of this shape and dtype on GPU `index`
+    (a cheap test before _need, which says what is wrong)."""
+    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == index)
+
+
+def _require(t, name, shape, dtype, dev):
+    """The address of a tensor that _need accepts; None for None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and _fits(t, shape, dtype, dev.index)):
+        _need(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _must(t, name, shape, dtype, dev):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return _require(t, name, shape, dtype, dev)
+
+
+class _on:
+    """The tensors' device made current for a call, if it is not already."""
+
+    def __init__(self, dev):
+        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _scratch(dev, nbytes):
     """Scratch of one call, from torch's allocator on the current stream: a
     captured graph keeps its own, and calls on different streams share none."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
-def _attn_shapes(q, k, v, log_decay, ndim):
-    """(batch, L, heads, kv_heads, dk, dv) of q, k and v, checked against each
-    other; L is 1 for single tokens (ndim 3)."""
+def _attn_shapes(q, k, v, ndim):
+    """(batch, L, heads, kv_heads, dk, dv) of q, k and v and their addresses,
+    checked against each other; L is 1 for single tokens (ndim 3)."""
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != ndim:
             raise ValueError(f"{name} must be (batch, {'L, ' if ndim == 4 else ''}heads, size)")
-    lead = tuple(q.shape[:-2])
-    heads, dk = q.shape[-2:]
-    kv_heads, dv = v.shape[-2:]
-    if kv_heads == 0 and heads or kv_heads and heads % kv_heads:
-        raise ValueError(f"q has {heads} heads, not a multiple of the {kv_heads} of k and v")
     dev, dt = q.device, q.dtype
+    if ndim == 4:
+        batch, seqlen, heads, dk = q.shape
+        kv_heads, dv = v.shape[2], v.shape[3]
+        kv = (batch, seqlen, kv_heads)
+    else:
+        batch, heads, dk = q.shape
+        seqlen = 1
+        kv_heads, dv = v.shape[1], v.shape[2]
+        kv = (batch, kv_heads)
+    if heads % kv_heads if kv_heads else heads:
+        raise ValueError(f"q has {heads} heads, not a multiple of the {kv_heads} of k and v")
     if dt not in _DTYPES:
         raise ValueError(f"unsupported I/O dtype {dt}")
     if dev.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
-    _need(q, "q", (*lead, heads, dk), dt, dev)
-    _need(k, "k", (*lead, kv_heads, dk), dt, dev)
-    _need(v, "v", (*lead, kv_heads, dv), dt, dev)
-    _need(log_decay, "log_decay", (heads,), torch.float32, dev)
-    return lead[0], (lead[1] if ndim == 4 else 1), heads, kv_heads, dk, dv
+    addresses = (_require(q, "q", q.shape, dt, dev), _require(k, "k", (*kv, dk), dt, dev),
+                 _require(v, "v", (*kv, dv), dt, dev))
+    return (batch, seqlen, heads, kv_heads, dk, dv), addresses
+
+
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(call, index, *sizes):
+    """Scratch bytes of a call: a function of its sizes and the GPU's kind."""
+    nbytes = ctypes.c_size_t(0)
+    _check(getattr(load_library(), call)(*sizes, ctypes.byref(nbytes)), call)
+    return nbytes.value
 
 
 def linear_attn_fwd(q, k, v, log_decay, h0=None, *, lengths=None, scale=None, return_state=True,
@@ -572,28 +626,30 @@ def linear_attn_fwd(q, k, v, log_decay, h0=None, *, lengths=None, scale=None, re
     after each row's last token; state_out may be h0. `segment_len` > 0 (a
     multiple of 64) forces the parallel segments' length."""
     lib = load_library()
-    batch, seqlen, heads, kv_heads, dk, dv = _attn_shapes(q, k, v, log_decay, 4)
+    sizes, (pq, pk, pv) = _attn_shapes(q, k, v, 4)
+    batch, seqlen, heads, _, dk, dv = sizes
     dev, dt = q.device, q.dtype
-    _need(h0, "h0", (batch, heads, dk, dv), torch.float32, dev)
-    _need(lengths, "lengths", (batch,), torch.int32, dev)
+    state = (batch, heads, dk, dv)
+    pg = _must(log_decay, "log_decay", (heads,), torch.float32, dev)
+    p0 = _require(h0, "h0", state, torch.float32, dev)
+    pl = _require(lengths, "lengths", (batch,), torch.int32, dev)
     o = out if out is not None else torch.empty(batch, seqlen, heads, dv, dtype=dt, device=dev)
-    _need(o, "out", (batch, seqlen, heads, dv), dt, dev)
-    hL = None
+    po = _require(o, "out", (batch, seqlen, heads, dv), dt, dev)
+    hL = ph = None
     if return_state:
-        hL = state_out if state_out is not None else torch.empty(batch, heads, dk, dv,
-                                                                 dtype=torch.float32, device=dev)
-        _need(hL, "state_out", (batch, heads, dk, dv), torch.float32, dev)
-    with torch.cuda.device(dev):
-        nbytes = ctypes.c_size_t(0)
-        _check(lib.linear_attn_fwd_workspace_size(batch, seqlen, heads, kv_heads, dk, dv,
-                                                  _DTYPES[dt], segment_len, ctypes.byref(nbytes)),
-               "linear_attn_fwd_workspace_size")
-        ws = _scratch(dev, nbytes.value)
-        st = lib.linear_attn_fwd(batch, seqlen, heads, kv_heads, dk, dv, _DTYPES[dt], _ptr(q),
-                                 _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(h0),
-                                 dk ** -0.5 if scale is None else scale, _ptr(o), _ptr(hL),
-                                 segment_len, _ptr(ws), nbytes.value, _stream(dev))
-    _check(st, "linear_attn_fwd")
+        hL = state_out if state_out is not None else torch.empty(state, dtype=torch.float32,
+                                                                 device=dev)
+        ph = _require(hL, "state_out", state, torch.float32, dev)
+    code = _DTYPES[dt]
+    with _on(dev):
+        nbytes = _scratch_bytes("linear_attn_fwd_workspace_size", dev.index, *sizes, code,
+                                segment_len)
+        ws = _scratch(dev, nbytes)
+        st = lib.linear_attn_fwd(*sizes, code, pq, pk, pv, pg, pl, p0,
+                                 dk ** -0.5 if scale is None else scale, po, ph, segment_len,
+                                 None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "linear_attn_fwd")
     return o, hL
 
 
@@ -604,31 +660,31 @@ def linear_attn_bwd(q, k, v, log_decay, h0=None, *, do, dhL=None, lengths=None, 
     a row's length); dlog_decay (heads,) fp32 and dh0 (batch, heads, dk, dv)
     fp32, None when not wanted."""
     lib = load_library()
-    batch, seqlen, heads, kv_heads, dk, dv = _attn_shapes(q, k, v, log_decay, 4)
+    sizes, (pq, pk, pv) = _attn_shapes(q, k, v, 4)
+    batch, seqlen, heads, _, dk, dv = sizes
     dev, dt = q.device, q.dtype
-    _need(h0, "h0", (batch, heads, dk, dv), torch.float32, dev)
-    _need(lengths, "lengths", (batch,), torch.int32, dev)
-    if do is None:
-        raise ValueError("do (the gradient at the output) is required")
-    _need(do, "do", (batch, seqlen, heads, dv), dt, dev)
-    _need(dhL, "dhL", (batch, heads, dk, dv), torch.float32, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
+    state = (batch, heads, dk, dv)
+    pg = _must(log_decay, "log_decay", (heads,), torch.float32, dev)
+    p0 = _require(h0, "h0", state, torch.float32, dev)
+    pl = _require(lengths, "lengths", (batch,), torch.int32, dev)
+    pdo = _must(do, "do", (batch, seqlen, heads, dv), dt, dev)
+    pdh = _require(dhL, "dhL", state, torch.float32, dev)
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-             dlog_decay=torch.empty(heads, **f32) if want_dlog_decay else None,
-             dh0=torch.empty(batch, heads, dk, dv, **f32) if want_dh0 else None)
-    with torch.cuda.device(dev):
-        nbytes = ctypes.c_size_t(0)
-        _check(lib.linear_attn_bwd_workspace_size(batch, seqlen, heads, kv_heads, dk, dv,
-                                                  _DTYPES[dt], segment_len, ctypes.byref(nbytes)),
-               "linear_attn_bwd_workspace_size")
-        ws = _scratch(dev, nbytes.value)
-        st = lib.linear_attn_bwd(batch, seqlen, heads, kv_heads, dk, dv, _DTYPES[dt], _ptr(q),
-                                 _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(h0),
-                                 dk ** -0.5 if scale is None else scale, _ptr(do), _ptr(dhL),
-                                 _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
-                                 _ptr(g["dlog_decay"]), _ptr(g["dh0"]), segment_len, _ptr(ws),
-                                 nbytes.value, _stream(dev))
-    _check(st, "linear_attn_bwd")
+             dlog_decay=(torch.empty(heads, dtype=torch.float32, device=dev) if want_dlog_decay
+                         else None),
+             dh0=torch.empty(state, dtype=torch.float32, device=dev) if want_dh0 else None)
+    code = _DTYPES[dt]
+    with _on(dev):
+        nbytes = _scratch_bytes("linear_attn_bwd_workspace_size", dev.index, *sizes, code,
+                                segment_len)
+        ws = _scratch(dev, nbytes)
+        st = lib.linear_attn_bwd(*sizes, code, pq, pk, pv, pg, pl, p0,
+                                 dk ** -0.5 if scale is None else scale, pdo, pdh,
+                                 *(None if t is None else t.data_ptr() for t in g.values()),
+                                 segment_len, None if ws is None else ws.data_ptr(), nbytes,
+                                 _raw_stream(dev))
+    if st:
+        _check(st, "linear_attn_bwd")
     return g
 
 
@@ -637,23 +693,22 @@ def linear_attn_update(h, q, k, v, log_decay, *, scale=None, out=None):
     in place; q (batch, heads, dk), k, v (batch, kv_heads, dk or dv); returns o
     (batch, heads, dv)."""
     lib = load_library()
-    batch, _, heads, kv_heads, dk, dv = _attn_shapes(q, k, v, log_decay, 3)
+    (batch, _, heads, kv_heads, dk, dv), (pq, pk, pv) = _attn_shapes(q, k, v, 3)
     dev, dt = q.device, q.dtype
-    if h is None:
-        raise ValueError("h (the state) is required")
-    _need(h, "h", (batch, heads, dk, dv), torch.float32, dev)
+    ph = _must(h, "h", (batch, heads, dk, dv), torch.float32, dev)
+    pg = _must(log_decay, "log_decay", (heads,), torch.float32, dev)
     o = out if out is not None else torch.empty(batch, heads, dv, dtype=dt, device=dev)
-    _need(o, "out", (batch, heads, dv), dt, dev)
-    with torch.cuda.device(dev):
-        st = lib.linear_attn_update(batch, heads, kv_heads, dk, dv, _DTYPES[dt], _ptr(h), _ptr(q),
-                                    _ptr(k), _ptr(v), _ptr(log_decay),
-                                    dk ** -0.5 if scale is None else scale, _ptr(o), _stream(dev))
-    _check(st, "linear_attn_update")
+    po = _require(o, "out", (batch, heads, dv), dt, dev)
+    with _on(dev):
+        st = lib.linear_attn_update(batch, heads, kv_heads, dk, dv, _DTYPES[dt], ph, pq, pk, pv, pg,
+                                    dk ** -0.5 if scale is None else scale, po, _raw_stream(dev))
+    if st:
+        _check(st, "linear_attn_update")
     return o
 
 
-def _norm_shapes(x, weight, groups):
-    """(rows, dim) of x, checked with the parameters."""
+def _norm_shapes(x, groups):
+    """(rows, dim) of x, and its address."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 1:
@@ -663,11 +718,10 @@ def _norm_shapes(x, weight, groups):
         raise ValueError(f"{dim} channels do not split into {groups} groups")
     if x.dtype not in _DTYPES:
         raise ValueError(f"unsupported I/O dtype {x.dtype}")
-    if x.device.type != "cuda":
+    dev = x.device
+    if dev.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
-    _need(x, "x", x.shape, x.dtype, x.device)
-    _need(weight, "weight", (dim,), torch.float32, x.device)
-    return x.numel() // dim if dim else 0, dim
+    return x.numel() // dim if dim else 0, dim, _require(x, "x", x.shape, x.dtype, dev)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out=None):
@@ -676,17 +730,19 @@ def layer_norm_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out=None):
     weight and bias (dim,) fp32. Returns (y, mean, rstd), mean and rstd
     (..., groups) fp32, which layer_norm_bwd takes; out may be x."""
     lib = load_library()
-    rows, dim = _norm_shapes(x, weight, groups)
+    rows, dim, px = _norm_shapes(x, groups)
     dev, dt = x.device, x.dtype
-    _need(bias, "bias", (dim,), torch.float32, dev)
+    pw = _require(weight, "weight", (dim,), torch.float32, dev)
+    pb = _require(bias, "bias", (dim,), torch.float32, dev)
     y = out if out is not None else torch.empty_like(x)
-    _need(y, "out", x.shape, dt, dev)
+    py = _require(y, "out", x.shape, dt, dev)
     mean = torch.empty(*x.shape[:-1], groups, dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
-    with torch.cuda.device(dev):
-        st = lib.layer_norm_fwd(rows, dim, groups, _DTYPES[dt], _ptr(x), _ptr(weight), _ptr(bias),
-                                eps, _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev))
-    _check(st, "layer_norm_fwd")
+    with _on(dev):
+        st = lib.layer_norm_fwd(rows, dim, groups, _DTYPES[dt], px, pw, pb, eps, py, mean.data_ptr(),
+                                rstd.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "layer_norm_fwd")
     return y, mean, rstd
 
 
@@ -696,27 +752,25 @@ def layer_norm_bwd(x, weight, mean, rstd, *, dy, groups=1, want_dbias=True, out=
     dweight (dim,) fp32 (None without a weight) and dbias (dim,) fp32 (None
     when not wanted)."""
     lib = load_library()
-    rows, dim = _norm_shapes(x, weight, groups)
+    rows, dim, px = _norm_shapes(x, groups)
     dev, dt = x.device, x.dtype
-    for t, name in ((mean, "mean"), (rstd, "rstd"), (dy, "dy")):
-        if t is None:
-            raise ValueError(f"{name} is required")
-    _need(mean, "mean", (*x.shape[:-1], groups), torch.float32, dev)
-    _need(rstd, "rstd", (*x.shape[:-1], groups), torch.float32, dev)
-    _need(dy, "dy", x.shape, dt, dev)
+    stats = (*x.shape[:-1], groups)
+    pw = _require(weight, "weight", (dim,), torch.float32, dev)
+    pm = _must(mean, "mean", stats, torch.float32, dev)
+    pr = _must(rstd, "rstd", stats, torch.float32, dev)
+    pdy = _must(dy, "dy", x.shape, dt, dev)
     dx = out if out is not None else torch.empty_like(x)
-    _need(dx, "out", x.shape, dt, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    g = dict(dx=dx, dweight=None if weight is None else torch.empty(dim, **f32),
-             dbias=torch.empty(dim, **f32) if want_dbias else None)
-    with torch.cuda.device(dev):
-        nbytes = ctypes.c_size_t(0)
-        _check(lib.layer_norm_bwd_workspace_size(rows, dim, groups, _DTYPES[dt],
-                                                 ctypes.byref(nbytes)),
-               "layer_norm_bwd_workspace_size")
-        ws = _scratch(dev, nbytes.value)
-        st = lib.layer_norm_bwd(rows, dim, groups, _DTYPES[dt], _ptr(x), _ptr(weight), _ptr(mean),
-                                _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(g["dweight"]),
-                                _ptr(g["dbias"]), _ptr(ws), nbytes.value, _stream(dev))
-    _check(st, "layer_norm_bwd")
-    return g
+    pdx = _require(dx, "out", x.shape, dt, dev)
+    dw = None if weight is None else torch.empty(dim, dtype=torch.float32, device=dev)
+    db = torch.empty(dim, dtype=torch.float32, device=dev) if want_dbias else None
+    code = _DTYPES[dt]
+    with _on(dev):
+        nbytes = _scratch_bytes("layer_norm_bwd_workspace_size", dev.index, rows, dim, groups, code)
+        ws = _scratch(dev, nbytes)
+        st = lib.layer_norm_bwd(rows, dim, groups, code, px, pw, pm, pr, pdy, pdx,
+                                None if dw is None else dw.data_ptr(),
+                                None if db is None else db.data_ptr(),
+                                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "layer_norm_bwd")
+    return dict(dx=dx, dweight=dw, dbias=db)

@@ -6,7 +6,6 @@
 #include <hip/hip_runtime_api.h>
 
 #include <math.h>
-#include <stdlib.h>
 #include <stdint.h>
 
 #include "internal.h"
@@ -57,13 +56,53 @@ int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, i
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The automatic division. Segments add a pass over keys and values and a
+// join, so a sequence is cut only where its chunks, walked one after the other,
+// would leave the chip idle. The time of a plan with n segments is taken as
+//     chunks / n * chunk * load(w) * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
+// with w the workgroups per compute unit: `chunk` the time of 64 tokens alone on
+// a unit, load what sharing one costs (two workgroups take 1.57 times as long as
+// one; the wide kernels, one to a unit, take turns), `summary` the states'
+// pass, join its launches. Microseconds measured on MI355X with one workgroup
+// per unit; examples, cut by this rule against not cut: one sequence of 65536,
+// 16 heads of 128: 349 us with 16 segments against 411 with 8 and 2.9 ms; 8 x
+// 2048 x 16 heads of 128: 76 us whole against 102 with 2; 4 x 1024 x 16 heads
+// of 64: 25 us whole against 29; gradients of 2 x 333 x 6 heads in fp32: 42 us
+// with 3 against 58 whole.
+struct PlanCost {
+    double chunk[2][3];   // [fp32, bf16][head width 64, 128, 256]
+    double summary;
+};
+constexpr PlanCost kFwdCost = {{{4.4, 8.0, 19.0}, {1.5, 2.3, 3.8}}, 0.5};
+constexpr PlanCost kBwdCost = {{{6.3, 11.0, 21.0}, {3.0, 4.1, 9.0}}, 0.35};
+constexpr double kJoinCost = 14.0;
+constexpr int64_t kMinSegment = 64;
+
+int64_t choose_segments(const PlanCost& cost, int io, int dc_pad, int64_t seqlen, int64_t units, int cu) {
+    const double chunk = cost.chunk[io == mamba::kIoF32 ? 0 : 1][dc_pad == 64 ? 0 : (dc_pad == 128 ? 1 : 2)];
+    const double chunks = static_cast<double>(seqlen) / 64.0;
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t n = 1; n <= ceil_div(seqlen, kMinSegment) && (n == 1 || units * n <= 8 * int64_t(cu)); ++n) {
+        const double w = static_cast<double>(units * n) / cu;
+        const double load = w <= 1.0 ? 1.0 : (dc_pad == 256 ? w : (w <= 2.0 ? 1.57 : 0.785 * w));
+        double t = ceil_div(ceil_div(seqlen, n), kSegUnit) * 1.0;
+        t = (t < chunks ? t : chunks) * chunk * load;
+        if (n > 1) t = t * (1.0 + cost.summary) + kJoinCost;
+        if (n == 1 || t < least) {
+            least = t;
+            best = n;
+        }
+    }
+    return best;
+}
+
 // How a call is divided. `passes` workgroups run per (row, head, segment,
-// column block): one forward, three backward, whose widest head decides.
+// column block): one forward, three backward, whose wider head decides.
 int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, LinPlan* p) {
-    const int64_t wide = passes == 1 ? c.dv : (c.dk > c.dv ? c.dk : c.dv);
-    const int64_t deep = passes == 1 ? c.dk : wide;
-    p->block_cols = wide > 64 ? 128 : 64;
-    if(getenv("LIN_COLS"))p->block_cols=atoi(getenv("LIN_COLS"));
+    const int wide = passes == 1 ? c.dv : (c.dk > c.dv ? c.dk : c.dv);
+    const int dc_pad = mamba::lin_padded(passes == 1 ? c.dk : wide);
+    const int64_t blocks = mamba::lin_blocks(dc_pad, wide);
     p->seg_len = c.seqlen > 0 ? c.seqlen : 1;
     p->nseg = 1;
     if (c.batch == 0 || c.heads == 0 || c.seqlen == 0) return MAMBA_OK;
@@ -72,11 +111,9 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
         int cu = 0;
         const int st = mamba::current_cu_count(&cu);
         if (st != MAMBA_OK) return st;
-        const int64_t units = c.batch * c.heads * ceil_div(wide, p->block_cols) * passes;
-        int64_t n = (2 * int64_t(cu)) / units;
-        const int64_t most = c.seqlen / 256;
-        if (n > most) n = most;
-        seg = n >= 2 ? ceil_div(ceil_div(c.seqlen, n), kSegUnit) * kSegUnit : c.seqlen;
+        const int64_t n = choose_segments(passes == 1 ? kFwdCost : kBwdCost, c.io, dc_pad, c.seqlen,
+                                          c.batch * c.heads * blocks * passes, cu);
+        seg = n > 1 ? ceil_div(ceil_div(c.seqlen, n), kSegUnit) * kSegUnit : c.seqlen;
     }
     if (seg < c.seqlen) {
         const int64_t n = ceil_div(c.seqlen, seg);
@@ -84,8 +121,7 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
         p->seg_len = seg;
         p->nseg = static_cast<int>(n);
     }
-    const int64_t blocks = c.batch * c.heads * p->nseg;
-    if (blocks > kMaxBlocks / (passes * ceil_div(wide, p->block_cols))) return MAMBA_ERR_UNSUPPORTED;
+    if (c.batch * c.heads * p->nseg > kMaxBlocks / (passes * blocks)) return MAMBA_ERR_UNSUPPORTED;
     // and a block per window of the decay's gradient
     if (passes > 1 && c.batch * c.heads > kMaxBlocks / (c.seqlen / mamba::kLinWindow + p->nseg + 1))
         return MAMBA_ERR_UNSUPPORTED;

@@ -165,6 +165,13 @@ hipError_t launch_ssd_fwd(const SsdArgs& a, hipStream_t stream);
 constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
 constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;   // passes of the backward launch
 constexpr int kLinMaxDim = 256;   // widest head
+// Waves of a workgroup and output columns of a wave. 64 columns leave two
+// workgroups on a compute unit (prompts of 8 x 2048 x 16 heads of 128: 76 us
+// against 95 us with 128 columns, their gradients 313 against 326); the wide
+// kernels' registers and LDS leave one, of 128 columns then (2 x 2048 x 8 heads
+// of 200 x 168: 55 us against 62 us with 64, gradients 175 against 194).
+constexpr int lin_waves(int dc_pad) { return dc_pad == 256 ? 8 : 4; }
+constexpr int kLinCols = 16;
 // Tokens of a chunk: fp32 takes half in the same LDS.
 constexpr int kLinChunkBF16 = 64, kLinChunkF32 = 32;
 // Tokens of a window of the decay's gradient: a state and an adjoint of dk x
@@ -209,7 +216,7 @@ struct LinArgs {
 };
 
 template <int IO, int MODE>
-hipError_t launch_linear_attn_variant(const LinArgs& a, int dc_pad, int block_cols, hipStream_t s);
+hipError_t launch_linear_attn_variant(const LinArgs& a, int dc_pad, hipStream_t s);
 
 // A call of linear attention; the backward's outputs are set for its
 // launches only.
@@ -230,13 +237,17 @@ struct LinearAttnCall {
 };
 
 // Division of a call over the GPU: segments of seg_len tokens (nseg == 1:
-// none) and output columns per workgroup.
+// none).
 struct LinPlan {
     int64_t seg_len = 0;
     int nseg = 1;
-    int block_cols = 64;
-    size_t workspace_bytes = 0;
 };
+
+// Head width the kernels are built for, and column blocks of `out` columns.
+constexpr int lin_padded(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
+constexpr int lin_blocks(int dc_pad, int out) {
+    return (out + lin_waves(dc_pad) * kLinCols - 1) / (lin_waves(dc_pad) * kLinCols);
+}
 
 size_t linear_attn_workspace_bytes(const LinearAttnCall& c, const LinPlan& p, bool bwd);
 hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s);

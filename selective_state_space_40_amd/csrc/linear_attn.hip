@@ -226,8 +226,6 @@ hipError_t launch_update_io(const LinUpdateArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-int padded(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
-
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The backward call's scratch, in order: each part 256-byte aligned.
@@ -256,6 +254,8 @@ BwdScratch bwd_scratch(const LinearAttnCall& c, const LinPlan& p, int nblk) {
 }
 
 int max_dim(const LinearAttnCall& c) { return c.dk > c.dv ? c.dk : c.dv; }
+
+int bwd_blocks(const LinearAttnCall& c) { return lin_blocks(lin_padded(max_dim(c)), max_dim(c)); }
 
 LinArgs base_args(const LinearAttnCall& c, const LinPlan& p) {
     LinArgs a = {};
@@ -292,9 +292,9 @@ LinPass forward_pass(const LinearAttnCall& c) {
 }
 
 template <int MODE>
-hipError_t launch_mode(const LinearAttnCall& c, const LinArgs& a, int dc, int cols, hipStream_t s) {
-    return c.io == kIoF32 ? launch_linear_attn_variant<kIoF32, MODE>(a, padded(dc), cols, s)
-                          : launch_linear_attn_variant<kIoBF16, MODE>(a, padded(dc), cols, s);
+hipError_t launch_mode(const LinearAttnCall& c, const LinArgs& a, int dc_pad, hipStream_t s) {
+    return c.io == kIoF32 ? launch_linear_attn_variant<kIoF32, MODE>(a, dc_pad, s)
+                          : launch_linear_attn_variant<kIoBF16, MODE>(a, dc_pad, s);
 }
 
 hipError_t launch_join(const LinearAttnCall& c, const LinPlan& p, float* seg_s, float* seg_d,
@@ -331,27 +331,27 @@ hipError_t launch_share(const LinearAttnCall& c, int dim, const float* part, voi
 }  // namespace
 
 size_t linear_attn_workspace_bytes(const LinearAttnCall& c, const LinPlan& p, bool bwd) {
-    if (bwd) return bwd_scratch(c, p, (max_dim(c) + p.block_cols - 1) / p.block_cols).total;
+    if (bwd) return bwd_scratch(c, p, bwd_blocks(c)).total;
     return p.nseg > 1 ? static_cast<size_t>(c.batch) * c.heads * p.nseg * c.dk * c.dv * 4 : 0;
 }
 
 hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s) {
     LinArgs a = base_args(c, p);
-    a.nblk = (c.dv + p.block_cols - 1) / p.block_cols;
+    a.nblk = lin_blocks(lin_padded(c.dk), c.dv);
     a.pass[0] = forward_pass(c);
     a.pass[0].seg_in = static_cast<float*>(ws);
     if (p.nseg > 1) {
-        hipError_t e = launch_mode<kLinState>(c, a, c.dk, p.block_cols, s);
+        hipError_t e = launch_mode<kLinState>(c, a, lin_padded(c.dk), s);
         if (e != hipSuccess) return e;
         e = launch_join(c, p, static_cast<float*>(ws), nullptr, s);
         if (e != hipSuccess) return e;
     }
-    return launch_mode<kLinFwd>(c, a, c.dk, p.block_cols, s);
+    return launch_mode<kLinFwd>(c, a, lin_padded(c.dk), s);
 }
 
 hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s) {
-    const int wide = max_dim(c);
-    const int nblk = (wide + p.block_cols - 1) / p.block_cols;
+    const int dc_pad = lin_padded(max_dim(c));
+    const int nblk = bwd_blocks(c);
     const BwdScratch w = bwd_scratch(c, p, nblk);
     char* base = static_cast<char*>(ws);
     float* seg_s = p.nseg > 1 ? reinterpret_cast<float*>(base + w.seg_s) : nullptr;
@@ -390,12 +390,12 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         adj.out32 = shared;
         if (p.nseg > 1) {
             LinArgs a = base_args(c, p);
-            a.nblk = (c.dv + p.block_cols - 1) / p.block_cols;
+            a.nblk = lin_blocks(lin_padded(c.dk), c.dv);
             a.npass = 2;
             a.exact = dg != nullptr;
             a.pass[0] = states;
             a.pass[1] = adj;
-            e = launch_mode<kLinState>(c, a, c.dk, p.block_cols, s);
+            e = launch_mode<kLinState>(c, a, lin_padded(c.dk), s);
             if (e != hipSuccess) return e;
             e = launch_join(c, p, seg_s, seg_d, s);
             if (e != hipSuccess) return e;
@@ -436,7 +436,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         k.sp = c.dv;
         k.dc = c.dv;
         k.dout = c.dk;
-        e = launch_mode<kLinBwd>(c, a, wide, p.block_cols, s);
+        e = launch_mode<kLinBwd>(c, a, dc_pad, s);
         if (e != hipSuccess) return e;
         if (shared) {
             e = launch_share(c, c.dk, part_k, c.d_k, s);

@@ -16,8 +16,8 @@
 //                (k, q, do) -> dv, adjoint dS, reversed
 //                (v, do, q) -> dk, adjoint dS^T, reversed
 //
-// Work mapping. A workgroup of 4 or 8 waves walks the chunks of one (row, head,
-// segment) for a block of 64 or 128 output columns; wave w owns 16 of them. The
+// Work mapping. A workgroup of 4 waves (8 for keys wider than 128) walks the
+// chunks of one (row, head, segment) for 16 output columns per wave. The
 // state's columns belong to the same wave, so its S (all DC rows, 16 columns)
 // stays in the accumulators for the whole walk, and the accumulator of two
 // 16 x 16 blocks is, up to a fixed order of the rows, the operand of the
@@ -50,18 +50,15 @@ typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLinCols = 16;   // output columns of a wave
 
 struct F32x8 {
     float v[8];
 };
 
-// A fragment holds, in lane (c, g) = (lane % 16, lane / 16), 8 of the 32
-// values that one row or column c of an operand contributes to a product:
-// nat() the values 8 g + e, perm() 4 g + e and 16 + 4 g + (e - 4), the order
-// in which two accumulator blocks hold them. Both operands of a product use
-// the same order. The fp32 instruction contracts 4 values at a time, value e
-// of the four lane groups in step e.
+// A fragment holds, in lane (c, g) = (lane % 16, lane / 16), the values 8 g + e
+// (e < 8) of the 32 that one row or column c of an operand contributes to a
+// product. The fp32 instruction contracts 4 values at a time, value e of the
+// four lane groups in step e.
 template <int IO>
 struct LinOps;
 
@@ -72,38 +69,24 @@ struct LinOps<kIoBF16> {
     static constexpr bool kSplit = true;    // fp32 values enter as bf16 terms
     static constexpr int kChunk = kLinChunkBF16;
     // LDS row padding (elements). Cycles of a CU per wave's read, measured:
-    // whole fragments of 16 rows (nat) 4 with 32 bytes, 8 with 16 and 32
-    // without; the transpose read 4 with either. P's rows, written 8 bytes a
-    // lane and read whole, take 8 and 8 with 16 bytes, 16 and 4 with 32.
-    static constexpr int kPad = 16, kPadP = 8;
+    // whole fragments of 16 rows (nat) 4 with 32 bytes, 8 with 16 or 64, 32
+    // without; the transpose read 4 with any, 8 with columns 8 apart and 32
+    // bytes, 4 with those and 64. P's rows, written 8 bytes a lane and read
+    // whole, take 8 and 8 with 16 bytes, 16 and 4 with 32.
+    static constexpr int kPad = 16, kPadK = 32, kPadP = 8;
 
     static __device__ __forceinline__ Frag nat(const T* row, int g) {
         return *reinterpret_cast<const bf16x8*>(row + 8 * g);
-    }
-    // The two halves are read on their own, from addresses that the compiler
-    // does not see to be 32 bytes apart: one ds_read2_b64 for both takes 32
-    // cycles where these take 4 each.
-    static __device__ __forceinline__ Frag perm(const T* lo, const T* hi) {
-        const bf16x4 a = *reinterpret_cast<const bf16x4*>(lo);
-        const bf16x4 b = *reinterpret_cast<const bf16x4*>(hi);
-        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-    // perm() from a tile staged in that order: a thread's 16 bytes, 8 values at
-    // 8 m of a row, go as two halves to where their fragments have them
-    static __device__ __forceinline__ Frag packed(const T* row, int g) { return nat(row, g); }
-    static __device__ __forceinline__ void pack(T* row, int m, uint4 x) {
-        T* p = row + 32 * (m >> 2) + 16 * (m & 1) + 4 * ((m >> 1) & 1);
-        *reinterpret_cast<uint2*>(p) = make_uint2(x.x, x.y);
-        *reinterpret_cast<uint2*>(p + 8) = make_uint2(x.z, x.w);
     }
     // 8 rows r0 + 8 g + e of column c0 + c of a row-major tile: the LDS
     // transpose read (ds_read_b64_tr_b16). Within each group of 16 lanes,
     // lane r receives as element e the element (r mod 4) of the 8 bytes that
     // lane 4 e + r / 4 of its group addresses, so lane s of the group
-    // addresses row s / 4, columns 4 (s mod 4) .. + 3 of a 4 x 16 block.
-    template <int RS>
+    // addresses row s / 4, columns 4 (s mod 4) .. + 3 of a 4 x 16 block; with
+    // STEP 8 the four groups of 4 columns are 8 apart.
+    template <int RS, int STEP>
     static __device__ __forceinline__ Frag tr(const T* tile, int r0, int c0, int c, int g) {
-        const T* p = tile + (r0 + 8 * g + (c >> 2)) * RS + c0 + 4 * (c & 3);
+        const T* p = tile + (r0 + 8 * g + (c >> 2)) * RS + c0 + STEP * (c & 3);
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(const_cast<T*>(p)));
         const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -146,7 +129,7 @@ struct LinOps<kIoF32> {
     typedef F32x8 Frag;
     static constexpr bool kSplit = false;
     static constexpr int kChunk = kLinChunkF32;
-    static constexpr int kPad = 4, kPadP = 4;
+    static constexpr int kPad = 4, kPadK = 4, kPadP = 4;
 
     static __device__ __forceinline__ Frag pair(const float* a, const float* b) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(a), y = *reinterpret_cast<const f32x4*>(b);
@@ -155,19 +138,12 @@ struct LinOps<kIoF32> {
     static __device__ __forceinline__ Frag nat(const T* row, int g) {
         return pair(row + 8 * g, row + 8 * g + 4);
     }
-    static __device__ __forceinline__ Frag perm(const T* lo, const T* hi) { return pair(lo, hi); }
-    // fp32 halves of a fragment are 16 bytes in any order
-    static __device__ __forceinline__ Frag packed(const T* row, int g) {
-        return pair(row + 4 * g, row + 16 + 4 * g);
-    }
-    static __device__ __forceinline__ void pack(T* row, int m, uint4 x) {
-        *reinterpret_cast<uint4*>(row + 4 * m) = x;
-    }
-    template <int RS>
+    template <int RS, int STEP>
     static __device__ __forceinline__ Frag tr(const T* tile, int r0, int c0, int c, int g) {
         Frag f;
+        const T* p = tile + (r0 + 8 * g) * RS + c0 + STEP * (c >> 2) + (c & 3);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f.v[e] = tile[(r0 + 8 * g + e) * RS + c0 + c];
+        for (int e = 0; e < 8; ++e) f.v[e] = p[e * RS];
         return f;
     }
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 acc) {
@@ -249,21 +225,16 @@ struct Tile {
 #pragma unroll
         for (int u = 0; u < COUNT; ++u) *reinterpret_cast<uint4*>(p + u * ROWS * kRow) = r[u];
     }
-    // in the order of packed()
-    __device__ __forceinline__ void stage_packed(T* lds) const {
-        T* p = lds + threadIdx.x / VPR * kRow;
-#pragma unroll
-        for (int u = 0; u < COUNT; ++u) LinOps<IO>::pack(p + u * ROWS * kRow, threadIdx.x % VPR, r[u]);
-    }
 };
 
-template <int IO, int DC, int WAVES, int MODE>
+template <int IO, int DC, int MODE>
 struct LinLds {
+    static constexpr int WAVES = lin_waves(DC);
     typedef typename LinOps<IO>::T T;
     static constexpr int kC = LinOps<IO>::kChunk;
     static constexpr int kRowP = kC + LinOps<IO>::kPadP;
     static constexpr int kThreads = WAVES * kWave, kCols = WAVES * kLinCols;
-    typedef Tile<IO, kThreads, DC, LinOps<IO>::kPad> TileK;
+    typedef Tile<IO, kThreads, DC, LinOps<IO>::kPadK> TileK;
     typedef Tile<IO, kThreads, kCols, LinOps<IO>::kPad> TileV;
     typedef Tile<IO, kThreads, DC, LinOps<IO>::kPad> TileQ;
     typedef Tile<IO, kThreads, kCols, LinOps<IO>::kPad> TileX;
@@ -303,6 +274,9 @@ __device__ __forceinline__ float decay_power(float g, int n) {
     return (x > 0.0f && x < __builtin_inff()) ? fmaf(x, e, x) : x;
 }
 
+// The first of the 4 state rows that lane group g holds in block nt.
+__device__ __forceinline__ int state_row(int nt, int g) { return 32 * (nt >> 1) + 8 * g + 4 * (nt & 1); }
+
 // xcd_contiguous_block in 32 bits.
 __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
     constexpr uint32_t X = kXcds;
@@ -310,8 +284,8 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
     return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
-template <int IO, int DC, int WAVES, int MODE>
-__global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a) {
+template <int IO, int DC, int MODE>
+__global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(LinArgs a) {
     typedef LinOps<IO> O;
     typedef typename O::T T;
     typedef typename O::Frag Frag;
@@ -319,10 +293,11 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
     constexpr int NT = C / 16;            // blocks of 16 tokens
     constexpr int NS = C / 32;            // product steps over tokens
     constexpr int NN = DC / 16;           // blocks of 16 state rows
+    constexpr int WAVES = lin_waves(DC);
     constexpr int DOB = WAVES * kLinCols; // columns per workgroup
     constexpr int THREADS = WAVES * kWave;
     constexpr bool kState = MODE == kLinState, kBwd = MODE == kLinBwd;
-    typedef LinLds<IO, DC, WAVES, MODE> Lds;
+    typedef LinLds<IO, DC, MODE> Lds;
     constexpr int RK = Lds::TileK::kRow, RV = Lds::TileV::kRow, RQ = Lds::TileQ::kRow, RX = Lds::TileX::kRow;
     __shared__ Lds lds;
 
@@ -421,7 +396,9 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
         fetch_vx(first, cnt);
     }
 
-    // S: block nt holds rows n = 16 nt + 4 g + v of column p0 + 16 w + c
+    // S: block nt holds rows state_row(nt, g) + v of column p0 + 16 w + c, so
+    // that blocks 2 k and 2 k + 1 of a lane are the rows 32 k + 8 g + 0..7 of a
+    // fragment
     const int pc = p0 + kLinCols * w + c;
     const int64_t state_elems = static_cast<int64_t>(dc) * dout;
     const int state_bytes = dc * dout * 4;
@@ -433,9 +410,9 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
     const bool runs = kBwd && sn == 1;   // a block's 4 rows lie together (transposed state)
     // dc is a multiple of 4: a block's 4 rows are all in or all out
     auto state_offset = [&](int nt) {
-        const int n = 16 * nt + 4 * g;
+        const int n = state_row(nt, g);
         const int off = (n * sn + pc * sp) * 4;
-        return (n < dc) & (pc < dout) ? off : kPastEnd;
+        return ((n < dc) & (pc < dout)) ? off : kPastEnd;
     };
     // f(nt, block) over a state in memory, zeros outside it
     auto load_state = [&](const float* from, auto f) {
@@ -472,10 +449,6 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
     constexpr int GR = WAVES / NT, OWN = NT > GR ? NT / GR : 1;
     const int jt = w % NT, grp = w / NT;
     const bool forms = grp < NT;
-    const T* klo = lds.K + (16 * jt + c) * RK + 4 * g;
-    int apart = 16;
-    asm volatile("" : "+v"(apart));
-    const T* khi = klo + apart;
     float fac[OWN][4], eo[NT];
     if constexpr (!kState) {
 #pragma unroll
@@ -528,6 +501,20 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
         }
     };
 
+    // the weights of a chunk's tokens in the state update; they change with
+    // the one chunk that may be short only
+    auto weigh = [&](int cnt) {
+        if (tid < C) lds.W[tid] = tid < cnt ? ps.state_scale * lds.pow[cnt - 1 - tid + r] : 0.0f;
+    };
+    int wcnt;
+    {
+        int64_t first;
+        chunk_at(0, first, wcnt);
+        weigh(wcnt);
+    }
+    // the state is waited for here, not at its uses in the loop
+#pragma unroll
+    for (int nt = 0; nt < NN; ++nt) asm volatile("" : "+v"(S[nt]));
     if constexpr (!kState) {
         // as many stores before the first chunk as a chunk issues (dropped, past
         // the end of an empty range): the waits for a chunk's loads then
@@ -545,10 +532,13 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
         chunk_at(ch, first, cnt);
         // (1) stage. The tiles' last readers passed the barrier before P V.
         tk.stage(lds.K);
-        if constexpr (!kState) tq.stage_packed(lds.Q);
+        if constexpr (!kState) tq.stage(lds.Q);
         tv.stage(lds.V);
         if constexpr (kBwd) tx.stage(lds.X);
-        if (tid < C) lds.W[tid] = tid < cnt ? ps.state_scale * lds.pow[cnt - 1 - tid + r] : 0.0f;
+        if (cnt != wcnt) {
+            wcnt = cnt;
+            weigh(cnt);
+        }
         __syncthreads();
         // the next chunk's loads go out in two groups, as the units that
         // address them take as long as a chunk's products
@@ -569,9 +559,9 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
             for (int k = 0; k < NN / 2; ++k) {
                 Frag q[NT];
 #pragma unroll
-                for (int it = 0; it < NT; ++it) q[it] = O::packed(lds.Q + (16 * it + c) * RQ + 32 * k, g);
+                for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + 32 * k, g);
                 if constexpr (GR == 1) {
-                    const Frag kf = O::perm(klo + 32 * k, khi + 32 * k);
+                    const Frag kf = O::nat(lds.K + (16 * jt + c) * RK + 32 * k, g);
 #pragma unroll
                     for (int u = 0; u < OWN; ++u) G[u] = O::mma(kf, q[u], G[u]);
                 }
@@ -595,14 +585,14 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
                 }
             }
             float dgi = 0.0f;
-            if (forms) {
+            if (GR == 1 || forms) {
                 if constexpr (GR > 1) {
 #pragma unroll
                     for (int k = 0; k < DC; k += 32) {
-                        const Frag kf = O::perm(klo + k, khi + k);
+                        const Frag kf = O::nat(lds.K + (16 * jt + c) * RK + k, g);
 #pragma unroll
                         for (int u = 0; u < OWN; ++u)
-                            G[u] = O::mma(kf, O::packed(lds.Q + (16 * (grp + GR * u) + c) * RQ + k, g), G[u]);
+                            G[u] = O::mma(kf, O::nat(lds.Q + (16 * (grp + GR * u) + c) * RQ + k, g), G[u]);
                     }
                 }
 #pragma unroll
@@ -610,8 +600,7 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
                     const int it = grp + GR * u;
                     f32x4 pv;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)   // a product above the diagonal may be non-finite: select
-                        pv[v] = 16 * (it - jt) + c >= 4 * g + v ? G[u][v] * fac[u][v] : 0.0f;
+                    for (int v = 0; v < 4; ++v) pv[v] = G[u][v] * fac[u][v];
                     O::st4(lds.P + (16 * it + c) * Lds::kRowP + 16 * jt + 4 * g, pv);
                     if constexpr (kBwd) {
                         if (ps.dg_pairs && it >= jt) {
@@ -663,7 +652,7 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
         // v as the products over tokens read it
         Frag vf[NS];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) vf[s] = O::template tr<RV>(lds.V, 32 * s, kLinCols * w, c, g);
+        for (int s = 0; s < NS; ++s) vf[s] = O::template tr<RV, 4>(lds.V, 32 * s, kLinCols * w, c, g);
 
         // (4) the state: S + (lam^cnt - 1) S, which rounds only the change (a
         // factor next to 1 applied chunk after chunk would drift by its own
@@ -688,7 +677,7 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void linear_attn_kernel(LinArgs a
             for (int n0 = 0; n0 < NN; n0 += U) {
                 Frag kf[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) kf[u] = O::template tr<RK>(lds.K, 32 * s, 16 * (n0 + u), c, g);
+                for (int u = 0; u < U; ++u) kf[u] = O::template tr<RK, 8>(lds.K, 32 * s, state_row(n0 + u, 0), c, g);
 #pragma unroll
                 for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v0, S[n0 + u]);
                 if constexpr (O::kSplit)
