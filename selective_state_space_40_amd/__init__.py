@@ -531,19 +531,18 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, h0=None, *, dt_bias=None, dt_softplu
     return y, hL
 
 
-def _fits(t, shape, dtype, index):
-    """Whether t is a contiguous tensor of this shape and dtype on GPU `index`
-    (a cheap test before _need, which says what is wrong)."""
-    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == index)
-
-
 def _require(t, name, shape, dtype, dev):
-    """The address of a tensor that _need accepts; None for None."""
+    """The address of a tensor that _need accepts; None for None. The cheap
+    test comes first, _need says what is wrong."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and _fits(t, shape, dtype, dev.index)):
-        _need(t, name, shape, dtype, dev)
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, shape, dtype, dev)
     return t.data_ptr()
 
 
@@ -568,7 +567,14 @@ class _on:
             self.guard.__exit__(*exc)
 
 
+# the current stream's handle, without the object around it where torch has a
+# function for that
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(dev):
+    if _raw_stream_of is not None:
+        return _raw_stream_of(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 

@@ -59,9 +59,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The automatic division. Segments add a pass over keys and values and a
 // join, so a sequence is cut only where its chunks, walked one after the other,
 // would leave the chip idle. The time of a plan with n segments is taken as
-//     chunks / n * chunk * load(w) * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
+//     (chunks / n * chunk + entry) * load(w) * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
 // with w the workgroups per compute unit: `chunk` the time of 64 tokens alone on
-// a unit, load what sharing one costs (two workgroups take 1.57 times as long as
+// a unit, `entry` a workgroup's beginning and end, load what sharing a unit costs (two workgroups take 1.57 times as long as
 // one; the wide kernels, one to a unit, take turns), `summary` the states'
 // pass, join its launches. Microseconds measured on MI355X with one workgroup
 // per unit; examples, cut by this rule against not cut: one sequence of 65536,
@@ -71,15 +71,17 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // with 3 against 58 whole.
 struct PlanCost {
     double chunk[2][3];   // [fp32, bf16][head width 64, 128, 256]
+    double entry[3];
     double summary;
 };
-constexpr PlanCost kFwdCost = {{{4.4, 8.0, 19.0}, {1.5, 2.3, 3.8}}, 0.5};
-constexpr PlanCost kBwdCost = {{{6.3, 11.0, 21.0}, {3.0, 4.1, 9.0}}, 0.35};
+constexpr PlanCost kFwdCost = {{{4.4, 8.0, 18.4}, {1.45, 2.3, 3.6}}, {2.0, 3.0, 9.0}, 0.5};
+constexpr PlanCost kBwdCost = {{{6.3, 11.0, 21.0}, {3.0, 4.1, 8.8}}, {2.0, 3.0, 5.0}, 0.35};
 constexpr double kJoinCost = 14.0;
 constexpr int64_t kMinSegment = 64;
 
 int64_t choose_segments(const PlanCost& cost, int io, int dc_pad, int64_t seqlen, int64_t units, int cu) {
-    const double chunk = cost.chunk[io == mamba::kIoF32 ? 0 : 1][dc_pad == 64 ? 0 : (dc_pad == 128 ? 1 : 2)];
+    const int width = dc_pad == 64 ? 0 : (dc_pad == 128 ? 1 : 2);
+    const double chunk = cost.chunk[io == mamba::kIoF32 ? 0 : 1][width];
     const double chunks = static_cast<double>(seqlen) / 64.0;
     int64_t best = 1;
     double least = 0.0;
@@ -87,7 +89,7 @@ int64_t choose_segments(const PlanCost& cost, int io, int dc_pad, int64_t seqlen
         const double w = static_cast<double>(units * n) / cu;
         const double load = w <= 1.0 ? 1.0 : (dc_pad == 256 ? w : (w <= 2.0 ? 1.57 : 0.785 * w));
         double t = ceil_div(ceil_div(seqlen, n), kSegUnit) * 1.0;
-        t = (t < chunks ? t : chunks) * chunk * load;
+        t = ((t < chunks ? t : chunks) * chunk + cost.entry[width]) * load;
         if (n > 1) t = t * (1.0 + cost.summary) + kJoinCost;
         if (n == 1 || t < least) {
             least = t;

@@ -143,53 +143,70 @@ __device__ __forceinline__ void load_params(const float* p, int64_t at, int n, i
         for (int e = 0; e < 8; ++e) v[u * 8 + e] = t.get(u, e);
 }
 
+// The forward pass. A workgroup stays with one group of columns, keeps its
+// weights in registers and walks rows slot, slot + slots, ... (times its teams),
+// the next row's loads out while one is normed: read per row, the weights'
+// fp32 values were twice a bf16 row's bytes from the L2 (16384 x 5120: 78 us).
+// The forward pass. A workgroup stays with one group of columns, keeps its
+// weights in registers and walks rows slot, slot + slots, ... (times its teams),
+// the next row's loads out while one is normed: read per row, the weights'
+// fp32 values were twice a bf16 row's bytes from the L2 (16384 x 5120: 78 us).
 template <int IO, int TEAM, int CH, bool VEC>
-__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_fwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_fwd_kernel(NormArgs a, int slots) {
     constexpr int THREADS = TEAM > 256 ? TEAM : 256;
     constexpr int TEAMS = THREADS / TEAM;
-    __shared__ float slots[2][THREADS / kWave];
-    const int lane = threadIdx.x % TEAM;
+    __shared__ float slot_sums[2][THREADS / kWave];
+    typedef Part<IO, TEAM, CH, VEC> P;
+    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const int n = static_cast<int>(a.dim / a.groups);
-    const int64_t parts = a.rows * a.groups;
-    const int64_t part = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
-    const bool in = part < parts;
-    const int64_t at = in ? part * n : 0;
-    const int m = in ? n : 0;
-    Part<IO, TEAM, CH, VEC> x;
-    x.load(a.x, at, m, lane);
-    float v[CH * 8];
-    float sum[1] = {0.0f};
-#pragma unroll
-    for (int u = 0; u < CH; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[u * 8 + e] = x.get(u, e);
-            sum[0] += v[u * 8 + e];
-        }
-    team_sum<TEAM>(sum, slots[0]);
-    const float mean = sum[0] / static_cast<float>(n);
-    float sq[1] = {0.0f};
-#pragma unroll
-    for (int u = 0; u < CH; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool have = Part<IO, TEAM, CH, VEC>::index(lane, u, e) < n;
-            float& t = v[u * 8 + e];
-            t = have ? t - mean : 0.0f;
-            sq[0] = fmaf(t, t, sq[0]);
-        }
-    team_sum<TEAM>(sq, slots[1]);
-    const float rstd = 1.0f / sqrtf(sq[0] / static_cast<float>(n) + a.eps);
-    const int64_t col = part % a.groups * n;
+    const int64_t grp = blockIdx.x % a.groups;
+    const int64_t slot = blockIdx.x / a.groups;
+    const float inv = 1.0f / static_cast<float>(n);
     float wt[CH * 8], bs[CH * 8];
-    load_params<TEAM, CH, VEC>(a.weight, col, m, lane, 1.0f, wt);
-    load_params<TEAM, CH, VEC>(a.bias, col, m, lane, 0.0f, bs);
+    load_params<TEAM, CH, VEC>(a.weight, grp * n, n, lane, 1.0f, wt);
+    load_params<TEAM, CH, VEC>(a.bias, grp * n, n, lane, 0.0f, bs);
+    const int64_t step = static_cast<int64_t>(slots) * TEAMS;
+    P x;
+    auto fetch = [&](int64_t row) {
+        const bool in = row < a.rows;
+        x.load(a.x, in ? (row * a.groups + grp) * n : 0, in ? n : 0, lane);
+    };
+    fetch(slot * TEAMS + team);
+    // every team of the workgroup takes the same number of turns
+    for (int64_t r0 = slot * TEAMS; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + team;
+        float v[CH * 8];
+        float sum[1] = {0.0f};
 #pragma unroll
-    for (int i = 0; i < CH * 8; ++i) v[i] = fmaf(v[i] * rstd, wt[i], bs[i]);
-    Part<IO, TEAM, CH, VEC>::store(a.y, at, m, lane, v);
-    if (in && lane == 0) {
-        if (a.mean != nullptr) a.mean[part] = mean;
-        if (a.rstd != nullptr) a.rstd[part] = rstd;
+        for (int u = 0; u < CH; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[u * 8 + e] = x.get(u, e);
+                sum[0] += v[u * 8 + e];
+            }
+        fetch(row + step);
+        team_sum<TEAM>(sum, slot_sums[0]);
+        const float mean = sum[0] * inv;
+        float sq[1] = {0.0f};
+#pragma unroll
+        for (int u = 0; u < CH; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float& t = v[u * 8 + e];
+                t = P::index(lane, u, e) < n ? t - mean : 0.0f;
+                sq[0] = fmaf(t, t, sq[0]);
+            }
+        team_sum<TEAM>(sq, slot_sums[1]);
+        const float rstd = 1.0f / sqrtf(sq[0] * inv + a.eps);
+#pragma unroll
+        for (int i = 0; i < CH * 8; ++i) v[i] = fmaf(v[i] * rstd, wt[i], bs[i]);
+        const int64_t part = row * a.groups + grp;
+        const bool in = row < a.rows;
+        P::store(a.y, in ? part * n : 0, in ? n : 0, lane, v);
+        if (in && lane == 0) {
+            if (a.mean != nullptr) a.mean[part] = mean;
+            if (a.rstd != nullptr) a.rstd[part] = rstd;
+        }
     }
 }
 
@@ -292,23 +309,41 @@ __global__ __launch_bounds__(kNormBwdThreads) void layer_norm_bwd_kernel(NormArg
     }
 }
 
-// Column sums over the slots: 64 columns per workgroup, its 4 waves a quarter
-// of the slots each.
-__global__ __launch_bounds__(256) void layer_norm_columns_kernel(int64_t dim, int slots,
-                                                                 const float* partial, float* dweight,
-                                                                 float* dbias) {
-    __shared__ float red[4][kWave];
+// Column sums over the slots: 64 columns per workgroup, its 16 waves a
+// sixteenth of the slots each, 4 loads in flight.
+constexpr int kColumnWaves = 16;
+
+__global__ __launch_bounds__(kColumnWaves * kWave) void layer_norm_columns_kernel(int64_t dim, int slots,
+                                                                                  const float* partial,
+                                                                                  float* dweight, float* dbias) {
+    __shared__ float red[kColumnWaves][kWave];
     const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kWave + lane;
     float* out = blockIdx.y ? dbias : dweight;
     if (out == nullptr) return;
     const float* p = partial + static_cast<int64_t>(blockIdx.y) * slots * dim;
     float s = 0.0f;
-    if (col < dim)
-        for (int k = w; k < slots; k += 4) s += p[static_cast<int64_t>(k) * dim + col];
+    if (col < dim) {
+        constexpr int U = 4;
+        for (int k0 = w; k0 < slots; k0 += U * kColumnWaves) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * kColumnWaves;
+                x[u] = k < slots ? p[static_cast<int64_t>(k) * dim + col] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) s += x[u];
+        }
+    }
     red[w][lane] = s;
     __syncthreads();
-    if (w == 0 && col < dim) out[col] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (w == 0 && col < dim) {
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kColumnWaves; ++k) t += red[k][lane];
+        out[col] = t;
+    }
 }
 
 __global__ __launch_bounds__(256) void layer_norm_zero_kernel(int64_t dim, float* dweight, float* dbias) {
@@ -327,6 +362,10 @@ Team team_for(int64_t n) {
     const int lanes = n <= 384 ? 16 : (n <= 1536 ? 64 : (n <= 6144 ? 256 : 512));
     return {lanes, static_cast<int>((n + 8 * lanes - 1) / (8 * lanes))};
 }
+
+// Workgroups of the forward pass, when there are rows for them: several rounds
+// of what the chip holds, so that the last one's idle part is small.
+constexpr int kFwdWorkgroups = 4096;
 
 // Threads per workgroup of the backward pass and slots (workgroups per group
 // of columns): about one workgroup of 512 per compute unit when there are
@@ -351,9 +390,12 @@ template <int IO, int TEAM, int CH, bool VEC>
 hipError_t launch_norm(const NormArgs& a, bool bwd, int threads, int slots, float* partial, hipStream_t s) {
     if (!bwd) {
         constexpr int TEAMS = (TEAM > 256 ? TEAM : 256) / TEAM;
-        const int64_t blocks = (a.rows * a.groups + TEAMS - 1) / TEAMS;
-        hipLaunchKernelGGL((layer_norm_fwd_kernel<IO, TEAM, CH, VEC>), dim3(static_cast<unsigned>(blocks)),
-                           dim3(TEAM > 256 ? TEAM : 256), 0, s, a);
+        const int64_t most = (a.rows + TEAMS - 1) / TEAMS;
+        const int turns = kFwdWorkgroups / static_cast<int>(a.groups < kFwdWorkgroups ? a.groups : kFwdWorkgroups);
+        const int row_slots = static_cast<int>(most < turns ? most : turns);
+        hipLaunchKernelGGL((layer_norm_fwd_kernel<IO, TEAM, CH, VEC>),
+                           dim3(static_cast<unsigned>(row_slots * a.groups)), dim3(TEAM > 256 ? TEAM : 256), 0, s,
+                           a, row_slots);
     } else {
         hipLaunchKernelGGL((layer_norm_bwd_kernel<IO, TEAM, CH, VEC>),
                            dim3(static_cast<unsigned>(slots * a.groups)), dim3(threads), 0, s, a, slots, partial);
@@ -415,7 +457,7 @@ hipError_t launch_layer_norm_bwd(const NormArgs& a, int cu, void* ws, hipStream_
     const hipError_t e = launch_norm_any(a, true, g.threads, g.slots, partial, s);
     if (e != hipSuccess || g.slots == 1 || (a.dweight == nullptr && a.dbias == nullptr)) return e;
     hipLaunchKernelGGL(layer_norm_columns_kernel, dim3(static_cast<unsigned>((a.dim + kWave - 1) / kWave), 2),
-                       dim3(256), 0, s, a.dim, g.slots, partial, a.dweight, a.dbias);
+                       dim3(kColumnWaves * kWave), 0, s, a.dim, g.slots, partial, a.dweight, a.dbias);
     return hipGetLastError();
 }
 

@@ -72,18 +72,26 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(JoinArgs a) {
 
 // Gradients of keys and values that several heads share: the sum of the
 // heads' fp32 gradients (batch, seqlen, heads, dim), rounded once.
+struct ShareArgs {
+    int64_t rows;           // (batch, seqlen, kv_heads)
+    int rep;                // heads per head of keys and values
+    int dim[2];
+    const float* part[2];
+    void* out[2];
+};
+
 template <int IO>
-__global__ __launch_bounds__(256) void linear_attn_share_kernel(int64_t rows, int rep, int dim,
-                                                                const float* part, void* out) {
-    const int64_t quads = dim / 4, count = rows * quads;
+__global__ __launch_bounds__(256) void linear_attn_share_kernel(ShareArgs a) {
+    const int which = blockIdx.y;
+    const int64_t quads = a.dim[which] / 4, count = a.rows * quads;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += stride) {
         const int64_t row = i / quads, q = i - row * quads;
-        const f32x4* p = reinterpret_cast<const f32x4*>(part) + row * rep * quads + q;
+        const f32x4* p = reinterpret_cast<const f32x4*>(a.part[which]) + row * a.rep * quads + q;
         f32x4 s = p[0];
-        for (int r = 1; r < rep; ++r) s += p[r * quads];
+        for (int r = 1; r < a.rep; ++r) s += p[r * quads];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) store_io<IO>(out, 4 * i + v, s[v]);
+        for (int v = 0; v < 4; ++v) store_io<IO>(a.out[which], 4 * i + v, s[v]);
     }
 }
 
@@ -318,13 +326,20 @@ hipError_t launch_join(const LinearAttnCall& c, const LinPlan& p, float* seg_s, 
     return hipGetLastError();
 }
 
-hipError_t launch_share(const LinearAttnCall& c, int dim, const float* part, void* out, hipStream_t s) {
-    const int64_t rows = c.batch * c.seqlen * c.kv_heads;
-    if (rows == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(stride_blocks(rows * (dim / 4)))), block(256);
-    const int rep = c.heads / c.kv_heads;
-    if (c.io == kIoF32) hipLaunchKernelGGL((linear_attn_share_kernel<kIoF32>), grid, block, 0, s, rows, rep, dim, part, out);
-    else hipLaunchKernelGGL((linear_attn_share_kernel<kIoBF16>), grid, block, 0, s, rows, rep, dim, part, out);
+hipError_t launch_share(const LinearAttnCall& c, const float* part_k, const float* part_v, hipStream_t s) {
+    ShareArgs a = {};
+    a.rows = c.batch * c.seqlen * c.kv_heads;
+    if (a.rows == 0) return hipSuccess;
+    a.rep = c.heads / c.kv_heads;
+    a.dim[0] = c.dk;
+    a.dim[1] = c.dv;
+    a.part[0] = part_k;
+    a.part[1] = part_v;
+    a.out[0] = c.d_k;
+    a.out[1] = c.d_v;
+    const dim3 grid(static_cast<unsigned>(stride_blocks(a.rows * (max_dim(c) / 4))), 2), block(256);
+    if (c.io == kIoF32) hipLaunchKernelGGL((linear_attn_share_kernel<kIoF32>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((linear_attn_share_kernel<kIoBF16>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -439,9 +454,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         e = launch_mode<kLinBwd>(c, a, dc_pad, s);
         if (e != hipSuccess) return e;
         if (shared) {
-            e = launch_share(c, c.dk, part_k, c.d_k, s);
-            if (e != hipSuccess) return e;
-            e = launch_share(c, c.dv, part_v, c.d_v, s);
+            e = launch_share(c, part_k, part_v, s);
             if (e != hipSuccess) return e;
         }
     }
