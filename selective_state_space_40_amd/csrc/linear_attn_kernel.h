@@ -597,26 +597,30 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
                 }
 #pragma unroll
                 for (int u = 0; u < OWN; ++u) {
-                    const int it = grp + GR * u;
-                    f32x4 pv;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) pv[v] = G[u][v] * fac[u][v];
-                    O::st4(lds.P + (16 * it + c) * Lds::kRowP + 16 * jt + 4 * g, pv);
-                    if constexpr (kBwd) {
-                        if (ps.dg_pairs && it >= jt) {
-                            // this column block's share of x_i . v_j
-                            const T* vrow = lds.V + (16 * jt + c) * RV;
-                            const T* xrow = lds.X + (16 * it + c) * RX;
-                            f32x4 A = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int v = 0; v < 4; ++v) G[u][v] *= fac[u][v];
+                    O::st4(lds.P + (16 * (grp + GR * u) + c) * Lds::kRowP + 16 * jt + 4 * g, G[u]);
+                }
+                if constexpr (kBwd) {
+                    if (ps.dg_pairs) {
+                        // this column block's share of x_i . v_j, against P's
+                        // value and the steps between i and j
+                        f32x4 A[OWN];
 #pragma unroll
-                            for (int k = 0; k < DOB; k += 32)
-                                A = O::mma(O::nat(vrow + k, g), O::nat(xrow + k, g), A);
+                        for (int u = 0; u < OWN; ++u) A[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                const int n = 16 * (it - jt) + c - 4 * g - v;
-                                dgi += n > 0 ? static_cast<float>(n) * pv[v] * A[v] : 0.0f;
-                            }
+                        for (int k = 0; k < DOB; k += 32) {
+                            const Frag vk = O::nat(lds.V + (16 * jt + c) * RV + k, g);
+#pragma unroll
+                            for (int u = 0; u < OWN; ++u)
+                                A[u] = O::mma(vk, O::nat(lds.X + (16 * (grp + GR * u) + c) * RX + k, g), A[u]);
                         }
+                        const float apart = static_cast<float>(c - 4 * g + 16 * (grp - jt));
+#pragma unroll
+                        for (int u = 0; u < OWN; ++u)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                dgi = fmaf((apart + static_cast<float>(16 * GR * u - v)) * G[u][v], A[u][v], dgi);
                     }
                 }
             }
