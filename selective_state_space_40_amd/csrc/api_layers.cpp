@@ -59,16 +59,17 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The automatic division. Segments add a pass over keys and values and a
 // join, so a sequence is cut only where its chunks, walked one after the other,
 // would leave the chip idle. The time of a plan with n segments is taken as
-//     (chunks / n * chunk + entry) * load(w) * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
-// with w the workgroups per compute unit: `chunk` the time of 64 tokens alone on
-// a unit, `entry` a workgroup's beginning and end, load what sharing a unit costs (two workgroups take 1.57 times as long as
-// one; the wide kernels, one to a unit, take turns), `summary` the states'
-// pass, join its launches. Microseconds measured on MI355X with one workgroup
-// per unit; examples, cut by this rule against not cut: one sequence of 65536,
-// 16 heads of 128: 349 us with 16 segments against 411 with 8 and 2.9 ms; 8 x
-// 2048 x 16 heads of 128: 76 us whole against 102 with 2; 4 x 1024 x 16 heads
-// of 64: 25 us whole against 29; gradients of 2 x 333 x 6 heads in fp32: 42 us
-// with 3 against 58 whole.
+//     (chunks / n * chunk + entry) * load * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
+// with `chunk` the time of 64 tokens alone on a compute unit, `entry` a
+// workgroup's beginning and end, `load` the rounds that the workgroups take (a
+// round of two to a unit takes 1.57 times as long as one of one; a unit holds
+// one of the wide kernels), `summary` the states' pass and `join` its
+// launches. Microseconds measured on MI355X with one workgroup per unit;
+// examples, cut by this rule against not cut: one sequence of 65536, 16 heads
+// of 128: 349 us with 16 segments against 411 with 8 and 2.9 ms; 8 x 2048 x 16
+// heads of 128: 74 us whole against 89 with 2; 4 x 1024 x 16 heads of 64: 25
+// us whole against 29; gradients of 2 x 333 x 6 heads in fp32: 37 us with 6
+// against 63 whole.
 struct PlanCost {
     double chunk[2][3];   // [fp32, bf16][head width 64, 128, 256]
     double entry[3];
@@ -86,8 +87,10 @@ int64_t choose_segments(const PlanCost& cost, int io, int dc_pad, int64_t seqlen
     int64_t best = 1;
     double least = 0.0;
     for (int64_t n = 1; n <= ceil_div(seqlen, kMinSegment) && (n == 1 || units * n <= 8 * int64_t(cu)); ++n) {
-        const double w = static_cast<double>(units * n) / cu;
-        const double load = w <= 1.0 ? 1.0 : (dc_pad == 256 ? w : (w <= 2.0 ? 1.57 : 0.785 * w));
+        const int64_t per_round = dc_pad == 256 ? cu : 2 * int64_t(cu);
+        const int64_t rest = units * n % per_round;
+        const double load = static_cast<double>(units * n / per_round) * (dc_pad == 256 ? 1.0 : 1.57) +
+                            (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : 1.57));
         double t = ceil_div(ceil_div(seqlen, n), kSegUnit) * 1.0;
         t = ((t < chunks ? t : chunks) * chunk + cost.entry[width]) * load;
         if (n > 1) t = t * (1.0 + cost.summary) + kJoinCost;
