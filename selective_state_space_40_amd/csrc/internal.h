@@ -163,7 +163,8 @@ hipError_t launch_ssd_fwd(const SsdArgs& a, hipStream_t stream);
 
 // Linear attention with a decay for each head (linear_attn_kernel.h).
 constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
-constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;   // passes of the backward launch
+// passes of the backward launch
+constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;
 constexpr int kLinMaxDim = 256;   // widest head
 // Waves of a workgroup and output columns of a wave. 64 columns leave two
 // workgroups on a compute unit (prompts of 8 x 2048 x 16 heads of 128: 76 us
