@@ -62,8 +62,8 @@ extern "C" {
  * Inside it a NaN or infinite value may, since the chunk products multiply the
  * causal mask's zeros by it, reach the earlier outputs of its own chunk of 64
  * tokens, in its own row and head. Sums and states are fp32; with bf16 I/O the
- * products' operands are bf16, those that reach the fp32 state carried as
- * two bf16 terms.
+ * products' operands are bf16; what reaches a state or a decay gradient that
+ * the caller gets is carried as three bf16 terms, with fp32's accuracy.
  */
 int linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
                                    int64_t dk, int64_t dv, int dtype, int64_t segment_len,

@@ -59,40 +59,57 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The automatic division. Segments add a pass over keys and values and a
 // join, so a sequence is cut only where its chunks, walked one after the other,
 // would leave the chip idle. The time of a plan with n segments is taken as
-//     (chunks / n * chunk + entry) * load * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
-// with `chunk` the time of 64 tokens alone on a compute unit, `entry` a
-// workgroup's beginning and end, `load` the rounds that the workgroups take (a
-// round of two to a unit takes 1.57 times as long as one of one; a unit holds
-// one of the wide kernels), `summary` the states' pass and `join` its
-// launches. Microseconds measured on MI355X with one workgroup per unit;
-// examples, cut by this rule against not cut: one sequence of 65536, 16 heads
-// of 128: 349 us with 16 segments against 411 with 8 and 2.9 ms; 8 x 2048 x 16
-// heads of 128: 74 us whole against 89 with 2; 4 x 1024 x 16 heads of 64: 25
-// us whole against 29; gradients of 2 x 333 x 6 heads in fp32: 37 us with 6
-// against 63 whole.
+//     (chunks / n * walk + entry) * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
+// with `entry` a workgroup's beginning and end, `summary` the states' pass,
+// `join` its launches and `walk` the time that 64 tokens take with all
+// workgroups on the chip. Alone on a compute unit they take `chunk`; a second
+// workgroup there makes it 1.57 times that, a third waits; of the wide kernels
+// a unit holds one. The backward's pass of dq, where the decay's gradient is
+// formed, takes `longest` and goes first, the other two passes run beside and
+// behind it (whether that gradient is wanted is not known here).
+// Microseconds measured on MI355X with one workgroup per unit; examples, cut
+// by this rule against not cut: one sequence of 65536, 16 heads of 128: 364 us
+// with 16 segments against 2.9 ms; 8 x 2048 x 16 heads of 128: 77 us whole
+// against 105 with 2, gradients 267 whole against 300 with 2; 4 x 1024 x 16
+// heads of 64: 27 us whole against 30 with 2, gradients 58 with 4 against 67;
+// gradients in fp32 of 2 x 333 x 6 heads: 40 us with 6 against 77, of 2 x 2048
+// x 8 heads of 200 x 168: 404 us with 4 against 1152.
 struct PlanCost {
     double chunk[2][3];   // [fp32, bf16][head width 64, 128, 256]
     double entry[3];
     double summary;
 };
 constexpr PlanCost kFwdCost = {{{4.4, 8.0, 18.4}, {1.45, 2.3, 3.6}}, {2.0, 3.0, 9.0}, 0.5};
-constexpr PlanCost kBwdCost = {{{6.3, 11.0, 21.0}, {3.0, 4.1, 8.8}}, {2.0, 3.0, 5.0}, 0.35};
-constexpr double kJoinCost = 14.0;
+constexpr PlanCost kBwdCost = {{{4.3, 6.7, 19.0}, {1.95, 2.6, 4.6}}, {2.0, 3.0, 5.0}, 0.35};
+constexpr double kBwdLongest[2][3] = {{7.5, 13.0, 36.0}, {3.6, 5.3, 16.3}};
+constexpr double kJoinCost = 14.0, kSharedUnit = 1.57;
 constexpr int64_t kMinSegment = 64;
 
-int64_t choose_segments(const PlanCost& cost, int io, int dc_pad, int64_t seqlen, int64_t units, int cu) {
-    const int width = dc_pad == 64 ? 0 : (dc_pad == 128 ? 1 : 2);
-    const double chunk = cost.chunk[io == mamba::kIoF32 ? 0 : 1][width];
+// `units` workgroups per segment and pass.
+int64_t choose_segments(bool bwd, int io, int dc_pad, int64_t seqlen, int64_t units, int cu) {
+    const PlanCost& cost = bwd ? kBwdCost : kFwdCost;
+    const bool wide = dc_pad == 256;
+    const int width = dc_pad == 64 ? 0 : (wide ? 2 : 1), type = io == mamba::kIoF32 ? 0 : 1;
+    const double chunk = cost.chunk[type][width], longest = kBwdLongest[type][width];
     const double chunks = static_cast<double>(seqlen) / 64.0;
+    const int64_t all = units * (bwd ? 3 : 1);
     int64_t best = 1;
     double least = 0.0;
-    for (int64_t n = 1; n <= ceil_div(seqlen, kMinSegment) && (n == 1 || units * n <= 8 * int64_t(cu)); ++n) {
-        const int64_t per_round = dc_pad == 256 ? cu : 2 * int64_t(cu);
-        const int64_t rest = units * n % per_round;
-        const double load = static_cast<double>(units * n / per_round) * (dc_pad == 256 ? 1.0 : 1.57) +
-                            (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : 1.57));
-        double t = ceil_div(ceil_div(seqlen, n), kSegUnit) * 1.0;
-        t = ((t < chunks ? t : chunks) * chunk + cost.entry[width]) * load;
+    for (int64_t n = 1; n <= ceil_div(seqlen, kMinSegment) && (n == 1 || all * n <= 8 * int64_t(cu)); ++n) {
+        double walk;
+        if (bwd) {
+            const double sum = (longest + 2.0 * chunk) * static_cast<double>(units * n) / cu;
+            const double least_walk = longest * (wide || all * n <= cu ? 1.0 : 1.3);
+            walk = sum * (wide ? 1.0 : kSharedUnit / 2);
+            if (walk < least_walk) walk = least_walk;
+        } else {
+            const int64_t round = wide ? cu : 2 * int64_t(cu), rest = all * n % round;
+            const double full = wide ? 1.0 : kSharedUnit;
+            walk = chunk * (static_cast<double>(all * n / round) * full +
+                            (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : kSharedUnit)));
+        }
+        const double each = static_cast<double>(ceil_div(ceil_div(seqlen, n), kSegUnit));
+        double t = (each < chunks ? each : chunks) * walk + cost.entry[width];
         if (n > 1) t = t * (1.0 + cost.summary) + kJoinCost;
         if (n == 1 || t < least) {
             least = t;
@@ -116,8 +133,7 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
         int cu = 0;
         const int st = mamba::current_cu_count(&cu);
         if (st != MAMBA_OK) return st;
-        const int64_t n = choose_segments(passes == 1 ? kFwdCost : kBwdCost, c.io, dc_pad, c.seqlen,
-                                          c.batch * c.heads * blocks * passes, cu);
+        const int64_t n = choose_segments(passes > 1, c.io, dc_pad, c.seqlen, c.batch * c.heads * blocks, cu);
         seg = n > 1 ? ceil_div(ceil_div(c.seqlen, n), kSegUnit) * kSegUnit : c.seqlen;
     }
     if (seg < c.seqlen) {
@@ -127,9 +143,6 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
         p->nseg = static_cast<int>(n);
     }
     if (c.batch * c.heads * p->nseg > kMaxBlocks / (passes * blocks)) return MAMBA_ERR_UNSUPPORTED;
-    // and a block per window of the decay's gradient
-    if (passes > 1 && c.batch * c.heads > kMaxBlocks / (c.seqlen / mamba::kLinWindow + p->nseg + 1))
-        return MAMBA_ERR_UNSUPPORTED;
     // the join's launch holds (row, head) in a 16-bit grid dimension
     if (p->nseg > 1 && c.batch * c.heads > 65535) {
         if (segment_len != 0) return MAMBA_ERR_UNSUPPORTED;

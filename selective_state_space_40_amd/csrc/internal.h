@@ -164,7 +164,7 @@ hipError_t launch_ssd_fwd(const SsdArgs& a, hipStream_t stream);
 // Linear attention with a decay for each head (linear_attn_kernel.h).
 constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
 // passes of the backward launch
-constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;
+constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;   // dq first
 constexpr int kLinMaxDim = 256;   // widest head
 // Waves of a workgroup and output columns of a wave. 64 columns leave two
 // workgroups on a compute unit (prompts of 8 x 2048 x 16 heads of 128: 76 us
@@ -175,42 +175,35 @@ constexpr int lin_waves(int dc_pad) { return dc_pad == 256 ? 8 : 4; }
 constexpr int kLinCols = 16;
 // Tokens of a chunk: fp32 takes half in the same LDS.
 constexpr int kLinChunkBF16 = 64, kLinChunkF32 = 32;
-// Tokens of a window of the decay's gradient: a state and an adjoint of dk x
-// dv values are kept per window (8% of the backward's traffic at 128 x 128).
-constexpr int kLinWindow = 1024;
 
 // One pass (q, k, v) -> out over the sequences; see the kernel's header.
 struct LinPass {
     const void* q;          // (batch, seqlen, hq, dc)
     const void* k;          // (batch, seqlen, hk, dc)
     const void* v;          // (batch, seqlen, hv, dout)
-    const void* x;          // (batch, seqlen, hx, dout) or nullptr: for the decay's gradient
+    const void* x;          // (batch, seqlen, heads, dout): q, where the pass forms the decay's gradient
     void* out;              // (batch, seqlen, heads, dout)
     const float* s_in;      // state the walk starts from, or nullptr (zeros)
     float* s_out;           // receives the state the walk ends with, or nullptr
-    float* marks;           // (batch, heads, nseg, nmark, dk, dv) or nullptr: receives the state
-                            // (adjoint) between a segment's windows of kLinWindow tokens
     float* seg_in;          // (batch, heads, nseg, dk, dv): state entering each segment
     int sn, sp;             // strides of a state's rows (dc) and columns (dout)
-    int hq, hk, hv, hx;     // heads of each tensor: the call's heads, or those of its keys
+    int hq, hk, hv;         // heads of each tensor: the call's heads, or those of its keys
     int dc, dout;
     float out_scale;        // factor of q S
     float state_scale;      // factor of the tokens' share of the state
     int rev;                // walks from the last token to the first
     int out32;              // out is fp32
-    int dg_pairs;           // adds the pairs of one chunk to the decay's gradient
 };
 
 struct LinArgs {
     int64_t batch, seqlen, seg_len;
     int heads, rep;           // heads, and how many share a head of keys and values
     int nseg, nblk, npass;
-    int nmark;                // windows less one of a segment
-    int exact;                // kLinState: the states serve the decay's gradient
+    int exact;                // kLinState: an fp32 result depends on the states
     const int32_t* lengths;   // (batch) or nullptr
     const float* log_decay;   // (heads)
     float scale;
-    double* dg;               // (heads, batch, nseg, 2, nblk) terms of the decay's gradient, or nullptr
+    double* dg;               // (heads, batch, nseg, nblk) terms of the decay's gradient, or nullptr
     const float* dhL;
     const float* adj_in;      // the adjoints' seg_in
     LinPass pass[3];

@@ -95,63 +95,13 @@ __global__ __launch_bounds__(256) void linear_attn_share_kernel(ShareArgs a) {
     }
 }
 
-// The decay's gradient through the windows' ends: kLinWindow times the adjoint
-// against the state, one term per mark.
-struct MarkArgs {
-    int64_t batch, seqlen, seg_len, state_elems;
-    int heads, nseg, nmark, chunk;
-    const int32_t* lengths;
-    const float* log_decay;
-    const float* state;
-    const float* adjoint;
-    double* out;              // (heads, batch, nseg, nmark)
-};
-
-__global__ __launch_bounds__(256) void linear_attn_marks_kernel(MarkArgs a) {
-    __shared__ double red[4];
-    // block (bh, seg, mark)
-    const int64_t id = blockIdx.x;
-    const int64_t mark = id % a.nmark, seg = id / a.nmark % a.nseg, bh = id / a.nmark / a.nseg;
-    const int64_t b = bh / a.heads, hd = bh - b * a.heads;
-    int64_t len = a.seqlen;
-    if (a.lengths != nullptr) {
-        const int64_t n = a.lengths[b];
-        len = n < 0 ? 0 : (n < len ? n : len);
-    }
-    int64_t ntok = len - seg * a.seg_len;
-    if (ntok > a.seg_len) ntok = a.seg_len;
-    // no mark was written at or behind a segment's last token, nor for heads
-    // that count inside chunks
-    const bool have = (mark + 1) * kLinWindow < ntok &&
-                      !(a.log_decay[hd] * static_cast<float>(a.chunk) <= -25.0f);
-    double s = 0.0;
-    if (have) {
-        const f32x4* x = reinterpret_cast<const f32x4*>(a.state + id * a.state_elems);
-        const f32x4* y = reinterpret_cast<const f32x4*>(a.adjoint + id * a.state_elems);
-        for (int64_t i = threadIdx.x; i < a.state_elems / 4; i += 256) {
-            const f32x4 p = x[i] * y[i];
-            s += static_cast<double>((p[0] + p[1]) + (p[2] + p[3]));
-        }
-    }
-#pragma unroll
-    for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
-    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = s;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        a.out[((hd * a.batch + b) * a.nseg + seg) * a.nmark + mark] =
-            kLinWindow * ((red[0] + red[1]) + (red[2] + red[3]));
-}
-
 // The decay's gradient: each head's terms in a fixed order.
 __global__ __launch_bounds__(256) void linear_attn_decay_kernel(int64_t terms, const double* dg,
-                                                                int64_t marks, const double* dgm,
                                                                 float* out) {
     __shared__ double red[4];
     const double* p = dg + static_cast<int64_t>(blockIdx.x) * terms;
-    const double* pm = dgm + static_cast<int64_t>(blockIdx.x) * marks;
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < terms; i += 256) s += p[i];
-    for (int64_t i = threadIdx.x; i < marks; i += 256) s += pm[i];
 #pragma unroll
     for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
     if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = s;
@@ -238,8 +188,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The backward call's scratch, in order: each part 256-byte aligned.
 struct BwdScratch {
-    size_t seg_s = 0, seg_d = 0, dg = 0, dgm = 0, mark_s = 0, mark_d = 0, dk = 0, dv = 0, total = 0;
-    int nmark = 0;
+    size_t seg_s = 0, seg_d = 0, dg = 0, dk = 0, dv = 0, total = 0;
 };
 
 BwdScratch bwd_scratch(const LinearAttnCall& c, const LinPlan& p, int nblk) {
@@ -249,12 +198,7 @@ BwdScratch bwd_scratch(const LinearAttnCall& c, const LinPlan& p, int nblk) {
     w.seg_s = 0;
     w.seg_d = seg;
     w.dg = w.seg_d + seg;
-    w.nmark = static_cast<int>((p.seg_len - 1) / kLinWindow);
-    w.dgm = w.dg + up256(bh * p.nseg * 2 * nblk * 8);
-    w.mark_s = w.dgm + up256(bh * p.nseg * w.nmark * 8);
-    const size_t marks = up256(bh * p.nseg * w.nmark * c.dk * c.dv * 4);
-    w.mark_d = w.mark_s + marks;
-    w.dk = w.mark_d + marks;
+    w.dk = w.dg + up256(bh * p.nseg * nblk * 8);
     const size_t rows = c.heads != c.kv_heads ? static_cast<size_t>(c.batch) * c.seqlen * c.heads : 0;
     w.dv = w.dk + up256(rows * c.dk * 4);
     w.total = w.dv + up256(rows * c.dv * 4);
@@ -290,7 +234,7 @@ LinPass forward_pass(const LinearAttnCall& c) {
     s.s_out = c.hL;
     s.sn = c.dv;
     s.sp = 1;
-    s.hq = s.hx = c.heads;
+    s.hq = c.heads;
     s.hk = s.hv = c.kv_heads;
     s.dc = c.dk;
     s.dout = c.dv;
@@ -355,6 +299,7 @@ hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, voi
     a.nblk = lin_blocks(lin_padded(c.dk), c.dv);
     a.pass[0] = forward_pass(c);
     a.pass[0].seg_in = static_cast<float*>(ws);
+    a.exact = c.hL != nullptr;
     if (p.nseg > 1) {
         hipError_t e = launch_mode<kLinState>(c, a, lin_padded(c.dk), s);
         if (e != hipSuccess) return e;
@@ -375,10 +320,6 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
     float* part_k = reinterpret_cast<float*>(base + w.dk);
     float* part_v = reinterpret_cast<float*>(base + w.dv);
     double* dg = c.dlog_decay != nullptr ? reinterpret_cast<double*>(base + w.dg) : nullptr;
-    double* dgm = reinterpret_cast<double*>(base + w.dgm);
-    const bool marked = dg != nullptr && w.nmark > 0;
-    float* mark_s = marked ? reinterpret_cast<float*>(base + w.mark_s) : nullptr;
-    float* mark_d = marked ? reinterpret_cast<float*>(base + w.mark_d) : nullptr;
     hipError_t e = hipSuccess;
     if (c.batch > 0) {
         // the states and adjoints, (dk, dv) in memory for every pass
@@ -388,7 +329,6 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         adj.q = c.k;
         adj.k = c.q;
         adj.v = c.d_o;
-        adj.x = nullptr;
         adj.out = shared ? part_v : c.d_v;
         adj.s_in = c.dhL;
         adj.s_out = c.dh0;
@@ -396,7 +336,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         adj.sn = c.dv;
         adj.sp = 1;
         adj.hq = c.kv_heads;
-        adj.hk = adj.hv = adj.hx = c.heads;
+        adj.hk = adj.hv = c.heads;
         adj.dc = c.dk;
         adj.dout = c.dv;
         adj.out_scale = 1.0f;
@@ -407,7 +347,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
             LinArgs a = base_args(c, p);
             a.nblk = lin_blocks(lin_padded(c.dk), c.dv);
             a.npass = 2;
-            a.exact = dg != nullptr;
+            a.exact = dg != nullptr || c.dh0 != nullptr;
             a.pass[0] = states;
             a.pass[1] = adj;
             e = launch_mode<kLinState>(c, a, lin_padded(c.dk), s);
@@ -421,30 +361,24 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         a.dg = dg;
         a.dhL = c.dhL;
         a.adj_in = seg_d;
-        a.nmark = w.nmark;
         a.pass[kLinPassDv] = adj;
-        a.pass[kLinPassDv].marks = mark_d;
         LinPass& q = a.pass[kLinPassDq];
         q = states;
         q.q = c.d_o;
         q.k = c.v;
         q.v = c.k;
-        q.x = dg != nullptr ? c.q : nullptr;
+        q.x = c.q;
         q.out = c.dq;
         q.s_out = nullptr;
         q.sn = 1;
         q.sp = c.dv;
         q.dc = c.dv;
         q.dout = c.dk;
-        q.dg_pairs = dg != nullptr;
-        q.marks = mark_s;
         LinPass& k = a.pass[kLinPassDk];
         k = adj;
         k.q = c.v;
         k.k = c.d_o;
         k.v = c.q;
-        k.x = dg != nullptr ? c.k : nullptr;
-        k.hx = c.kv_heads;
         k.out = shared ? static_cast<void*>(part_k) : c.d_k;
         k.s_out = nullptr;
         k.sn = 1;
@@ -459,29 +393,8 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         }
     }
     if (c.dlog_decay != nullptr) {
-        if (marked && c.batch > 0) {
-            MarkArgs m = {};
-            m.batch = c.batch;
-            m.seqlen = c.seqlen;
-            m.seg_len = p.seg_len;
-            m.state_elems = static_cast<int64_t>(c.dk) * c.dv;
-            m.heads = c.heads;
-            m.nseg = p.nseg;
-            m.nmark = w.nmark;
-            m.chunk = c.io == kIoF32 ? kLinChunkF32 : kLinChunkBF16;
-            m.lengths = c.lengths;
-            m.log_decay = c.log_decay;
-            m.state = mark_s;
-            m.adjoint = mark_d;
-            m.out = dgm;
-            hipLaunchKernelGGL(linear_attn_marks_kernel,
-                               dim3(static_cast<unsigned>(c.batch * c.heads * p.nseg * w.nmark)), dim3(256), 0, s, m);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
         hipLaunchKernelGGL(linear_attn_decay_kernel, dim3(static_cast<unsigned>(c.heads)), dim3(256), 0, s,
-                           c.batch * p.nseg * 2 * nblk, dg, marked ? c.batch * p.nseg * w.nmark : 0, dgm,
-                           c.dlog_decay);
+                           c.batch * p.nseg * nblk, dg, c.dlog_decay);
         e = hipGetLastError();
     }
     return e;

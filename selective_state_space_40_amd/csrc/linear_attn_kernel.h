@@ -29,11 +29,21 @@
 // bf16 operands. q, k and v enter the products exactly. P is rounded to bf16
 // (its effect on a bf16 output is that of the output's own rounding). What
 // reaches fp32 results goes in as a sum of bf16 terms, each the rounding of
-// what the ones before leave: two for the state (2^-16 of a term at most),
-// three where the gradient of the decay is formed, since it weighs rounding
-// errors with a token's place in its segment. The product q S that only an
-// output sees needs one. fp32 I/O uses the fp32 matrix instruction and no
-// rounding.
+// what the ones before leave: three (2^-25 of a term at most) for a state that
+// leaves in fp32 and for the gradient of the decay, two (2^-17) for a state
+// that only bf16 outputs see, and one for the product q S that they see
+// directly. fp32 I/O uses the fp32 matrix instruction and no rounding.
+//
+// The gradient of the log decay is formed in the pass of dq, with the state's
+// derivative T = dS/d(log lam) as a second state:
+//     T_i = lam^(i+1) (T + (i+1) S) + sum_{j <= i} (i-j) lam^(i-j) k_j^T v_j
+//     dlog_decay = sum_i scale do_i . (q_i T_i) + <adjoint at the end, T_end>
+// where the sum over j <= i of one chunk is taken pair by pair, from P. Every
+// pair of tokens enters once, with its own number of steps, so nothing
+// cancels; a second way, sums of token places against q . dq and k . dk,
+// needs no T but cancels down from a window's length to a memory's, and was 6
+// to 10 times less exact with windows of 1024 tokens. T starts at zero in every
+// segment, whose end's adjoint carries its steps on.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -244,25 +254,9 @@ struct LinLds {
     alignas(16) T P[MODE == kLinState ? 8 : kC * kRowP];
     alignas(16) float W[kC];      // weight of token j in the state update
     float pow[kC + 1];            // lam^n
+    float fac[MODE == kLinBwd ? 2 * kC : 1];   // P's factor n tokens apart at n + C: zero for n < 0
     double red[WAVES];
 };
-
-// The gradient of the log decay is the sum over pairs (t, j) of steps t - j
-// times the pair's term lam^(t-j) scale (q_t . k_j) (do_t . v_j), the entering
-// state counting as a token before the first and the gradient of the final
-// state as one at the last. Pairs of one chunk are added as they are. For the
-// others, with x_t = q_t . (dq_t through the state) and z_j = k_j . (dk_j
-// through the adjoint), both cut at the same chunks, and places counted in a
-// window of W tokens (that starts afresh in every segment),
-//     sum_t (t + 1) x_t - sum_j (j + 1) z_j + W <adjoint, state at its end>
-// gives every pair its steps. The three cancel down to a memory's length from
-// a window's, so their rounding (fp32 throughout) is amplified by W over that
-// length: W is kLinWindow, and a head that forgets within a chunk (lam^C below
-// e^-25) counts inside chunks instead, t + 1 from a chunk's start and C - 1 - j
-// to its end; what crosses a whole chunk is nothing there.
-__device__ __forceinline__ bool decay_is_strong(float g, int chunk) {
-    return g * static_cast<float>(chunk) <= -25.0f;
-}
 
 // lam^n = exp(g n), the product's rounding error put back.
 __device__ __forceinline__ float decay_power(float g, int n) {
@@ -283,8 +277,13 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
     return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
-template <int IO, int DC, int MODE>
-__global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(LinArgs a) {
+// One workgroup's walk: column block blk of pass ip over segment seg of (row,
+// head) bh. EXACT: the state enters with three terms. DG: the pass also forms
+// the decay's gradient.
+template <int IO, int DC, int MODE, bool EXACT, bool DG>
+__device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC, MODE>& lds, const int ip,
+                                                 const int blk, int seg, const int64_t bh, const int64_t b,
+                                                 const int hd) {
     typedef LinOps<IO> O;
     typedef typename O::T T;
     typedef typename O::Frag Frag;
@@ -298,55 +297,25 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     constexpr bool kState = MODE == kLinState, kBwd = MODE == kLinBwd;
     typedef LinLds<IO, DC, MODE> Lds;
     constexpr int RK = Lds::TileK::kRow, RV = Lds::TileV::kRow, RQ = Lds::TileQ::kRow, RX = Lds::TileX::kRow;
-    __shared__ Lds lds;
-
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane & 15, g = lane >> 4;
 
-    // which (row, head, segment, pass, column block); neighbours in this
-    // order read the same rows and share an XCD's L2. With the decay's gradient
-    // the passes that form it take longest and go first, the third fills the
-    // compute units they leave (8 x 2048 x 16 heads of 128: 267 us, mixed 288;
-    // without that gradient, all alike: mixed 216, so ordered 224).
-    const uint32_t nsegs = kState ? a.nseg - 1 : a.nseg;
-    const bool ordered = kBwd && a.dg != nullptr;
-    const uint32_t last = ordered ? gridDim.x / 3 : 0, most = gridDim.x - last;
-    const bool third = blockIdx.x >= most;
-    uint32_t id = third ? xcd_order(blockIdx.x - most, last) : xcd_order(blockIdx.x, most);
-    uint32_t up = id / a.nblk;
-    const int blk = static_cast<int>(id - up * a.nblk);
-    id = up;
-    int ip = kLinPassDv;
-    if (!third) {
-        const uint32_t np = ordered ? 2 : a.npass;
-        up = id / np;
-        ip = static_cast<int>(id - up * np) * (ordered ? kLinPassDk : 1);
-        id = up;
-    }
-    up = id / nsegs;
-    int seg = static_cast<int>(id - up * nsegs);
-    id = up;
-    const int64_t bh = id;                       // row * heads + head
-    const uint32_t row = id / a.heads;
-    const int hd = static_cast<int>(id - row * a.heads);
-    const int64_t b = row;
     const LinPass& ps = a.pass[ip];
     const bool rev = ps.rev != 0;
-    const bool exact = kState ? a.exact != 0 : ps.x != nullptr;   // three terms, for the decay's gradient
     if (kState && rev) seg += 1;   // the reversed walk's last segment is the first
+    // where the state goes at the end: to the join of the segments (kLinState)
+    // or to the caller
+    float* sout = nullptr;
+    if (kState) sout = ps.seg_in;
+    else if (seg == (rev ? 0 : a.nseg - 1)) sout = ps.s_out;
     const int p0 = blk * DOB;
     const int dc = ps.dc, dout = ps.dout;
-    // this workgroup's term of the decay's gradient
-    double* dg_out = nullptr;
-    if constexpr (kBwd) {
-        if (a.dg != nullptr && ip != kLinPassDv)
-            dg_out = a.dg + (((static_cast<int64_t>(hd) * a.batch + b) * a.nseg + seg) * 2 +
-                             (ip == kLinPassDq ? 0 : 1)) * a.nblk + blk;
-    }
+    double* const dg_out =
+        DG ? a.dg + ((static_cast<int64_t>(hd) * a.batch + b) * a.nseg + seg) * a.nblk + blk : nullptr;
     if (p0 >= dout) {   // fewer blocks than another pass of the launch
-        if (kBwd && dg_out != nullptr && tid == 0) *dg_out = 0.0;
+        if (DG && tid == 0) *dg_out = 0.0;
         return;
     }
 
@@ -362,7 +331,6 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     const int64_t ntok = end > seg0 ? end - seg0 : 0;
 
     const float g1 = a.log_decay[hd];
-    const bool strong = decay_is_strong(g1, C);
     const int r = rev ? 1 : 0;
 
     // the inputs' rows and this thread's place in them; the first chunk's
@@ -372,14 +340,12 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     const HeadRows rk(ps.k, row0, ps.hk, ps.hk == a.heads ? hd : shared, dc, sizeof(T));
     const HeadRows rv(ps.v, row0, ps.hv, ps.hv == a.heads ? hd : shared, dout, sizeof(T));
     const HeadRows rq(ps.q, row0, ps.hq, ps.hq == a.heads ? hd : shared, dc, sizeof(T));
-    const HeadRows rx(ps.x, row0, ps.hx, ps.hx == a.heads ? hd : shared, dout, sizeof(T));
+    const HeadRows rx(ps.x, row0, a.heads, hd, dout, sizeof(T));
     const int ok = Lds::TileK::offset(rk, 0, rev), ov = Lds::TileV::offset(rv, p0, rev);
     const int oq = Lds::TileQ::offset(rq, 0, rev), ox = Lds::TileX::offset(rx, p0, rev);
     const int64_t nchunks = (ntok + C - 1) / C;
     // chunk ch of the walk: its first token in the segment and count (0 past
-    // the end). Both directions cut at the same tokens, as the decay's gradient
-    // adds what one direction forms inside a chunk to what both form across
-    // chunks.
+    // the end); both directions cut at the same tokens
     auto chunk_at = [&](int64_t ch, int64_t& first, int& cnt) {
         first = (rev ? nchunks - 1 - ch : ch) * C;
         const int64_t left = ch < nchunks ? ntok - first : 0;
@@ -395,7 +361,7 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     };
     auto fetch_vx = [&](int64_t first, int cnt) {
         tv.load(rv, ov, first, cnt, rev);
-        if constexpr (kBwd) tx.load(rx, ox, first, ps.x != nullptr ? cnt : 0, rev);
+        if constexpr (DG) tx.load(rx, ox, first, cnt, rev);
     };
     {
         int64_t first;
@@ -458,8 +424,10 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     constexpr int GR = WAVES / NT, OWN = NT > GR ? NT / GR : 1;
     const int jt = w % NT, grp = w / NT;
     const bool forms = grp < NT;
-    float fac[OWN][4], eo[NT];
-    if constexpr (!kState) {
+    float eo[NT], fac[DG ? 1 : OWN][4];
+    if constexpr (DG) {
+        for (int n = tid; n < 2 * C; n += THREADS) lds.fac[n] = n < C ? 0.0f : a.scale * lds.pow[n - C];
+    } else if constexpr (!kState) {
 #pragma unroll
         for (int u = 0; u < OWN; ++u)
 #pragma unroll
@@ -467,6 +435,8 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
                 const int n = 16 * (grp + GR * u - jt) + c - 4 * g - v;
                 fac[u][v] = n >= 0 && n < C ? a.scale * lds.pow[n] : 0.0f;
             }
+    }
+    if constexpr (!kState) {
 #pragma unroll
         for (int it = 0; it < NT; ++it) eo[it] = ps.out_scale * lds.pow[16 * it + c + 1 - r];
     }
@@ -481,19 +451,10 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     const HeadRows ro(ps.out, row0, a.heads, hd, dout, osize);
     const int po = p0 + kLinCols * w + 4 * g;
     const int oo = po < dout ? (rev ? -c : c) * ro.stride + po * osize : kPastEnd;
-    double dg = 0.0;
-    // the adjoint at the segment's end against S, this thread's part
-    auto adjoint_dot = [&]() -> double {
-        const float* adj = a.nseg > 1 ? a.adj_in + (bh * a.nseg + seg) * state_elems
-                                      : (a.dhL != nullptr ? a.dhL + bh * state_elems : nullptr);
-        if (adj == nullptr) return 0.0;
-        float sum = 0.0f;
-        load_state(adj, [&](int nt, f32x4 x) {
+    double dg = 0.0;   // this thread's part of the decay's gradient
+    f32x4 D[DG ? NN : 1];   // the state's derivative
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sum = fmaf(S[nt][v], x[v], sum);
-        });
-        return static_cast<double>(sum);
-    };
+    for (int nt = 0; nt < (DG ? NN : 1); ++nt) D[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto store_state = [&](float* to) {
         const __amdgpu_buffer_rsrc_t rs = lin_rsrc(to, state_bytes);
         if (runs) {
@@ -543,18 +504,22 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
         tk.stage(lds.K);
         if constexpr (!kState) tq.stage(lds.Q);
         tv.stage(lds.V);
-        if constexpr (kBwd) tx.stage(lds.X);
+        if constexpr (DG) tx.stage(lds.X);
         if (cnt != wcnt) {
             wcnt = cnt;
             weigh(cnt);
         }
         __syncthreads();
         // the next chunk's loads go out in two groups, as the units that
-        // address them take as long as a chunk's products
+        // address them take as long as a chunk's products; with a second state
+        // the registers for them are free behind its product with q only, for
+        // wide heads behind both states' updates (gradients in fp32, 2 x 2048 x
+        // 8 heads of 200 x 168: 419 us, 450 with spills)
+        constexpr bool kLate = DG && DC == 256;
         int64_t next;
         int next_cnt;
         chunk_at(ch + 1, next, next_cnt);
-        fetch_kq(next, next_cnt);
+        if constexpr (!DG) fetch_kq(next, next_cnt);
 
         f32x4 Y[NT];
         if constexpr (!kState) {
@@ -564,6 +529,14 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
             for (int u = 0; u < OWN; ++u) G[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int it = 0; it < NT; ++it) Y[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // the second and third terms of x onto a product
+            auto rest_terms = [](float (&x)[8], const Frag (&q)[NT], auto& y) {
+                const Frag x1 = O::term(x), x2 = O::term(x);
+#pragma unroll
+                for (int it = 0; it < NT; ++it) y[it] = O::mma(x1, q[it], y[it]);
+#pragma unroll
+                for (int it = 0; it < NT; ++it) y[it] = O::mma(x2, q[it], y[it]);
+            };
 #pragma unroll
             for (int k = 0; k < NN / 2; ++k) {
                 Frag q[NT];
@@ -583,17 +556,10 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
                 const Frag s0 = O::term(x);
 #pragma unroll
                 for (int it = 0; it < NT; ++it) Y[it] = O::mma(s0, q[it], Y[it]);
-                if constexpr (kBwd && O::kSplit) {
-                    if (exact) {
-                        const Frag s1 = O::term(x), s2 = O::term(x);
-#pragma unroll
-                        for (int it = 0; it < NT; ++it) Y[it] = O::mma(s1, q[it], Y[it]);
-#pragma unroll
-                        for (int it = 0; it < NT; ++it) Y[it] = O::mma(s2, q[it], Y[it]);
-                    }
-                }
+                if constexpr (DG && O::kSplit) rest_terms(x, q, Y);
             }
             float dgi = 0.0f;
+            const float* const pf = lds.fac + (C + 16 * (grp - jt) + c - 4 * g);
             if (GR == 1 || forms) {
                 if constexpr (GR > 1) {
 #pragma unroll
@@ -607,61 +573,69 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
 #pragma unroll
                 for (int u = 0; u < OWN; ++u) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) G[u][v] *= fac[u][v];
+                    for (int v = 0; v < 4; ++v) G[u][v] *= DG ? pf[16 * GR * u - v] : fac[DG ? 0 : u][v];
                     O::st4(lds.P + (16 * (grp + GR * u) + c) * Lds::kRowP + 16 * jt + 4 * g, G[u]);
                 }
-                if constexpr (kBwd) {
-                    if (ps.dg_pairs) {
-                        // this column block's share of x_i . v_j, against P's
-                        // value and the steps between i and j
-                        f32x4 A[OWN];
+                if constexpr (DG) {
+                    // this column block's share of x_i . v_j, against P's
+                    // value and the steps between i and j
+                    f32x4 A[OWN];
 #pragma unroll
-                        for (int u = 0; u < OWN; ++u) A[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int u = 0; u < OWN; ++u) A[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int k = 0; k < DOB; k += 32) {
-                            const Frag vk = O::nat(lds.V + (16 * jt + c) * RV + k, g);
-#pragma unroll
-                            for (int u = 0; u < OWN; ++u)
-                                A[u] = O::mma(vk, O::nat(lds.X + (16 * (grp + GR * u) + c) * RX + k, g), A[u]);
-                        }
-                        const float apart = static_cast<float>(c - 4 * g + 16 * (grp - jt));
+                    for (int k = 0; k < DOB; k += 32) {
+                        const Frag vk = O::nat(lds.V + (16 * jt + c) * RV + k, g);
 #pragma unroll
                         for (int u = 0; u < OWN; ++u)
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                dgi = fmaf((apart + static_cast<float>(16 * GR * u - v)) * G[u][v], A[u][v], dgi);
+                            A[u] = O::mma(vk, O::nat(lds.X + (16 * (grp + GR * u) + c) * RX + k, g), A[u]);
                     }
+                    const float apart = static_cast<float>(c - 4 * g + 16 * (grp - jt));
+#pragma unroll
+                    for (int u = 0; u < OWN; ++u)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            dgi = fmaf((apart + static_cast<float>(16 * GR * u - v)) * G[u][v], A[u][v], dgi);
                 }
             }
 #pragma unroll
             for (int it = 0; it < NT; ++it) Y[it] *= eo[it];
-            if constexpr (kBwd) {
-                if (ps.x != nullptr) {
-                    // the decay's gradient through the state: x_i . (this part
-                    // of the output), by the token's place in its window
-                    float sum = dgi;
-                    const int win = static_cast<int>(first % kLinWindow);
+            if constexpr (DG) {
+                // the decay's gradient through the entering state; a second
+                // walk over q's fragments, as the registers hold no more at once
+                f32x4 YD[NT];
 #pragma unroll
-                    for (int it = 0; it < NT; ++it) {
-                        const int i = 16 * it + c;
-                        float d = 0.0f;
-                        const f32x4 x = O::ld4(lds.X + i * RX + kLinCols * w + 4 * g);
+                for (int it = 0; it < NT; ++it) YD[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) d = fmaf(x[v], Y[it][v], d);
-                        const int at = rev ? cnt - 1 - i : i;   // the token's place in the chunk
-                        int place = win + at + 1;
-                        if (strong) place = rev ? at + 1 - cnt : at + 1;
-                        sum = fmaf(static_cast<float>(rev ? -place : place), d, sum);
+                for (int k = 0; k < NN / 2; ++k) {
+                    Frag q[NT];
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + 32 * k, g);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = D[2 * k][e];
+                        x[e + 4] = D[2 * k + 1][e];
                     }
-                    dg += static_cast<double>(sum);
-                    // the last chunk of a head that counts inside chunks may be short
-                    if (strong && ps.dg_pairs && ch == nchunks - 1)
-                        dg += adjoint_dot() * static_cast<double>(static_cast<float>(cnt) * lds.pow[cnt]);
+                    const Frag d0 = O::term(x);
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) YD[it] = O::mma(d0, q[it], YD[it]);
+                    if constexpr (O::kSplit) rest_terms(x, q, YD);
                 }
+#pragma unroll
+                for (int it = 0; it < NT; ++it) {
+                    const f32x4 x = O::ld4(lds.X + (16 * it + c) * RX + kLinCols * w + 4 * g);
+                    const float steps = static_cast<float>(16 * it + c + 1);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) dgi = fmaf(x[v], fmaf(steps, Y[it][v], YD[it][v] * eo[it]), dgi);
+                }
+                dg += static_cast<double>(dgi);
             }
         }
 
-        fetch_vx(next, next_cnt);
+        if constexpr (!kLate) {
+            if constexpr (DG) fetch_kq(next, next_cnt);
+            fetch_vx(next, next_cnt);
+        }
         // v as the products over tokens read it
         Frag vf[NS];
 #pragma unroll
@@ -671,6 +645,14 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
         // factor next to 1 applied chunk after chunk would drift by its own
         // rounding), then the chunk's tokens
         const float em = cnt == C ? em_full : em_short;
+        if constexpr (DG) {
+            // the derivative, with the steps that the state takes here
+            const float f = static_cast<float>(cnt) * lds.pow[cnt];
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) D[nt][v] = fmaf(S[nt][v], f, fmaf(D[nt][v], em, D[nt][v]));
+        }
 #pragma unroll
         for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
@@ -682,9 +664,23 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = O::get(vf[s], e) * (e < 4 ? w0[e] : w1[e - 4]);
-            Frag v0 = O::term(x), v1, v2;
-            if constexpr (O::kSplit) v1 = O::term(x);
-            if constexpr (O::kSplit && MODE != kLinFwd) v2 = O::term(x);
+            float y[DG ? 8 : 1];
+            if constexpr (DG)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = x[e] * static_cast<float>(cnt - 1 - (32 * s + 8 * g + e));
+            Frag v0 = O::term(x), v1, v2, d0, d1, d2;
+            if constexpr (O::kSplit) {
+                v1 = O::term(x);
+                if constexpr (EXACT) v2 = O::term(x);
+            }
+            if constexpr (DG) {
+                d0 = O::term(y);
+                if constexpr (O::kSplit) {
+                    d1 = O::term(y);
+                    d2 = O::term(y);
+                }
+            }
+            if constexpr (!DG) __builtin_amdgcn_sched_barrier(0);
             constexpr int U = 4;   // independent blocks between the terms of one
 #pragma unroll
             for (int n0 = 0; n0 < NN; n0 += U) {
@@ -696,21 +692,25 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
                 if constexpr (O::kSplit)
 #pragma unroll
                     for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v1, S[n0 + u]);
-                if constexpr (O::kSplit && MODE != kLinFwd) {
-                    if (exact)
+                if constexpr (O::kSplit && EXACT && !DG) __builtin_amdgcn_sched_barrier(0);
+                if constexpr (O::kSplit && EXACT)
 #pragma unroll
-                        for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v2, S[n0 + u]);
+                    for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v2, S[n0 + u]);
+                if constexpr (DG) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) D[n0 + u] = O::mma(kf[u], d0, D[n0 + u]);
+                    if constexpr (O::kSplit) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) D[n0 + u] = O::mma(kf[u], d1, D[n0 + u]);
+#pragma unroll
+                        for (int u = 0; u < U; ++u) D[n0 + u] = O::mma(kf[u], d2, D[n0 + u]);
+                    }
                 }
             }
         }
-        if constexpr (kBwd) {
-            // where two windows meet, the state and the adjoint are kept for
-            // linear_attn_marks_kernel
-            if (ps.marks != nullptr && !strong) {
-                const int64_t at = rev ? first : first + cnt;
-                if (at % kLinWindow == 0 && at > 0 && at < ntok)
-                    store_state(ps.marks + ((bh * a.nseg + seg) * a.nmark + at / kLinWindow - 1) * state_elems);
-            }
+        if constexpr (kLate) {
+            fetch_kq(next, next_cnt);
+            fetch_vx(next, next_cnt);
         }
         __syncthreads();
 
@@ -745,16 +745,7 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
         }
     }
 
-    // the walk's end: the state leaves for the caller, or (kLinState) for the
-    // join of the segments
-    float* sout = nullptr;
-    if constexpr (kState) {
-        sout = ps.seg_in + (bh * a.nseg + seg) * state_elems;
-    } else {
-        const bool last = seg == (rev ? 0 : a.nseg - 1);
-        if (last && ps.s_out != nullptr) sout = ps.s_out + bh * state_elems;
-    }
-    if (sout != nullptr) store_state(sout);
+    if (sout != nullptr) store_state(sout + (kState ? bh * a.nseg + seg : bh) * state_elems);
     if constexpr (!kState) {
         // rows behind the sequence's end: zeros
         const int64_t z0 = end > seg0 ? end : seg0;
@@ -766,21 +757,67 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
             else static_cast<__bf16*>(ps.out)[at] = static_cast<__bf16>(0.0f);
         }
     }
-    if constexpr (kBwd) {
-        if (dg_out != nullptr) {
-            if (ps.dg_pairs && ntok > 0 && !strong)
-                dg += adjoint_dot() * static_cast<double>((ntok - 1) % kLinWindow + 1);
+    if constexpr (DG) {
+        const float* adj = a.nseg > 1 ? a.adj_in + (bh * a.nseg + seg) * state_elems
+                                      : (a.dhL != nullptr ? a.dhL + bh * state_elems : nullptr);
+        if (adj != nullptr && ntok > 0) {
+            float sum = 0.0f;
+            load_state(adj, [&](int nt, f32x4 x) {
 #pragma unroll
-            for (int m = 1; m < kWave; m *= 2) dg += __shfl_xor(dg, m);
-            if (lane == 0) lds.red[w] = dg;
-            __syncthreads();
-            if (tid == 0) {
-                double sum = 0.0;
-                for (int u = 0; u < WAVES; ++u) sum += lds.red[u];
-                *dg_out = sum;
-            }
+                for (int v = 0; v < 4; ++v) sum = fmaf(D[nt][v], x[v], sum);
+            });
+            dg += static_cast<double>(sum);
+        }
+#pragma unroll
+        for (int m = 1; m < kWave; m *= 2) dg += __shfl_xor(dg, m);
+        if (lane == 0) lds.red[w] = dg;
+        __syncthreads();
+        if (tid == 0) {
+            double sum = 0.0;
+            for (int u = 0; u < WAVES; ++u) sum += lds.red[u];
+            *dg_out = sum;
         }
     }
+}
+
+template <int IO, int DC, int MODE>
+__global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(LinArgs a) {
+    __shared__ LinLds<IO, DC, MODE> lds;
+    // which (row, head, segment, pass, column block); neighbours in this
+    // order read the same rows and share an XCD's L2. The pass that forms the
+    // decay's gradient takes longest and goes first; the others run beside it.
+    const bool ordered = MODE == kLinBwd && a.dg != nullptr;
+    const uint32_t most = ordered ? gridDim.x / 3 : 0;
+    const bool first = blockIdx.x < most;
+    uint32_t id = first ? xcd_order(blockIdx.x, most) : xcd_order(blockIdx.x - most, gridDim.x - most);
+    uint32_t up = id / a.nblk;
+    const int blk = static_cast<int>(id - up * a.nblk);
+    id = up;
+    int ip = kLinPassDq;
+    if (!first) {
+        const uint32_t np = ordered ? 2 : a.npass;
+        up = id / np;
+        ip = static_cast<int>(id - up * np) + (ordered ? 1 : 0);
+        id = up;
+    }
+    const uint32_t nsegs = MODE == kLinState ? a.nseg - 1 : a.nseg;
+    up = id / nsegs;
+    const int seg = static_cast<int>(id - up * nsegs);
+    const uint32_t row = up / a.heads;
+    const int hd = static_cast<int>(up - row * a.heads);
+    if constexpr (MODE == kLinBwd) {
+        if (first) {
+            linear_attn_walk<IO, DC, MODE, true, true>(a, lds, ip, blk, seg, up, row, hd);
+            return;
+        }
+    }
+    // a state that the caller gets
+    const LinPass& ps = a.pass[ip];
+    const bool leaves = ps.s_out != nullptr && seg == (ps.rev ? 0 : a.nseg - 1);
+    if (IO == kIoBF16 && (MODE == kLinState ? a.exact != 0 : leaves))
+        linear_attn_walk<IO, DC, MODE, IO == kIoBF16, false>(a, lds, ip, blk, seg, up, row, hd);
+    else
+        linear_attn_walk<IO, DC, MODE, false, false>(a, lds, ip, blk, seg, up, row, hd);
 }
 
 }  // namespace

@@ -13,27 +13,25 @@ sum, so two of the three together: sqrt(2) * 1.7e-3 = 2.4e-3, taken as 4e-3.
 Elementwise: 2^-8 of the value for the output and 2^-8 of terms that add up
 incoherently to the largest outputs; 2.5 * 2^-8 < 1e-2 of the largest value.
 
-fp32 results from bf16 inputs: weights times v in two bf16 terms leave
-1.7e-3 squared = 2.9e-6, taken as 6e-6; 3e-5 of the largest elementwise.
-
-fp32 inputs: sums of n = dk + 64 + chunks terms in fp32 round n times, errors
+fp32 results, from fp32 or bf16 inputs (products of bf16 values are exact and
+what the kernel splits into three bf16 terms keeps 2^-25): sums of n = dk + 64 + chunks terms in fp32 round n times, errors
 independent, each 2^-24 / sqrt(3) of a partial sum: sqrt(400) * 3.5e-8 = 7e-7
 for the longest here; the powers of the decay add 2^-23; taken as 3e-6, and
 1.5e-5 of the largest elementwise.
 
-The decay's gradient weighs a token's terms, formed with fp32 accuracy (three
-bf16 terms), by its place in a window of at most 1024 tokens, and what remains
-is of the size of the sum of |dS_t . lam S_(t-1)| over tokens: sqrt(L) * 1e-7 *
-(place L against a memory of two tokens and more) is the worst, 700^0.5 * 1e-7
-* 10 = 2.6e-5 of it for the longest here; taken as 3e-5. Where the decay's own
-power is below 2^-126, the smallest normal fp32 number, fp32 holds none of it:
-the gradient may be off by 2^-126 times the sum of |S| |dS|, under 1e8 here.
+The decay's gradient adds terms of the same fp32 accuracy, 7e-7 of their size,
+with errors that add up no faster than the terms. It is bounded by the sum over
+tokens of |dS_t . lam S_(t-1)|, in which the pairs of tokens that a token lies
+between add up with any sign, to about the root of their number (under 200
+here): sqrt(200) * 7e-7 = 1e-5 of that sum. Where the decay's own power is below
+2^-126, the smallest normal fp32 number, fp32 holds none of it: the gradient may
+be off by 2^-126 times the sum of |S| |dS|, under 1e8 here.
 """
 import torch
 
-TWO_NORM = {"bf16": 4e-3, "f32_from_bf16": 6e-6, "f32": 3e-6}
-LARGEST = {"bf16": 1e-2, "f32_from_bf16": 3e-5, "f32": 1.5e-5}
-DECAY_GRAD = 3e-5
+TWO_NORM = {"bf16": 4e-3, "f32": 3e-6}
+LARGEST = {"bf16": 1e-2, "f32": 1.5e-5}
+DECAY_GRAD = 1e-5
 
 
 def check(got, want, kind, what):
@@ -109,11 +107,10 @@ def attn_token(h, q, k, v, log_decay, scale=None):
 
 def check_grads(got, want, dtype, what):
     kind = "bf16" if dtype == torch.bfloat16 else "f32"
-    state = "f32_from_bf16" if dtype == torch.bfloat16 else "f32"
     for name in ("dq", "dk", "dv"):
         check(got[name], want[name], kind, f"{what} {name}")
     if got["dh0"] is not None:
-        check(got["dh0"], want["dh0"], state, f"{what} dh0")
+        check(got["dh0"], want["dh0"], "f32", f"{what} dh0")
     if got["dlog_decay"] is not None:
         err = (got["dlog_decay"].double().cpu() - want["dlog_decay"]).abs()
         bound = DECAY_GRAD * want["decay_scale"] + 2.0 ** -126 * 1e8

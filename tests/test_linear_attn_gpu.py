@@ -57,13 +57,13 @@ def _bwd(i, **kw):
 def _check_all(i, what, segments=(0,), **kw):
     o, hL, grads = ref.attn(**i, **kw)
     dt = i["q"].dtype
-    kind, state = ("bf16", "f32_from_bf16") if dt == BF else ("f32", "f32")
+    kind = "bf16" if dt == BF else "f32"
     for seg in segments:
         _say(f"case {what} segment_len={seg}")
         got_o, got_h = _fwd(i, segment_len=seg, **kw)
         torch.cuda.synchronize()
         ref.check(got_o, o, kind, f"{what} o")
-        ref.check(got_h, hL, state, f"{what} hL")
+        ref.check(got_h, hL, "f32", f"{what} hL")
         got = _bwd(i, segment_len=seg, **kw)
         torch.cuda.synchronize()
         ref.check_grads(got, grads, dt, what)
@@ -134,12 +134,12 @@ def test_decays(dtype):
     # none, one that underflows within a chunk, one that forgets at once
     i = _make(1, 190, 5, 5, 64, 64, dtype, seed=4, decay=[0.0, -1e-6, -2.0, -100.0, -math.inf])
     o, hL, grads = ref.attn(**{**i, "log_decay": i["log_decay"].clamp(min=-1e4)})
-    kind, state = ("bf16", "f32_from_bf16") if dtype == BF else ("f32", "f32")
+    kind = "bf16" if dtype == BF else "f32"
     for seg in (0, 64):
         _say(f"case decays {dtype} segment_len={seg}")
         got_o, got_h = _fwd(i, segment_len=seg)
         ref.check(got_o, o, kind, "o")
-        ref.check(got_h, hL, state, "hL")
+        ref.check(got_h, hL, "f32", "hL")
         ref.check_grads(_bwd(i, segment_len=seg), grads, dtype, "decays")
 
 
@@ -204,7 +204,7 @@ def test_split_sequence_carries_state_in_place():
     torch.cuda.synchronize()
     ref.check(torch.cat(outs, 1), o, "bf16", "o")
     # two calls' two-term roundings and one more chunk edge: still the state's bound
-    ref.check(state, hL, "f32_from_bf16", "state")
+    ref.check(state, hL, "f32", "state")
 
 
 def test_empty_calls():
@@ -260,7 +260,7 @@ def test_tokens_continue_a_prompt():
                                           i["log_decay"])[:, None])
     torch.cuda.synchronize()
     ref.check(torch.cat(outs, 1), o, "bf16", "o")
-    ref.check(h, hL, "f32_from_bf16", "h")
+    ref.check(h, hL, "f32", "h")
 
 
 def test_offsets_past_32_bits():
@@ -277,7 +277,7 @@ def test_offsets_past_32_bits():
     o1, h1 = ms.linear_attn_fwd(*one, decay, segment_len=16384)
     torch.cuda.synchronize()
     ref.check(o[-1:], o1, "bf16", "o")
-    ref.check(h[-1:], h1, "f32_from_bf16", "h")
+    ref.check(h[-1:], h1, "f32", "h")
 
 
 @pytest.mark.parametrize("seg", [0, 64])
