@@ -59,29 +59,30 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The automatic division. Segments add a pass over keys and values and a
 // join, so a sequence is cut only where its chunks, walked one after the other,
 // would leave the chip idle. The time of a plan with n segments is taken as
-//     (chunks / n * walk + entry) * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
-// with `entry` a workgroup's beginning and end, `summary` the states' pass,
-// `join` its launches and `walk` the time that 64 tokens take with all
-// workgroups on the chip. Alone on a compute unit they take `chunk`; a second
-// workgroup there makes it 1.57 times that, a third waits; of the wide kernels
-// a unit holds one. The backward's pass of dq, where the decay's gradient is
-// formed, takes `longest` and goes first, the other two passes run beside and
-// behind it (whether that gradient is wanted is not known here).
+//     (chunks / n * chunk + entry) * load * (n > 1 ? 1 + summary : 1) + (n > 1 ? join : 0)
+// with `chunk` the time of 64 tokens alone on a compute unit, `entry` a
+// workgroup's beginning and end, `summary` the states' pass, `join` its launches
+// and `load` what sharing the chip costs: a second workgroup on a unit makes a
+// round 1.57 times as long, a third waits for the next; of the wide kernels a
+// unit holds one. The backward's pass of dq, where the decay's gradient is
+// formed, takes `longest` for 64 tokens and goes first, the other two passes
+// run beside and behind it (whether that gradient is wanted is not known here).
 // Microseconds measured on MI355X with one workgroup per unit; examples, cut
 // by this rule against not cut: one sequence of 65536, 16 heads of 128: 364 us
 // with 16 segments against 2.9 ms; 8 x 2048 x 16 heads of 128: 77 us whole
 // against 105 with 2, gradients 267 whole against 300 with 2; 4 x 1024 x 16
 // heads of 64: 27 us whole against 30 with 2, gradients 58 with 4 against 67;
-// gradients in fp32 of 2 x 333 x 6 heads: 40 us with 6 against 77, of 2 x 2048
-// x 8 heads of 200 x 168: 404 us with 4 against 1152.
+// gradients in fp32 of 2 x 333 x 6 heads: 40 us with 6 against 77; 2 x 2048 x
+// 8 heads of 200 x 168: 51 us with 5 against 98, gradients 158 with 2 against
+// 225.
 struct PlanCost {
     double chunk[2][3];   // [fp32, bf16][head width 64, 128, 256]
     double entry[3];
     double summary;
 };
-constexpr PlanCost kFwdCost = {{{4.4, 8.0, 18.4}, {1.45, 2.3, 3.6}}, {2.0, 3.0, 9.0}, 0.5};
-constexpr PlanCost kBwdCost = {{{4.3, 6.7, 19.0}, {1.95, 2.6, 4.6}}, {2.0, 3.0, 5.0}, 0.35};
-constexpr double kBwdLongest[2][3] = {{7.5, 13.0, 36.0}, {3.6, 5.3, 16.3}};
+constexpr PlanCost kFwdCost = {{{4.4, 8.0, 10.8}, {1.45, 2.3, 2.75}}, {2.0, 3.0, 9.0}, 0.5};
+constexpr PlanCost kBwdCost = {{{4.3, 6.7, 11.0}, {1.95, 2.6, 3.0}}, {2.0, 3.0, 5.0}, 0.35};
+constexpr double kBwdLongest[2][3] = {{7.5, 13.0, 19.5}, {3.6, 5.3, 6.6}};
 constexpr double kJoinCost = 14.0, kSharedUnit = 1.57;
 constexpr int64_t kMinSegment = 64;
 
@@ -96,20 +97,19 @@ int64_t choose_segments(bool bwd, int io, int dc_pad, int64_t seqlen, int64_t un
     int64_t best = 1;
     double least = 0.0;
     for (int64_t n = 1; n <= ceil_div(seqlen, kMinSegment) && (n == 1 || all * n <= 8 * int64_t(cu)); ++n) {
-        double walk;
+        double load;
         if (bwd) {
-            const double sum = (longest + 2.0 * chunk) * static_cast<double>(units * n) / cu;
-            const double least_walk = longest * (wide || all * n <= cu ? 1.0 : 1.3);
-            walk = sum * (wide ? 1.0 : kSharedUnit / 2);
-            if (walk < least_walk) walk = least_walk;
+            const double sum = (1.0 + 2.0 * chunk / longest) * static_cast<double>(units * n) / cu;
+            load = sum * (wide ? 1.0 : kSharedUnit / 2);
+            const double alone = wide || all * n <= cu ? 1.0 : 1.3;   // beside shorter ones
+            if (load < alone) load = alone;
         } else {
             const int64_t round = wide ? cu : 2 * int64_t(cu), rest = all * n % round;
-            const double full = wide ? 1.0 : kSharedUnit;
-            walk = chunk * (static_cast<double>(all * n / round) * full +
-                            (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : kSharedUnit)));
+            load = static_cast<double>(all * n / round) * (wide ? 1.0 : kSharedUnit) +
+                   (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : kSharedUnit));
         }
         const double each = static_cast<double>(ceil_div(ceil_div(seqlen, n), kSegUnit));
-        double t = (each < chunks ? each : chunks) * walk + cost.entry[width];
+        double t = ((each < chunks ? each : chunks) * (bwd ? longest : chunk) + cost.entry[width]) * load;
         if (n > 1) t = t * (1.0 + cost.summary) + kJoinCost;
         if (n == 1 || t < least) {
             least = t;
@@ -124,7 +124,7 @@ int64_t choose_segments(bool bwd, int io, int dc_pad, int64_t seqlen, int64_t un
 int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, LinPlan* p) {
     const int wide = passes == 1 ? c.dv : (c.dk > c.dv ? c.dk : c.dv);
     const int dc_pad = mamba::lin_padded(passes == 1 ? c.dk : wide);
-    const int64_t blocks = mamba::lin_blocks(dc_pad, wide);
+    const int64_t blocks = mamba::lin_blocks(wide);
     p->seg_len = c.seqlen > 0 ? c.seqlen : 1;
     p->nseg = 1;
     if (c.batch == 0 || c.heads == 0 || c.seqlen == 0) return MAMBA_OK;

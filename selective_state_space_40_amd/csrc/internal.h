@@ -166,13 +166,16 @@ constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
 // passes of the backward launch
 constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;   // dq first
 constexpr int kLinMaxDim = 256;   // widest head
-// Waves of a workgroup and output columns of a wave. 64 columns leave two
-// workgroups on a compute unit (prompts of 8 x 2048 x 16 heads of 128: 76 us
-// against 95 us with 128 columns, their gradients 313 against 326); the wide
-// kernels' registers and LDS leave one, of 128 columns then (2 x 2048 x 8 heads
-// of 200 x 168: 55 us against 62 us with 64, gradients 175 against 194).
-constexpr int lin_waves(int dc_pad) { return dc_pad == 256 ? 8 : 4; }
-constexpr int kLinCols = 16;
+// Output columns of a workgroup; its waves have 16 each. Of heads wider than 128
+// two waves share 16 columns, each with half of the state's rows, since a wave
+// that holds all 256 leaves no registers (12 x 1500 x 10 heads of 192 x 72: 77 us
+// against 104 with whole columns, 128 to a workgroup; gradients of 2 x 2048 x
+// 8 heads of 200 x 168: 158 against 190). For 128 rows the split costs more LDS
+// reads than it saves waiting (8 x 2048 x 16 heads of 128: 94 us against 77).
+// 64 columns leave two workgroups on a compute unit (95 us with 128).
+constexpr int kLinBlock = 64, kLinCols = 16;
+constexpr int lin_split(int dc_pad) { return dc_pad == 256 ? 2 : 1; }
+constexpr int lin_waves(int dc_pad) { return kLinBlock / kLinCols * lin_split(dc_pad); }
 // Tokens of a chunk: fp32 takes half in the same LDS.
 constexpr int kLinChunkBF16 = 64, kLinChunkF32 = 32;
 
@@ -237,11 +240,9 @@ struct LinPlan {
     int nseg = 1;
 };
 
-// Head width the kernels are built for, and column blocks of `out` columns.
+// Head width the kernels are built for, and blocks of `out` columns.
 constexpr int lin_padded(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : 256); }
-constexpr int lin_blocks(int dc_pad, int out) {
-    return (out + lin_waves(dc_pad) * kLinCols - 1) / (lin_waves(dc_pad) * kLinCols);
-}
+constexpr int lin_blocks(int out) { return (out + kLinBlock - 1) / kLinBlock; }
 
 size_t linear_attn_workspace_bytes(const LinearAttnCall& c, const LinPlan& p, bool bwd);
 hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s);

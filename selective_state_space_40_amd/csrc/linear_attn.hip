@@ -207,7 +207,7 @@ BwdScratch bwd_scratch(const LinearAttnCall& c, const LinPlan& p, int nblk) {
 
 int max_dim(const LinearAttnCall& c) { return c.dk > c.dv ? c.dk : c.dv; }
 
-int bwd_blocks(const LinearAttnCall& c) { return lin_blocks(lin_padded(max_dim(c)), max_dim(c)); }
+int bwd_blocks(const LinearAttnCall& c) { return lin_blocks(max_dim(c)); }
 
 LinArgs base_args(const LinearAttnCall& c, const LinPlan& p) {
     LinArgs a = {};
@@ -296,7 +296,7 @@ size_t linear_attn_workspace_bytes(const LinearAttnCall& c, const LinPlan& p, bo
 
 hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s) {
     LinArgs a = base_args(c, p);
-    a.nblk = lin_blocks(lin_padded(c.dk), c.dv);
+    a.nblk = lin_blocks(c.dv);
     a.pass[0] = forward_pass(c);
     a.pass[0].seg_in = static_cast<float*>(ws);
     a.exact = c.hL != nullptr;
@@ -345,7 +345,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         adj.out32 = shared;
         if (p.nseg > 1) {
             LinArgs a = base_args(c, p);
-            a.nblk = lin_blocks(lin_padded(c.dk), c.dv);
+            a.nblk = lin_blocks(c.dv);
             a.npass = 2;
             a.exact = dg != nullptr || c.dh0 != nullptr;
             a.pass[0] = states;

@@ -16,15 +16,17 @@
 //                (k, q, do) -> dv, adjoint dS, reversed
 //                (v, do, q) -> dk, adjoint dS^T, reversed
 //
-// Work mapping. A workgroup of 4 waves (8 for keys wider than 128) walks the
-// chunks of one (row, head, segment) for 16 output columns per wave. The
-// state's columns belong to the same wave, so its S (all DC rows, 16 columns)
-// stays in the accumulators for the whole walk, and the accumulator of two
-// 16 x 16 blocks is, up to a fixed order of the rows, the operand of the
-// product q S: the state passes through neither LDS nor another wave. The
-// chunk's q, k and v rows are staged in LDS; the next chunk's are loaded into
-// registers meanwhile. The C x C matrix P is split over the waves by 16 x 16
-// blocks and exchanged through LDS.
+// Work mapping. A workgroup walks the chunks of one (row, head, segment) for
+// 64 output columns, 16 to a wave. The state's columns belong to the same wave,
+// so its S (all DC rows, 16 columns) stays in the accumulators for the whole
+// walk, and the accumulator of two 16 x 16 blocks is, up to a fixed order of
+// the rows, the operand of the product q S: the state passes through neither
+// LDS nor another wave. Of heads wider than 128 two waves share 16 columns, each
+// with half of S's rows; they form q S for all of a chunk's tokens and exchange
+// halves, so that each goes on with half of the tokens. The chunk's q, k and v
+// rows are staged in LDS; the next chunk's are loaded into registers meanwhile.
+// The C x C matrix P is split over the waves by 16 x 16 blocks and exchanged
+// through LDS.
 //
 // bf16 operands. q, k and v enter the products exactly. P is rounded to bf16
 // (its effect on a bf16 output is that of the output's own rounding). What
@@ -242,7 +244,8 @@ struct LinLds {
     typedef typename LinOps<IO>::T T;
     static constexpr int kC = LinOps<IO>::kChunk;
     static constexpr int kRowP = kC + LinOps<IO>::kPadP;
-    static constexpr int kThreads = WAVES * kWave, kCols = WAVES * kLinCols;
+    static constexpr int kThreads = WAVES * kWave, kCols = kLinBlock;
+    static constexpr int kSplit = lin_split(DC);
     typedef Tile<IO, kThreads, DC, LinOps<IO>::kPadK> TileK;
     typedef Tile<IO, kThreads, kCols, LinOps<IO>::kPad> TileV;
     typedef Tile<IO, kThreads, DC, LinOps<IO>::kPad> TileQ;
@@ -252,6 +255,8 @@ struct LinLds {
     alignas(16) T Q[MODE == kLinState ? 8 : kC * TileQ::kRow];
     alignas(16) T X[MODE == kLinBwd ? kC * TileX::kRow : 8];
     alignas(16) T P[MODE == kLinState ? 8 : kC * kRowP];
+    // half of q S, 16 x 16 blocks as the accumulators hold them
+    alignas(16) f32x4 half[kSplit > 1 && MODE != kLinState ? WAVES * (kC / 32) * kWave : 1];
     alignas(16) float W[kC];      // weight of token j in the state update
     float pow[kC + 1];            // lam^n
     float fac[MODE == kLinBwd ? 2 * kC : 1];   // P's factor n tokens apart at n + C: zero for n < 0
@@ -290,9 +295,11 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     constexpr int C = O::kChunk;
     constexpr int NT = C / 16;            // blocks of 16 tokens
     constexpr int NS = C / 32;            // product steps over tokens
-    constexpr int NN = DC / 16;           // blocks of 16 state rows
     constexpr int WAVES = lin_waves(DC);
-    constexpr int DOB = WAVES * kLinCols; // columns per workgroup
+    constexpr int SPLIT = lin_split(DC);
+    constexpr int NN = DC / SPLIT / 16;   // a wave's blocks of 16 state rows
+    constexpr int OT = NT / SPLIT;        // and of 16 tokens of the output
+    constexpr int DOB = kLinBlock;   // columns per workgroup
     constexpr int THREADS = WAVES * kWave;
     constexpr bool kState = MODE == kLinState, kBwd = MODE == kLinBwd;
     typedef LinLds<IO, DC, MODE> Lds;
@@ -301,6 +308,9 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     const int lane = tid & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane & 15, g = lane >> 4;
+    // this wave's columns of the block, and its part of the state's rows
+    const int wc = SPLIT > 1 ? w % (WAVES / SPLIT) : w, part = SPLIT > 1 ? w / (WAVES / SPLIT) : 0;
+    const int n0w = part * (DC / SPLIT);
 
     const LinPass& ps = a.pass[ip];
     const bool rev = ps.rev != 0;
@@ -374,7 +384,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     // S: block nt holds rows state_row(nt, g) + v of column p0 + 16 w + c, so
     // that blocks 2 k and 2 k + 1 of a lane are the rows 32 k + 8 g + 0..7 of a
     // fragment
-    const int pc = p0 + kLinCols * w + c;
+    const int pc = p0 + kLinCols * wc + c;
     const int64_t state_elems = static_cast<int64_t>(dc) * dout;
     const int state_bytes = dc * dout * 4;
     // a state in memory, read or written by buffer offsets: rows and columns
@@ -385,7 +395,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     const bool runs = kBwd && sn == 1;   // a block's 4 rows lie together (transposed state)
     // dc is a multiple of 4: a block's 4 rows are all in or all out
     auto state_offset = [&](int nt) {
-        const int n = state_row(nt, g);
+        const int n = n0w + state_row(nt, g);
         const int off = (n * sn + pc * sp) * 4;
         return ((n < dc) & (pc < dout)) ? off : kPastEnd;
     };
@@ -424,6 +434,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     constexpr int GR = WAVES / NT, OWN = NT > GR ? NT / GR : 1;
     const int jt = w % NT, grp = w / NT;
     const bool forms = grp < NT;
+    const int it0 = SPLIT > 1 ? part * OT : 0;   // the first of this wave's blocks of the output
     float eo[NT], fac[DG ? 1 : OWN][4];
     if constexpr (DG) {
         for (int n = tid; n < 2 * C; n += THREADS) lds.fac[n] = n < C ? 0.0f : a.scale * lds.pow[n - C];
@@ -449,7 +460,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     const bool wide = IO == kIoF32 || (kBwd && ps.out32);
     const int osize = wide ? 4 : 2;
     const HeadRows ro(ps.out, row0, a.heads, hd, dout, osize);
-    const int po = p0 + kLinCols * w + 4 * g;
+    const int po = p0 + kLinCols * wc + 4 * g;
     const int oo = po < dout ? (rev ? -c : c) * ro.stride + po * osize : kPastEnd;
     double dg = 0.0;   // this thread's part of the decay's gradient
     f32x4 D[DG ? NN : 1];   // the state's derivative
@@ -491,7 +502,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         // count the stores behind them and need not wait for those
         const __amdgpu_buffer_rsrc_t none = lin_rsrc(ps.out, 0);
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
+        for (int u = 0; u < OT; ++u) {
             if (wide) __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, none, 16 * u, 0, 0);
             else __builtin_amdgcn_raw_buffer_store_b64(u32x2{0, 0}, none, 16 * u, 0, 0);
         }
@@ -512,10 +523,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         __syncthreads();
         // the next chunk's loads go out in two groups, as the units that
         // address them take as long as a chunk's products; with a second state
-        // the registers for them are free behind its product with q only, for
-        // wide heads behind both states' updates (gradients in fp32, 2 x 2048 x
-        // 8 heads of 200 x 168: 419 us, 450 with spills)
-        constexpr bool kLate = DG && DC == 256;
+        // the registers for them are free behind its product with q only
         int64_t next;
         int next_cnt;
         chunk_at(ch + 1, next, next_cnt);
@@ -541,7 +549,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
             for (int k = 0; k < NN / 2; ++k) {
                 Frag q[NT];
 #pragma unroll
-                for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + 32 * k, g);
+                for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + n0w + 32 * k, g);
                 if constexpr (GR == 1) {
                     const Frag kf = O::nat(lds.K + (16 * jt + c) * RK + 32 * k, g);
 #pragma unroll
@@ -609,7 +617,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 for (int k = 0; k < NN / 2; ++k) {
                     Frag q[NT];
 #pragma unroll
-                    for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + 32 * k, g);
+                    for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + n0w + 32 * k, g);
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -623,23 +631,31 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 }
 #pragma unroll
                 for (int it = 0; it < NT; ++it) {
-                    const f32x4 x = O::ld4(lds.X + (16 * it + c) * RX + kLinCols * w + 4 * g);
+                    const f32x4 x = O::ld4(lds.X + (16 * it + c) * RX + kLinCols * wc + 4 * g);
                     const float steps = static_cast<float>(16 * it + c + 1);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) dgi = fmaf(x[v], fmaf(steps, Y[it][v], YD[it][v] * eo[it]), dgi);
                 }
                 dg += static_cast<double>(dgi);
             }
+            if constexpr (SPLIT > 1) {
+                // this wave goes on with the tokens of its part; the others'
+                // half of q S is left for the wave that has them
+                f32x4* to = lds.half + ((1 - part) * (WAVES / SPLIT) + wc) * OT * kWave + lane;
+#pragma unroll
+                for (int u = 0; u < OT; ++u) {
+                    to[u * kWave] = part == 0 ? Y[OT + u] : Y[u];
+                    Y[u] = part == 0 ? Y[u] : Y[OT + u];
+                }
+            }
         }
 
-        if constexpr (!kLate) {
-            if constexpr (DG) fetch_kq(next, next_cnt);
-            fetch_vx(next, next_cnt);
-        }
+        if constexpr (DG) fetch_kq(next, next_cnt);
+        fetch_vx(next, next_cnt);
         // v as the products over tokens read it
         Frag vf[NS];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) vf[s] = O::template tr<RV, 4>(lds.V, 32 * s, kLinCols * w, c, g);
+        for (int s = 0; s < NS; ++s) vf[s] = O::template tr<RV, 4>(lds.V, 32 * s, kLinCols * wc, c, g);
 
         // (4) the state: S + (lam^cnt - 1) S, which rounds only the change (a
         // factor next to 1 applied chunk after chunk would drift by its own
@@ -681,12 +697,12 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 }
             }
             if constexpr (!DG) __builtin_amdgcn_sched_barrier(0);
-            constexpr int U = 4;   // independent blocks between the terms of one
+            constexpr int U = NN < 4 ? NN : 4;   // independent blocks between the terms of one
 #pragma unroll
             for (int n0 = 0; n0 < NN; n0 += U) {
                 Frag kf[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) kf[u] = O::template tr<RK, 8>(lds.K, 32 * s, state_row(n0 + u, 0), c, g);
+                for (int u = 0; u < U; ++u) kf[u] = O::template tr<RK, 8>(lds.K, 32 * s, n0w + state_row(n0 + u, 0), c, g);
 #pragma unroll
                 for (int u = 0; u < U; ++u) S[n0 + u] = O::mma(kf[u], v0, S[n0 + u]);
                 if constexpr (O::kSplit)
@@ -708,38 +724,39 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 }
             }
         }
-        if constexpr (kLate) {
-            fetch_kq(next, next_cnt);
-            fetch_vx(next, next_cnt);
-        }
         __syncthreads();
 
         // (5) P v onto q S, and out; the next chunk's tiles may be staged by
         // other waves meanwhile
         if constexpr (!kState) {
+            if constexpr (SPLIT > 1) {
+                const f32x4* from = lds.half + w * OT * kWave + lane;
 #pragma unroll
-            for (int it = 0; it < NT; ++it)
+                for (int u = 0; u < OT; ++u) Y[u] += from[u * kWave];
+            }
+#pragma unroll
+            for (int u = 0; u < OT; ++u)
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
-                    if (32 * s < 16 * (it + 1)) {
-                        const Frag p = O::nat(lds.P + (16 * it + c) * Lds::kRowP + 32 * s, g);
-                        Y[it] = O::mma(vf[s], p, Y[it]);
+                    if (32 * s < 16 * (it0 + u + 1)) {
+                        const Frag p = O::nat(lds.P + (16 * (it0 + u) + c) * Lds::kRowP + 32 * s, g);
+                        Y[u] = O::mma(vf[s], p, Y[u]);
                     }
             const __amdgpu_buffer_rsrc_t rs = ro.chunk(first, cnt);
             const int start = rev ? (cnt - 1) * ro.stride : 0, step = (rev ? -16 : 16) * ro.stride;
             if (wide) {
 #pragma unroll
-                for (int it = 0; it < NT; ++it)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[it]), rs,
-                                                           oo + (start + it * step), 0, 0);
+                for (int u = 0; u < OT; ++u)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, Y[u]), rs,
+                                                           oo + (start + (it0 + u) * step), 0, 0);
             } else {
 #pragma unroll
-                for (int it = 0; it < NT; ++it) {
+                for (int u = 0; u < OT; ++u) {
                     bf16x4 o;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[it][v]);
+                    for (int v = 0; v < 4; ++v) o[v] = static_cast<__bf16>(Y[u][v]);
                     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), rs,
-                                                          oo + (start + it * step), 0, 0);
+                                                          oo + (start + (it0 + u) * step), 0, 0);
                 }
             }
         }
