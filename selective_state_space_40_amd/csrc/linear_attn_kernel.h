@@ -59,6 +59,7 @@ namespace {
 
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8;
 typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
+typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -112,13 +113,16 @@ struct LinOps<kIoBF16> {
     }
     // The next term of fp32 values: x rounded, and x becomes what is left.
     static __device__ __forceinline__ Frag term(float (&x)[8]) {
-        Frag f;
+        uint32_t f[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[e] = static_cast<__bf16>(x[e]);
-            x[e] -= static_cast<float>(f[e]);
+        for (int e = 0; e < 8; e += 2) {
+            // one conversion for both, and its halves taken as fp32 again
+            const bf16x2 p = {static_cast<__bf16>(x[e]), static_cast<__bf16>(x[e + 1])};
+            f[e / 2] = __builtin_bit_cast(uint32_t, p);
+            x[e] -= __uint_as_float(f[e / 2] << 16);
+            x[e + 1] -= __uint_as_float(f[e / 2] & 0xffff0000u);
         }
-        return f;
+        return __builtin_bit_cast(Frag, f);
     }
     // four consecutive elements as fp32
     static __device__ __forceinline__ f32x4 ld4(const T* p) {
