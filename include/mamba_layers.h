@@ -57,7 +57,9 @@ extern "C" {
  *             the outputs; the result is the same up to rounding.
  *
  * dk and dv are multiples of MAMBA_LINATTN_DIM_UNIT up to
- * MAMBA_LINATTN_MAX_DIM, heads at most MAMBA_LINATTN_MAX_HEADS (else
+ * MAMBA_LINATTN_MAX_DIM, heads at most MAMBA_LINATTN_MAX_HEADS, and a launch,
+ * of 256 threads (512 for heads wider than 128) per row, head, segment and 64
+ * columns, three times that for gradients, counts fewer than 2^32 (else
  * MAMBA_ERR_UNSUPPORTED). What stands behind a row's length is never read.
  * Inside it a NaN or infinite value may, since the chunk products multiply the
  * causal mask's zeros by it, reach the earlier outputs of its own chunk of 64
@@ -108,6 +110,8 @@ int linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_hea
  * h   (batch, heads, dk, dv) fp32   read and updated in place
  * q   (batch, heads, dk), k (batch, kv_heads, dk), v (batch, kv_heads, dv)
  * o   (batch, heads, dv)            written
+ * batch * heads * ceil(dv / 64) * 256 is below 2^32 (else
+ * MAMBA_ERR_UNSUPPORTED).
  */
 int linear_attn_update(int64_t batch, int64_t heads, int64_t kv_heads, int64_t dk, int64_t dv,
                        int dtype, float* h, const void* q, const void* k, const void* v,
@@ -130,7 +134,8 @@ int linear_attn_update(int64_t batch, int64_t heads, int64_t kv_heads, int64_t d
  * eps          >= 0 and finite
  * mean, rstd   (rows, groups) fp32        optional: what the backward pass reads
  * dim is a multiple of groups (else MAMBA_ERR_INVALID_ARG) and dim / groups at
- * most MAMBA_NORM_MAX_DIM (else MAMBA_ERR_UNSUPPORTED). rows == 0 is a no-op.
+ * most MAMBA_NORM_MAX_DIM, dim at most 2^27, groups 2^22 and rows * groups 2^30
+ * (else MAMBA_ERR_UNSUPPORTED). rows == 0 is a no-op.
  */
 int layer_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int dtype, const void* x,
                    const float* weight, const float* bias, float eps, void* y, float* mean,

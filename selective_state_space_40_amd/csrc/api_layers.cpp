@@ -33,8 +33,11 @@ int check_aligned(const void* const (&ptrs)[N]) {
 
 // Tokens per chunk of the widest-chunked kernel: segments are whole chunks of it.
 constexpr int64_t kSegUnit = 64;
-// Workgroups a launch holds at most, and elements of a tensor.
-constexpr int64_t kMaxBlocks = int64_t(1) << 30;
+// Threads that a launch counts (32 bits), elements of a tensor, rows times
+// groups and channels of a norm.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+constexpr int64_t kMaxParts = int64_t(1) << 30;
+constexpr int64_t kMaxChannels = int64_t(1) << 27;
 constexpr int64_t kMaxElems = int64_t(1) << 48;
 
 int check_attn(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads, int64_t dk, int64_t dv,
@@ -127,9 +130,9 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
     const int64_t blocks = mamba::lin_blocks(wide);
     p->seg_len = c.seqlen > 0 ? c.seqlen : 1;
     p->nseg = 1;
-    if (c.batch == 0 || c.heads == 0 || c.seqlen == 0) return MAMBA_OK;
+    if (c.batch == 0 || c.heads == 0) return MAMBA_OK;
     int64_t seg = segment_len;
-    if (seg == 0) {
+    if (seg == 0 && c.seqlen > 0) {
         int cu = 0;
         const int st = mamba::current_cu_count(&cu);
         if (st != MAMBA_OK) return st;
@@ -142,7 +145,8 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
         p->seg_len = seg;
         p->nseg = static_cast<int>(n);
     }
-    if (c.batch * c.heads * p->nseg > kMaxBlocks / (passes * blocks)) return MAMBA_ERR_UNSUPPORTED;
+    const int64_t threads = passes * blocks * mamba::lin_waves(dc_pad) * mamba::kWave;
+    if (c.batch * c.heads * p->nseg > kMaxThreads / threads) return MAMBA_ERR_UNSUPPORTED;
     // the join's launch holds (row, head) in a 16-bit grid dimension
     if (p->nseg > 1 && c.batch * c.heads > 65535) {
         if (segment_len != 0) return MAMBA_ERR_UNSUPPORTED;
@@ -182,8 +186,8 @@ int check_norm(int64_t rows, int64_t dim, int64_t groups, int dtype) {
     if (rows < 0 || dim < 0 || groups < 1 || !known_dtype(dtype) || dim % groups != 0)
         return MAMBA_ERR_INVALID_ARG;
     if (dim / groups > MAMBA_NORM_MAX_DIM) return MAMBA_ERR_UNSUPPORTED;
-    if (dim > (int64_t(1) << 30) || (dim > 0 && rows > kMaxElems / dim) ||
-        rows > kMaxBlocks / groups)
+    if (dim > kMaxChannels || groups > kMaxChannels / 32 || (dim > 0 && rows > kMaxElems / dim) ||
+        rows > kMaxParts / groups)
         return MAMBA_ERR_UNSUPPORTED;
     return MAMBA_OK;
 }
@@ -289,7 +293,8 @@ int linear_attn_update(int64_t batch, int64_t heads, int64_t kv_heads, int64_t d
     const void* const ptrs[] = {h, q, k, v, log_decay, o};
     st = check_aligned(ptrs);
     if (st != MAMBA_OK) return st;
-    if (batch * heads > kMaxBlocks / (MAMBA_LINATTN_MAX_DIM / 64)) return MAMBA_ERR_UNSUPPORTED;
+    if (batch * heads > kMaxThreads / (mamba::lin_blocks(static_cast<int>(dv)) * mamba::kLinUpdateThreads))
+        return MAMBA_ERR_UNSUPPORTED;
     mamba::LinUpdateArgs a = {};
     a.batch = batch;
     a.heads = static_cast<int>(heads);

@@ -248,6 +248,8 @@ size_t linear_attn_workspace_bytes(const LinearAttnCall& c, const LinPlan& p, bo
 hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s);
 hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s);
 
+constexpr int kLinUpdateThreads = 256;
+
 struct LinUpdateArgs {
     int64_t batch;
     int heads, kv_heads, dk, dv, io;

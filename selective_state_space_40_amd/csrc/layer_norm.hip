@@ -8,7 +8,10 @@
 // part of n = dim / groups values is held by a team of 16, 64, 256 or 512
 // lanes, 8 to 32 values per lane in registers, so the mean, the centred sum
 // of squares and the output take one pass over memory; the variance is the
-// mean square of the centred values, not a difference of sums.
+// mean square of the centred values, not a difference of sums. 16384 x 5120 in
+// bf16: 66 us forward (5.1 TB/s), 109 us backward (4.6 TB/s with the sums of the
+// parameters' gradients, 105 for its main kernel and 4 for the columns'), where a
+// large copy reaches 5.5 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -146,11 +149,8 @@ __device__ __forceinline__ void load_params(const float* p, int64_t at, int n, i
 // The forward pass. A workgroup stays with one group of columns, keeps its
 // weights in registers and walks rows slot, slot + slots, ... (times its teams),
 // the next row's loads out while one is normed: read per row, the weights'
-// fp32 values were twice a bf16 row's bytes from the L2 (16384 x 5120: 78 us).
-// The forward pass. A workgroup stays with one group of columns, keeps its
-// weights in registers and walks rows slot, slot + slots, ... (times its teams),
-// the next row's loads out while one is normed: read per row, the weights'
-// fp32 values were twice a bf16 row's bytes from the L2 (16384 x 5120: 78 us).
+// fp32 values were twice a bf16 row's bytes from the L2 (16384 x 5120: 78 us
+// against 66).
 template <int IO, int TEAM, int CH, bool VEC>
 __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_fwd_kernel(NormArgs a, int slots) {
     constexpr int THREADS = TEAM > 256 ? TEAM : 256;

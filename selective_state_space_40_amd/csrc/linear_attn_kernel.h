@@ -46,6 +46,15 @@
 // needs no T but cancels down from a window's length to a memory's, and was 6
 // to 10 times less exact with windows of 1024 tokens. T starts at zero in every
 // segment, whose end's adjoint carries its steps on.
+//
+// What bounds it. A prompt of 8 x 2048 x 16 heads of 128 in bf16 takes 75 us
+// against 50 for its bytes at the rate of a large copy. It is a workgroup per
+// compute unit: each SIMD has one wave, whose steps (staging, q k^T and q S, P,
+// the state, P v) wait for each other at two barriers a chunk, with the matrix
+// cores 25% busy, the vector units 27% and LDS 31%. Cutting it into segments
+// for a second workgroup costs the states' pass more than the waiting (105 us).
+// The gradients (263 us, 87 by their bytes) hold two workgroups on a unit:
+// matrix cores 31%, vector units 40% busy, much of it the terms' splitting.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -96,6 +96,10 @@ def test_attention_refuses_bad_sequences_and_segments(lib):
         assert call(lib, batch=1 << 20, seqlen=1 << 20) == UNSUPPORTED
         assert call(lib, seqlen=(1 << 16) * 64 + 1, seg=64) == UNSUPPORTED   # too many segments
         assert call(lib, batch=65536, heads=1, kv_heads=1, seqlen=128, seg=64) == UNSUPPORTED
+    # more threads than a launch counts
+    for call in (_fwd, _bwd, _update):
+        assert call(lib, batch=1 << 18, heads=64, kv_heads=64, seqlen=64, seg=64) == UNSUPPORTED
+    assert _fwd(lib, batch=1 << 18, heads=64, kv_heads=64, seqlen=0) == UNSUPPORTED
     s, seg = _shape()
     assert lib.linear_attn_fwd_workspace_size(*s, seg, None) == INVALID
 
@@ -167,6 +171,8 @@ def test_norm_refuses_bad_arguments(lib):
         assert call(lib, dim=16385) == UNSUPPORTED
         assert call(lib, dim=1 << 31, groups=1 << 20) == UNSUPPORTED
         assert call(lib, rows=1 << 40) == UNSUPPORTED
+        assert call(lib, dim=1 << 28, groups=1 << 16) == UNSUPPORTED
+        assert call(lib, dim=1 << 26, groups=1 << 23) == UNSUPPORTED
         assert call(lib, rows=1 << 30, dim=64, groups=64) == UNSUPPORTED
     for eps in (-1.0, float("nan"), float("inf")):
         assert _norm(lib, eps=eps) == INVALID

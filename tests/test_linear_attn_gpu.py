@@ -100,6 +100,28 @@ def test_rows_of_different_lengths(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(200, 168), (144, 256), (256, 8), (8, 200)])
+def test_wide_heads_of_different_lengths(dk, dv, dtype):
+    # two waves share a wide head's columns; rows that are empty, end in the
+    # first chunk, at a chunk's end and inside the last, heads of every memory
+    lengths = [0, 1, 64, 150]
+    i = _make(len(lengths), 150, 4, 2, dk, dv, dtype, seed=dk + dv, lengths=lengths,
+              decay=[0.0, -0.01, -0.5, float("-inf")])
+    _check_all(i, f"wide {dk}x{dv} {dtype}", segments=(0, 64))
+
+
+def test_outputs_without_the_final_state():
+    # the state then enters with fewer terms, which bf16 outputs do not show
+    for dk, dv in ((64, 64), (128, 72), (192, 136)):
+        i = _make(2, 300, 2, 1, dk, dv, BF, seed=dk)
+        o, _, _ = ref.attn(**i)
+        for seg in (0, 128):
+            got, none = _fwd(i, return_state=False, segment_len=seg)
+            assert none is None
+            ref.check(got, o, "bf16", f"{dk}x{dv} o")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_padding_is_neither_read_nor_left(dtype):
     # NaN and infinity behind the rows' ends change nothing, outputs and
     # gradients there are zeros
