@@ -109,7 +109,7 @@ def test_groups(case, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_many_rows(dtype):
     # every workgroup takes several turns, the last ones of different length
-    for rows, dim in ((20011, 64), (5003, 520), (3001, 2050)):
+    for rows, dim in ((20011, 64), (5003, 520), (2051, 1531), (2100, 1536), (3001, 2050)):
         _say(f"case rows {rows} x {dim} {dtype}")
         _check(*_make(rows, dim, dtype, rows), 1, f"rows {rows} x {dim} {dtype}")
 
