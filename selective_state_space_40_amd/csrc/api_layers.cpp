@@ -86,34 +86,66 @@ struct PlanCost {
 constexpr PlanCost kFwdCost = {{{4.4, 8.0, 10.8}, {1.45, 2.3, 2.75}}, {2.0, 3.0, 9.0}, 0.5};
 constexpr PlanCost kBwdCost = {{{4.3, 6.7, 11.0}, {1.95, 2.6, 3.0}}, {2.0, 3.0, 5.0}, 0.35};
 constexpr double kBwdLongest[2][3] = {{7.5, 13.0, 19.5}, {3.6, 5.3, 6.6}};
-constexpr double kJoinCost = 14.0, kSharedUnit = 1.57;
+constexpr double kJoinCost = 14.0, kLaunchCost = 4.0, kSharedUnit = 1.57;
 constexpr int64_t kMinSegment = 64;
 
-// `units` workgroups per segment and pass.
-int64_t choose_segments(bool bwd, int io, int dc_pad, int64_t seqlen, int64_t units, int cu) {
-    const PlanCost& cost = bwd ? kBwdCost : kFwdCost;
-    const bool wide = dc_pad == 256;
-    const int width = dc_pad == 64 ? 0 : (wide ? 2 : 1), type = io == mamba::kIoF32 ? 0 : 1;
-    const double chunk = cost.chunk[type][width], longest = kBwdLongest[type][width];
-    const double chunks = static_cast<double>(seqlen) / 64.0;
-    const int64_t all = units * (bwd ? 3 : 1);
+int width_class(int d) { return mamba::lin_padded(d) == 64 ? 0 : (mamba::lin_padded(d) == 128 ? 1 : 2); }
+
+// Microseconds of a pass cut into n segments, without those of the cut: `each`
+// runs of 64 tokens per workgroup, of which `walk` is the longest.
+double fwd_time(const LinearAttnCall& c, int64_t n, double each, int cu) {
+    const int type = c.io == mamba::kIoF32 ? 0 : 1, w = width_class(c.dk);
+    const int64_t all = c.batch * c.heads * mamba::lin_blocks(c.dv) * n;
+    const int64_t round = w == 2 ? cu : 2 * int64_t(cu), rest = all % round;
+    const double load = static_cast<double>(all / round) * (w == 2 ? 1.0 : kSharedUnit) +
+                        (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : kSharedUnit));
+    return (each * kFwdCost.chunk[type][w] + kFwdCost.entry[w]) * load;
+}
+
+// One launch of gradients at width class w: `dq` and `others` workgroups per
+// segment of the pass of dq and of the other passes.
+double bwd_launch_time(int type, int w, int64_t dq, int64_t others, int64_t n, double each, int cu) {
+    const double chunk = kBwdCost.chunk[type][w], longest = dq > 0 ? kBwdLongest[type][w] : chunk;
+    const double work = (longest * static_cast<double>(dq) + chunk * static_cast<double>(others)) *
+                        static_cast<double>(n) / cu;
+    const double alone = w == 2 || (dq + others) * n <= cu ? 1.0 : 1.3;   // beside shorter ones
+    double load = work / longest * (w == 2 ? 1.0 : kSharedUnit / 2);
+    if (load < alone) load = alone;
+    return (each * longest + kBwdCost.entry[w]) * load;
+}
+
+// The gradients in one launch, at the wider head's width, or in two: dq and dk
+// contract over dv, dv over dk. Two launches save what a narrow head wastes at
+// a wide one's width, one lets all passes run beside each other: fp32, 9 x 202 x
+// 12 heads of 232 x 16, 126 us in two against 287; 2 x 333 x 6 heads of 64 x 96,
+// 39 us in one.
+double bwd_time(const LinearAttnCall& c, int64_t n, double each, int cu, bool* two) {
+    const int type = c.io == mamba::kIoF32 ? 0 : 1, wk = width_class(c.dk), wv = width_class(c.dv);
+    const int64_t bh = c.batch * c.heads, over_k = bh * mamba::lin_blocks(c.dk), over_v = bh * mamba::lin_blocks(c.dv);
+    const double one = bwd_launch_time(type, wk > wv ? wk : wv, over_k, over_k + over_v, n, each, cu);
+    const double both = bwd_launch_time(type, wv, over_k, over_k, n, each, cu) +
+                        bwd_launch_time(type, wk, 0, over_v, n, each, cu) + kLaunchCost;
+    *two = wk != wv && both < one;
+    return *two ? both : one;
+}
+
+double runs_of_64(int64_t seqlen, int64_t n) {
+    const double each = static_cast<double>(ceil_div(ceil_div(seqlen, n), kSegUnit));
+    const double whole = static_cast<double>(seqlen) / 64.0;
+    return each < whole ? each : whole;
+}
+
+int64_t choose_segments(const LinearAttnCall& c, bool bwd, int cu) {
+    const int64_t bh = c.batch * c.heads;
+    const int64_t all = bwd ? bh * (2 * mamba::lin_blocks(c.dk) + mamba::lin_blocks(c.dv))
+                            : bh * mamba::lin_blocks(c.dv);
     int64_t best = 1;
     double least = 0.0;
-    for (int64_t n = 1; n <= ceil_div(seqlen, kMinSegment) && (n == 1 || all * n <= 8 * int64_t(cu)); ++n) {
-        double load;
-        if (bwd) {
-            const double sum = (1.0 + 2.0 * chunk / longest) * static_cast<double>(units * n) / cu;
-            load = sum * (wide ? 1.0 : kSharedUnit / 2);
-            const double alone = wide || all * n <= cu ? 1.0 : 1.3;   // beside shorter ones
-            if (load < alone) load = alone;
-        } else {
-            const int64_t round = wide ? cu : 2 * int64_t(cu), rest = all * n % round;
-            load = static_cast<double>(all * n / round) * (wide ? 1.0 : kSharedUnit) +
-                   (rest == 0 ? 0.0 : (rest <= cu ? 1.0 : kSharedUnit));
-        }
-        const double each = static_cast<double>(ceil_div(ceil_div(seqlen, n), kSegUnit));
-        double t = ((each < chunks ? each : chunks) * (bwd ? longest : chunk) + cost.entry[width]) * load;
-        if (n > 1) t = t * (1.0 + cost.summary) + kJoinCost;
+    for (int64_t n = 1; n <= ceil_div(c.seqlen, kMinSegment) && (n == 1 || all * n <= 8 * int64_t(cu)); ++n) {
+        const double each = runs_of_64(c.seqlen, n);
+        bool two;
+        double t = bwd ? bwd_time(c, n, each, cu, &two) : fwd_time(c, n, each, cu);
+        if (n > 1) t = t * (1.0 + (bwd ? kBwdCost : kFwdCost).summary) + kJoinCost;
         if (n == 1 || t < least) {
             least = t;
             best = n;
@@ -136,7 +168,7 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
         int cu = 0;
         const int st = mamba::current_cu_count(&cu);
         if (st != MAMBA_OK) return st;
-        const int64_t n = choose_segments(passes > 1, c.io, dc_pad, c.seqlen, c.batch * c.heads * blocks, cu);
+        const int64_t n = choose_segments(c, passes > 1, cu);
         seg = n > 1 ? ceil_div(ceil_div(c.seqlen, n), kSegUnit) * kSegUnit : c.seqlen;
     }
     if (seg < c.seqlen) {
@@ -279,6 +311,12 @@ int linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_hea
     c.d_v = d_v;
     c.dlog_decay = dlog_decay;
     c.dh0 = dh0;
+    if (batch > 0 && seqlen > 0 && mamba::lin_padded(c.dk) != mamba::lin_padded(c.dv)) {
+        int cu = 0;
+        st = mamba::current_cu_count(&cu);
+        if (st != MAMBA_OK) return st;
+        bwd_time(c, p.nseg, runs_of_64(seqlen, p.nseg), cu, &p.two);
+    }
     return mamba::launch_linear_attn_bwd(c, p, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 

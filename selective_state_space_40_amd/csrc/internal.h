@@ -163,8 +163,6 @@ hipError_t launch_ssd_fwd(const SsdArgs& a, hipStream_t stream);
 
 // Linear attention with a decay for each head (linear_attn_kernel.h).
 constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
-// passes of the backward launch
-constexpr int kLinPassDq = 0, kLinPassDv = 1, kLinPassDk = 2;   // dq first
 constexpr int kLinMaxDim = 256;   // widest head
 // Output columns of a workgroup; its waves have 16 each. Of heads wider than 128
 // two waves share 16 columns, each with half of the state's rows, since a wave
@@ -238,6 +236,7 @@ struct LinearAttnCall {
 struct LinPlan {
     int64_t seg_len = 0;
     int nseg = 1;
+    bool two = false;   // gradients in two launches, each at its own width
 };
 
 // Head width the kernels are built for, and blocks of `out` columns.

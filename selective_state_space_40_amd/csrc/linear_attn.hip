@@ -315,8 +315,8 @@ hipError_t launch_linear_attn_fwd(const LinearAttnCall& c, const LinPlan& p, voi
 
 hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, void* ws, hipStream_t s) {
     const int dc_pad = lin_padded(max_dim(c));
-    const int nblk = bwd_blocks(c);
-    const BwdScratch w = bwd_scratch(c, p, nblk);
+    const int nblk = p.two ? lin_blocks(c.dk) : bwd_blocks(c);   // of the launch with dq
+    const BwdScratch w = bwd_scratch(c, p, bwd_blocks(c));
     char* base = static_cast<char*>(ws);
     float* seg_s = p.nseg > 1 ? reinterpret_cast<float*>(base + w.seg_s) : nullptr;
     float* seg_d = p.nseg > 1 ? reinterpret_cast<float*>(base + w.seg_d) : nullptr;
@@ -360,13 +360,10 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
             if (e != hipSuccess) return e;
         }
         LinArgs a = base_args(c, p);
-        a.nblk = nblk;
-        a.npass = 3;
         a.dg = dg;
         a.dhL = c.dhL;
         a.adj_in = seg_d;
-        a.pass[kLinPassDv] = adj;
-        LinPass& q = a.pass[kLinPassDq];
+        LinPass& q = a.pass[0];   // the pass that forms the decay's gradient is the first
         q = states;
         q.q = c.d_o;
         q.k = c.v;
@@ -378,7 +375,7 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         q.sp = c.dv;
         q.dc = c.dv;
         q.dout = c.dk;
-        LinPass& k = a.pass[kLinPassDk];
+        LinPass& k = a.pass[1];
         k = adj;
         k.q = c.v;
         k.k = c.d_o;
@@ -389,8 +386,19 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
         k.sp = c.dv;
         k.dc = c.dv;
         k.dout = c.dk;
-        e = launch_mode<kLinBwd>(c, a, dc_pad, s);
+        a.pass[2] = adj;
+        a.npass = p.two ? 2 : 3;
+        a.nblk = nblk;
+        e = launch_mode<kLinBwd>(c, a, p.two ? lin_padded(c.dv) : dc_pad, s);
         if (e != hipSuccess) return e;
+        if (p.two) {
+            a.pass[0] = adj;
+            a.npass = 1;
+            a.nblk = lin_blocks(c.dv);
+            a.dg = nullptr;
+            e = launch_mode<kLinBwd>(c, a, lin_padded(c.dk), s);
+            if (e != hipSuccess) return e;
+        }
         if (shared) {
             e = launch_share(c, part_k, part_v, s);
             if (e != hipSuccess) return e;

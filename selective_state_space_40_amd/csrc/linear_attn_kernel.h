@@ -817,15 +817,15 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     // order read the same rows and share an XCD's L2. The pass that forms the
     // decay's gradient takes longest and goes first; the others run beside it.
     const bool ordered = MODE == kLinBwd && a.dg != nullptr;
-    const uint32_t most = ordered ? gridDim.x / 3 : 0;
+    const uint32_t most = ordered ? gridDim.x / a.npass : 0;
     const bool first = blockIdx.x < most;
     uint32_t id = first ? xcd_order(blockIdx.x, most) : xcd_order(blockIdx.x - most, gridDim.x - most);
     uint32_t up = id / a.nblk;
     const int blk = static_cast<int>(id - up * a.nblk);
     id = up;
-    int ip = kLinPassDq;
+    int ip = 0;
     if (!first) {
-        const uint32_t np = ordered ? 2 : a.npass;
+        const uint32_t np = ordered ? a.npass - 1 : a.npass;
         up = id / np;
         ip = static_cast<int>(id - up * np) + (ordered ? 1 : 0);
         id = up;

@@ -110,6 +110,16 @@ def test_wide_heads_of_different_lengths(dk, dv, dtype):
     _check_all(i, f"wide {dk}x{dv} {dtype}", segments=(0, 64))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(200, 16), (16, 200), (136, 64), (64, 96)])
+def test_gradients_of_heads_of_unlike_widths(dk, dv, dtype):
+    # rows and heads enough that the passes over dk and over dv are launched
+    # apart, each at its own width
+    lengths = [70, 0, 33, 64, 70, 1]
+    i = _make(6, 70, 24, 8, dk, dv, dtype, seed=dk, lengths=lengths)
+    _check_all(i, f"unlike {dk}x{dv} {dtype}", segments=(0, 64))
+
+
 def test_outputs_without_the_final_state():
     # the state then enters with fewer terms, which bf16 outputs do not show
     for dk, dv in ((64, 64), (128, 72), (192, 136)):
