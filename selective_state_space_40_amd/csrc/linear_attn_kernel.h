@@ -296,9 +296,10 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
 }
 
 // One workgroup's walk: column block blk of pass ip over segment seg of (row,
-// head) bh. EXACT: the state enters with three terms. DG: the pass also forms
-// the decay's gradient.
-template <int IO, int DC, int MODE, bool EXACT, bool DG>
+// head) bh. ALT: bf16: the state enters with three terms; fp32: blocks of 32
+// state rows past the head's width are left out. DG: the pass also forms the
+// decay's gradient.
+template <int IO, int DC, int MODE, bool ALT, bool DG>
 __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC, MODE>& lds, const int ip,
                                                  const int blk, int seg, const int64_t bh, const int64_t b,
                                                  const int hd) {
@@ -315,6 +316,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     constexpr int DOB = kLinBlock;   // columns per workgroup
     constexpr int THREADS = WAVES * kWave;
     constexpr bool kState = MODE == kLinState, kBwd = MODE == kLinBwd;
+    constexpr bool EXACT = O::kSplit && ALT, SKIP = !O::kSplit && ALT;
     typedef LinLds<IO, DC, MODE> Lds;
     constexpr int RK = Lds::TileK::kRow, RV = Lds::TileV::kRow, RQ = Lds::TileQ::kRow, RX = Lds::TileX::kRow;
     const int tid = threadIdx.x;
@@ -341,6 +343,9 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         if (DG && tid == 0) *dg_out = 0.0;
         return;
     }
+
+    // whether the 32 rows from n on are to be formed
+    auto used = [&](int n) { return !SKIP || n < dc; };
 
     const int64_t L = a.seqlen;
     int64_t len = L;
@@ -560,6 +565,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
             };
 #pragma unroll
             for (int k = 0; k < NN / 2; ++k) {
+                if (!used(n0w + 32 * k)) continue;
                 Frag q[NT];
 #pragma unroll
                 for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + n0w + 32 * k, g);
@@ -585,6 +591,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 if constexpr (GR > 1) {
 #pragma unroll
                     for (int k = 0; k < DC; k += 32) {
+                        if (!used(k)) continue;
                         const Frag kf = O::nat(lds.K + (16 * jt + c) * RK + k, g);
 #pragma unroll
                         for (int u = 0; u < OWN; ++u)
@@ -628,6 +635,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 for (int it = 0; it < NT; ++it) YD[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k = 0; k < NN / 2; ++k) {
+                    if (!used(n0w + 32 * k)) continue;
                     Frag q[NT];
 #pragma unroll
                     for (int it = 0; it < NT; ++it) q[it] = O::nat(lds.Q + (16 * it + c) * RQ + n0w + 32 * k, g);
@@ -710,9 +718,10 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 }
             }
             if constexpr (!DG) __builtin_amdgcn_sched_barrier(0);
-            constexpr int U = NN < 4 ? NN : 4;   // independent blocks between the terms of one
+            constexpr int U = SKIP ? 2 : 4;   // independent blocks between the terms of one
 #pragma unroll
             for (int n0 = 0; n0 < NN; n0 += U) {
+                if (!used(n0w + state_row(n0, 0))) continue;
                 Frag kf[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) kf[u] = O::template tr<RK, 8>(lds.K, 32 * s, n0w + state_row(n0 + u, 0), c, g);
@@ -835,17 +844,26 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     const int seg = static_cast<int>(id - up * nsegs);
     const uint32_t row = up / a.heads;
     const int hd = static_cast<int>(up - row * a.heads);
+    const LinPass& ps = a.pass[ip];
+    // Whole blocks of 32 state rows past the head's width. The fp32 kernels, bound
+    // by their matrix instruction, leave them out (6 x 3036 x 18 heads of 24 x
+    // 72: 153 us against 198); in bf16, and where nothing is unused, the
+    // branches cost more than they save (bf16, 1 x 7905 x 48 heads of 224 x 192:
+    // 1717 us against 1353).
+    const bool unused = ps.dc <= DC - 32;
     if constexpr (MODE == kLinBwd) {
         if (first) {
-            linear_attn_walk<IO, DC, MODE, true, true>(a, lds, ip, blk, seg, up, row, hd);
+            if (IO == kIoBF16 || unused)
+                linear_attn_walk<IO, DC, MODE, true, true>(a, lds, ip, blk, seg, up, row, hd);
+            else
+                linear_attn_walk<IO, DC, MODE, IO == kIoBF16, true>(a, lds, ip, blk, seg, up, row, hd);
             return;
         }
     }
     // a state that the caller gets
-    const LinPass& ps = a.pass[ip];
     const bool leaves = ps.s_out != nullptr && seg == (ps.rev ? 0 : a.nseg - 1);
-    if (IO == kIoBF16 && (MODE == kLinState ? a.exact != 0 : leaves))
-        linear_attn_walk<IO, DC, MODE, IO == kIoBF16, false>(a, lds, ip, blk, seg, up, row, hd);
+    if (IO == kIoBF16 ? (MODE == kLinState ? a.exact != 0 : leaves) : unused)
+        linear_attn_walk<IO, DC, MODE, true, false>(a, lds, ip, blk, seg, up, row, hd);
     else
         linear_attn_walk<IO, DC, MODE, false, false>(a, lds, ip, blk, seg, up, row, hd);
 }
