@@ -72,23 +72,56 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(JoinArgs a) {
     }
 }
 
+// The decay's gradient: each head's terms in a fixed order, in 64 bits, one
+// workgroup of 256 per head.
+struct DecaySumArgs {
+    int64_t terms;        // of a head
+    int heads;
+    const double* dg;     // (heads, terms)
+    float* out;           // (heads) or nullptr: not wanted
+};
+
+__device__ __forceinline__ void decay_sum(const DecaySumArgs& a, int head, double (&red)[4]) {
+    const double* p = a.dg + head * a.terms;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < a.terms; i += 256) s += p[i];
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
+    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) a.out[head] = static_cast<float>(((red[0] + red[1]) + red[2]) + red[3]);
+}
+
+__global__ __launch_bounds__(256) void linear_attn_decay_kernel(DecaySumArgs a) {
+    __shared__ double red[4];
+    decay_sum(a, static_cast<int>(blockIdx.x), red);
+}
+
 // Gradients of keys and values that several heads share: the sum of the
 // heads' fp32 gradients (batch, seqlen, heads, dim), rounded once. Added in a
-// fixed order, not by atomics. Bound by memory (4 us at 2 x 333 x 6 heads).
+// fixed order, not by atomics. Bound by memory (4 us at 2 x 333 x 6 heads). The
+// first workgroups, one per head, sum the decay's gradient, which saves a launch.
 struct ShareArgs {
     int64_t rows;           // (batch, seqlen, kv_heads)
     int rep;                // heads per head of keys and values
     int dim[2];
     const float* part[2];
     void* out[2];
+    DecaySumArgs decay;
 };
 
 template <int IO>
 __global__ __launch_bounds__(256) void linear_attn_share_kernel(ShareArgs a) {
     const int which = blockIdx.y;
+    const int heads = a.decay.out != nullptr ? a.decay.heads : 0;
+    if (static_cast<int>(blockIdx.x) < heads) {
+        __shared__ double red[4];
+        if (which == 0) decay_sum(a.decay, static_cast<int>(blockIdx.x), red);
+        return;
+    }
     const int64_t quads = a.dim[which] / 4, count = a.rows * quads;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += stride) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x - heads) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x - heads) * 256 + threadIdx.x; i < count; i += stride) {
         const int64_t row = i / quads, q = i - row * quads;
         const f32x4* p = reinterpret_cast<const f32x4*>(a.part[which]) + row * a.rep * quads + q;
         f32x4 s = p[0];
@@ -96,20 +129,6 @@ __global__ __launch_bounds__(256) void linear_attn_share_kernel(ShareArgs a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) store_io<IO>(a.out[which], 4 * i + v, s[v]);
     }
-}
-
-// The decay's gradient: each head's terms in a fixed order, in 64 bits (2 us).
-__global__ __launch_bounds__(256) void linear_attn_decay_kernel(int64_t terms, const double* dg,
-                                                                float* out) {
-    __shared__ double red[4];
-    const double* p = dg + static_cast<int64_t>(blockIdx.x) * terms;
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < terms; i += 256) s += p[i];
-#pragma unroll
-    for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
-    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) out[blockIdx.x] = static_cast<float>(((red[0] + red[1]) + red[2]) + red[3]);
 }
 
 // One token: S <- lam S + k^T v in place, o = scale q S. Bound by the state,
@@ -274,10 +293,10 @@ hipError_t launch_join(const LinearAttnCall& c, const LinPlan& p, float* seg_s, 
     return hipGetLastError();
 }
 
-hipError_t launch_share(const LinearAttnCall& c, const float* part_k, const float* part_v, hipStream_t s) {
+hipError_t launch_share(const LinearAttnCall& c, const float* part_k, const float* part_v,
+                        const DecaySumArgs& decay, hipStream_t s) {
     ShareArgs a = {};
     a.rows = c.batch * c.seqlen * c.kv_heads;
-    if (a.rows == 0) return hipSuccess;
     a.rep = c.heads / c.kv_heads;
     a.dim[0] = c.dk;
     a.dim[1] = c.dv;
@@ -285,7 +304,9 @@ hipError_t launch_share(const LinearAttnCall& c, const float* part_k, const floa
     a.part[1] = part_v;
     a.out[0] = c.d_k;
     a.out[1] = c.d_v;
-    const dim3 grid(static_cast<unsigned>(stride_blocks(a.rows * (max_dim(c) / 4))), 2), block(256);
+    a.decay = decay;
+    const int64_t sums = decay.out != nullptr ? decay.heads : 0;
+    const dim3 grid(static_cast<unsigned>(sums + stride_blocks(a.rows * (max_dim(c) / 4))), 2), block(256);
     if (c.io == kIoF32) hipLaunchKernelGGL((linear_attn_share_kernel<kIoF32>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((linear_attn_share_kernel<kIoBF16>), grid, block, 0, s, a);
     return hipGetLastError();
@@ -399,14 +420,12 @@ hipError_t launch_linear_attn_bwd(const LinearAttnCall& c, const LinPlan& p, voi
             e = launch_mode<kLinBwd>(c, a, lin_padded(c.dk), s);
             if (e != hipSuccess) return e;
         }
-        if (shared) {
-            e = launch_share(c, part_k, part_v, s);
-            if (e != hipSuccess) return e;
-        }
     }
+    // the sums over workgroups and heads
+    const DecaySumArgs decay = {c.batch * p.nseg * nblk, c.heads, dg, c.dlog_decay};
+    if (shared && c.batch > 0 && c.seqlen > 0) return launch_share(c, part_k, part_v, decay, s);
     if (c.dlog_decay != nullptr) {
-        hipLaunchKernelGGL(linear_attn_decay_kernel, dim3(static_cast<unsigned>(c.heads)), dim3(256), 0, s,
-                           c.batch * p.nseg * nblk, dg, c.dlog_decay);
+        hipLaunchKernelGGL(linear_attn_decay_kernel, dim3(static_cast<unsigned>(c.heads)), dim3(256), 0, s, decay);
         e = hipGetLastError();
     }
     return e;
