@@ -552,19 +552,23 @@ def _must(t, name, shape, dtype, dev):
     return _require(t, name, shape, dtype, dev)
 
 
-class _on:
-    """The tensors' device made current for a call, if it is not already."""
-
-    def __init__(self, dev):
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+class _Stay:
+    """The device that is current already."""
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        pass
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        pass
+
+
+_STAY = _Stay()
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on(dev):
+    """The tensors' device made current for a call, if it is not already."""
+    return _STAY if _device_now() == dev.index else torch.cuda.device(dev)
 
 
 # the current stream's handle, without the object around it where torch has a
@@ -586,7 +590,29 @@ def _scratch(dev, nbytes):
 
 def _attn_shapes(q, k, v, ndim):
     """(batch, L, heads, kv_heads, dk, dv) of q, k and v and their addresses,
-    checked against each other; L is 1 for single tokens (ndim 3)."""
+    checked against each other; L is 1 for single tokens (ndim 3). The cheap
+    test comes first, _attn_checked says what is wrong."""
+    try:
+        if ndim == 4:
+            batch, seqlen, heads, dk = q.shape
+            kb, kl, kv_heads, kd = k.shape
+            vb, vl, vh, dv = v.shape
+        else:
+            (batch, heads, dk), (kb, kv_heads, kd), (vb, vh, dv) = q.shape, k.shape, v.shape
+            seqlen = kl = vl = 1
+        dt, index = q.dtype, q.get_device()
+        if (kb == batch == vb and kl == seqlen == vl and kd == dk and kv_heads == vh > 0
+                and heads % vh == 0 and dt in _DTYPES and k.dtype is dt and v.dtype is dt
+                and index >= 0 and k.get_device() == index and v.get_device() == index
+                and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+            return ((batch, seqlen, heads, kv_heads, dk, dv),
+                    (q.data_ptr(), k.data_ptr(), v.data_ptr()))
+    except (AttributeError, ValueError, TypeError):
+        pass
+    return _attn_checked(q, k, v, ndim)
+
+
+def _attn_checked(q, k, v, ndim):
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
