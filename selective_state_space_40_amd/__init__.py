@@ -552,6 +552,14 @@ def _must(t, name, shape, dtype, dev):
     return _require(t, name, shape, dtype, dev)
 
 
+def _output(t, name, shape, dtype, dev):
+    """The caller's tensor for an output, or a new one, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _require(t, name, shape, dtype, dev)
+
+
 class _Stay:
     """The device that is current already."""
 
@@ -665,13 +673,10 @@ def linear_attn_fwd(q, k, v, log_decay, h0=None, *, lengths=None, scale=None, re
     pg = _must(log_decay, "log_decay", (heads,), torch.float32, dev)
     p0 = _require(h0, "h0", state, torch.float32, dev)
     pl = _require(lengths, "lengths", (batch,), torch.int32, dev)
-    o = out if out is not None else torch.empty(batch, seqlen, heads, dv, dtype=dt, device=dev)
-    po = _require(o, "out", (batch, seqlen, heads, dv), dt, dev)
+    o, po = _output(out, "out", (batch, seqlen, heads, dv), dt, dev)
     hL = ph = None
     if return_state:
-        hL = state_out if state_out is not None else torch.empty(state, dtype=torch.float32,
-                                                                 device=dev)
-        ph = _require(hL, "state_out", state, torch.float32, dev)
+        hL, ph = _output(state_out, "state_out", state, torch.float32, dev)
     code = _DTYPES[dt]
     with _on(dev):
         nbytes = _scratch_bytes("linear_attn_fwd_workspace_size", dev.index, *sizes, code,
@@ -729,8 +734,7 @@ def linear_attn_update(h, q, k, v, log_decay, *, scale=None, out=None):
     dev, dt = q.device, q.dtype
     ph = _must(h, "h", (batch, heads, dk, dv), torch.float32, dev)
     pg = _must(log_decay, "log_decay", (heads,), torch.float32, dev)
-    o = out if out is not None else torch.empty(batch, heads, dv, dtype=dt, device=dev)
-    po = _require(o, "out", (batch, heads, dv), dt, dev)
+    o, po = _output(out, "out", (batch, heads, dv), dt, dev)
     with _on(dev):
         st = lib.linear_attn_update(batch, heads, kv_heads, dk, dv, _DTYPES[dt], ph, pq, pk, pv, pg,
                                     dk ** -0.5 if scale is None else scale, po, _raw_stream(dev))
@@ -740,7 +744,19 @@ def linear_attn_update(h, q, k, v, log_decay, *, scale=None, out=None):
 
 
 def _norm_shapes(x, groups):
-    """(rows, dim) of x, and its address."""
+    """(rows, dim) of x, and its address. The cheap test comes first,
+    _norm_checked says what is wrong."""
+    try:
+        dim = x.shape[-1]
+        if (groups > 0 and dim > 0 and dim % groups == 0 and x.dtype in _DTYPES
+                and x.get_device() >= 0 and x.is_contiguous()):
+            return x.numel() // dim, dim, x.data_ptr()
+    except (AttributeError, IndexError, TypeError):
+        pass
+    return _norm_checked(x, groups)
+
+
+def _norm_checked(x, groups):
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 1:
@@ -766,9 +782,8 @@ def layer_norm_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out=None):
     dev, dt = x.device, x.dtype
     pw = _require(weight, "weight", (dim,), torch.float32, dev)
     pb = _require(bias, "bias", (dim,), torch.float32, dev)
-    y = out if out is not None else torch.empty_like(x)
-    py = _require(y, "out", x.shape, dt, dev)
-    mean = torch.empty(*x.shape[:-1], groups, dtype=torch.float32, device=dev)
+    y, py = _output(out, "out", x.shape, dt, dev)
+    mean = torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     with _on(dev):
         st = lib.layer_norm_fwd(rows, dim, groups, _DTYPES[dt], px, pw, pb, eps, py, mean.data_ptr(),
@@ -791,8 +806,7 @@ def layer_norm_bwd(x, weight, mean, rstd, *, dy, groups=1, want_dbias=True, out=
     pm = _must(mean, "mean", stats, torch.float32, dev)
     pr = _must(rstd, "rstd", stats, torch.float32, dev)
     pdy = _must(dy, "dy", x.shape, dt, dev)
-    dx = out if out is not None else torch.empty_like(x)
-    pdx = _require(dx, "out", x.shape, dt, dev)
+    dx, pdx = _output(out, "out", x.shape, dt, dev)
     dw = None if weight is None else torch.empty(dim, dtype=torch.float32, device=dev)
     db = torch.empty(dim, dtype=torch.float32, device=dev) if want_dbias else None
     code = _DTYPES[dt]
