@@ -12,10 +12,24 @@ namespace {
 
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 
-// exp(g) - 1 for a whole number n of steps of log decay g.
-__device__ __forceinline__ float decay_minus_one(float g, int64_t n) {
-    return g == 0.0f || n == 0 ? 0.0f : expm1f(g * static_cast<float>(n));
-}
+// A state's decay over n steps of log decay g, as keep s + change s: a slow one
+// by its difference from 1, which rounds only the change, a fast one as a
+// factor, whose difference from 1 would round at the state's size.
+struct Decay {
+    float keep, change;
+
+    __device__ __forceinline__ Decay(float g, int64_t n) : keep(1.0f), change(0.0f) {
+        if (g == 0.0f || n == 0) return;
+        const float p = g * static_cast<float>(n);
+        if (p > -0.6931472f) {
+            change = expm1f(p);
+        } else {
+            keep = 0.0f;
+            change = expf(p);
+        }
+    }
+    __device__ __forceinline__ float of(float s) const { return fmaf(s, change, keep * s); }
+};
 
 // Join of the segments, in place: on entry seg[(b, h), s] holds what segment
 // s adds to the state it is entered with, on exit the state entering it.
@@ -65,9 +79,9 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(JoinArgs a) {
             seg[sg * quads] = s;
             int64_t n = len - sg * a.seg_len;
             n = n < 0 ? 0 : (n < a.seg_len ? n : a.seg_len);
-            const float em = decay_minus_one(g, n);
+            const Decay decay(g, n);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) s[v] = fmaf(s[v], em, s[v]) + add[u][v];
+            for (int v = 0; v < 4; ++v) s[v] = decay.of(s[v]) + add[u][v];
         }
     }
 }
@@ -169,7 +183,7 @@ __global__ __launch_bounds__(kLinUpdateThreads) void linear_attn_update_kernel(L
         qs[n] = have ? raw_to_f32<IO>(load_raw<IO>(a.q, bh * a.dk + n)) : 0.0f;
         ks[n] = have ? raw_to_f32<IO>(load_raw<IO>(a.k, kv * a.dk + n)) : 0.0f;
     }
-    const float em = decay_minus_one(a.log_decay[hd], 1);
+    const Decay decay(a.log_decay[hd], 1);
     __syncthreads();
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -178,7 +192,7 @@ __global__ __launch_bounds__(kLinUpdateThreads) void linear_attn_update_kernel(L
         const float kn = ks[n], qn = qs[n];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[u][e] = fmaf(kn, v[e], fmaf(s[u][e], em, s[u][e]));
+            s[u][e] = fmaf(kn, v[e], decay.of(s[u][e]));
             o[e] = fmaf(qn, s[u][e], o[e]);
         }
         if (in && n < a.dk) *reinterpret_cast<f32x4*>(h + static_cast<int64_t>(n) * a.dv) = s[u];

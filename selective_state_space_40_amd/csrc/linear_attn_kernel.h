@@ -784,7 +784,23 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         }
     }
 
-    if (sout != nullptr) store_state(sout + (kState ? bh * a.nseg + seg : bh) * state_elems);
+    if (!DG && sout != nullptr) {   // the pass of dq leaves no state
+        // A fast head's chunks leave S + em S, em within 2^-25 of lam^cnt - 1, of
+        // the entering state, an error of 2^-25 of it where it should be down to
+        // lam^cnt: put right here, since a large entering state may show through
+        // what little a short sequence adds (later chunks wipe it out)
+        const float kept_full = 1.0f + em_full, kept_short = 1.0f + em_short;   // exact below a half
+        if (!kState && sin != nullptr && ntok > 0 && (kept_full <= 0.5f || kept_short <= 0.5f)) {
+            float kept = kept_short;
+            for (int64_t n = ntok / C; n > 0 && kept > 1e-37f; --n) kept *= kept_full;
+            const float missing = decay_power(g1, ntok < 65536 ? static_cast<int>(ntok) : 65536) - kept;
+            load_state(sin, [&](int nt, f32x4 x) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) S[nt][v] = fmaf(x[v], missing, S[nt][v]);
+            });
+        }
+        store_state(sout + (kState ? bh * a.nseg + seg : bh) * state_elems);
+    }
     if constexpr (!kState) {
         // rows behind the sequence's end: zeros
         const int64_t z0 = end > seg0 ? end : seg0;

@@ -120,6 +120,24 @@ def test_gradients_of_heads_of_unlike_widths(dk, dv, dtype):
     _check_all(i, f"unlike {dk}x{dv} {dtype}", segments=(0, 64))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("decay", [-0.8, -3.0, -9.0])
+def test_large_states_that_fade_fast(decay, dtype):
+    # a carried state (and its gradient) far above what a short sequence adds:
+    # what remains of it is small, and must not be rounded at its old size
+    for length in (1, 3, 43, 64, 70):
+        i = _make(2, length, 2, 1, 136 if length == 43 else 64, 64, dtype, seed=length, decay=[decay, 1.5 * decay])
+        i["h0"] *= 100.0
+        i["dhL"] *= 100.0
+        _check_all(i, f"fading {decay} {length} {dtype}", segments=(0, 64))
+        h = i["h0"].clone()
+        one = [i[n][:, 0].contiguous() for n in ("q", "k", "v")]
+        want_o, want_h = ref.attn_token(i["h0"], *one, i["log_decay"])
+        o = ms.linear_attn_update(h, *one, i["log_decay"])
+        ref.check(o, want_o, "bf16" if dtype == BF else "f32", "token o")
+        ref.check(h, want_h, "f32", "token h")
+
+
 def test_outputs_without_the_final_state():
     # the state then enters with fewer terms, which bf16 outputs do not show
     for dk, dv in ((64, 64), (128, 72), (192, 136)):
