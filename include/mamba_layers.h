@@ -54,7 +54,9 @@ extern "C" {
  * segment_len tokens per parallel segment, 0: automatic, else a multiple of
  *             64. A cut sequence takes a pass over k and v that gives each
  *             segment's share of the state, a join, and the pass that writes
- *             the outputs; the result is the same up to rounding.
+ *             the outputs; the result is the same up to rounding. A forced
+ *             segment_len below seqlen takes at most 65536 segments and 65535
+ *             rows times heads (else MAMBA_ERR_UNSUPPORTED).
  *
  * dk and dv are multiples of MAMBA_LINATTN_DIM_UNIT up to
  * MAMBA_LINATTN_MAX_DIM, heads at most MAMBA_LINATTN_MAX_HEADS, and a launch,
