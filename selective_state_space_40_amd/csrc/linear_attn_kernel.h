@@ -285,6 +285,11 @@ __device__ __forceinline__ float decay_power(float g, int n) {
     return (x > 0.0f && x < __builtin_inff()) ? fmaf(x, e, x) : x;
 }
 
+// A value that all lanes hold, moved to a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // The first of the 4 state rows that lane group g holds in block nt.
 __device__ __forceinline__ int state_row(int nt, int g) { return 32 * (nt >> 1) + 8 * g + 4 * (nt & 1); }
 
@@ -471,8 +476,8 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     }
     // lam^cnt - 1 of whole chunks and of a short one
     const int short_cnt = static_cast<int>(ntok % C);
-    const float em_full = g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(C));
-    const float em_short = g1 == 0.0f || short_cnt == 0 ? 0.0f : expm1f(g1 * static_cast<float>(short_cnt));
+    const float em_full = uniform(g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(C)));
+    const float em_short = uniform(g1 == 0.0f || short_cnt == 0 ? 0.0f : expm1f(g1 * static_cast<float>(short_cnt)));
     // where this lane's outputs go: token 16 it + c, columns 4 g .. + 3 of the
     // wave's
     const bool wide = IO == kIoF32 || (kBwd && ps.out32);
@@ -626,7 +631,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                 }
             }
 #pragma unroll
-            for (int it = 0; it < NT; ++it) Y[it] *= eo[it];
+            for (int it = 0; it < NT; ++it) Y[it] *= DG ? ps.out_scale * lds.pow[16 * it + c + 1] : eo[it];
             if constexpr (DG) {
                 // the decay's gradient through the entering state; a second
                 // walk over q's fragments, as the registers hold no more at once
@@ -655,7 +660,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
                     const f32x4 x = O::ld4(lds.X + (16 * it + c) * RX + kLinCols * wc + 4 * g);
                     const float steps = static_cast<float>(16 * it + c + 1);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) dgi = fmaf(x[v], fmaf(steps, Y[it][v], YD[it][v] * eo[it]), dgi);
+                    for (int v = 0; v < 4; ++v) dgi = fmaf(x[v], fmaf(steps, Y[it][v], YD[it][v] * (ps.out_scale * lds.pow[16 * it + c + 1])), dgi);
                 }
                 dg += static_cast<double>(dgi);
             }
@@ -684,7 +689,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         const float em = cnt == C ? em_full : em_short;
         if constexpr (DG) {
             // the derivative, with the steps that the state takes here
-            const float f = static_cast<float>(cnt) * lds.pow[cnt];
+            const float f = uniform(static_cast<float>(cnt) * lds.pow[cnt]);
 #pragma unroll
             for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
