@@ -5,10 +5,10 @@
 //     dw = sum over rows of dy xh,  db = sum over rows of dy
 //
 // Both are bound by memory: one read of x (and dy), one write of y (dx). A
-// part of n = dim / groups values is held by a team of 16, 64, 256 or 512
-// lanes, 8 to 32 values per lane in registers, so the mean, the centred sum
-// of squares and the output take one pass over memory; the variance is the
-// mean square of the centred values, not a difference of sums. 16384 x 5120 in
+// part of n = dim / groups values is held by a team of 16 to 1024 lanes, 8 to 32
+// values per lane in registers, so the mean, the centred sum of squares and the
+// output take one pass over memory; the variance is the mean square of the
+// centred values, not a difference of sums. 16384 x 5120 in
 // bf16: 66 us forward (5.1 TB/s), 109 us backward (4.6 TB/s with the sums of the
 // parameters' gradients, 105 for its main kernel and 4 for the columns'), where a
 // large copy reaches 5.5 TB/s.
@@ -215,12 +215,17 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_fwd_kernel
 // dw and db in registers, its teams' sums meet in LDS at the end, and one
 // (slot, column) pair per workgroup goes to `partial` (2, slots, dim), from
 // which layer_norm_columns_kernel adds the slots in order.
+// The widest parts take teams of 1024 lanes, whose 128 registers hold neither the
+// next row's loads nor a row's products: those are formed again after the sums
+// (bf16, 2665 x 15734: 203 us, 523 with 512 lanes of 32 values, spilled; of
+// 12288 values that 512 lanes hold as 24 each: 48 us against 69).
 constexpr int kNormBwdThreads = 512;
 
 template <int IO, int TEAM, int CH, bool VEC>
-__global__ __launch_bounds__(kNormBwdThreads) void layer_norm_bwd_kernel(NormArgs a, int slots,
-                                                                         float* partial) {
-    __shared__ float red[2][2 * kNormBwdThreads / kWave];
+__global__ __launch_bounds__(TEAM > kNormBwdThreads ? TEAM : kNormBwdThreads) void layer_norm_bwd_kernel(
+    NormArgs a, int slots, float* partial) {
+    constexpr bool kLean = TEAM > kNormBwdThreads;
+    __shared__ float red[2][2 * (kLean ? TEAM : kNormBwdThreads) / kWave];
     __shared__ float cols[TEAM > 256 ? 1 : CH * 8 * kNormBwdThreads];
     typedef Part<IO, TEAM, CH, VEC> P;
     const int lane = threadIdx.x % TEAM;
@@ -245,10 +250,11 @@ __global__ __launch_bounds__(kNormBwdThreads) void layer_norm_bwd_kernel(NormArg
         rstd = in ? a.rstd[part] : 0.0f;
     };
     int odd = 0;
-    fetch(slot * teams + team);
+    if constexpr (!kLean) fetch(slot * teams + team);
     // every team of the workgroup takes the same number of turns
     for (int64_t r0 = slot * teams; r0 < a.rows; r0 += step) {
         const int64_t row = r0 + team;
+        if constexpr (kLean) fetch(row);
         float xh[CH * 8], wdy[CH * 8];
         float s[2] = {0.0f, 0.0f};
         const float mu = mean, rs = rstd;
@@ -257,21 +263,35 @@ __global__ __launch_bounds__(kNormBwdThreads) void layer_norm_bwd_kernel(NormArg
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int i = u * 8 + e;
-                const bool have = P::index(lane, u, e) < n;
-                xh[i] = have ? (x.get(u, e) - mu) * rs : 0.0f;
+                xh[i] = P::index(lane, u, e) < n ? (x.get(u, e) - mu) * rs : 0.0f;
                 const float d = dy.get(u, e);
+                wdy[i] = d * wt[i];
                 dw[i] = fmaf(d, xh[i], dw[i]);
                 db[i] += d;
-                wdy[i] = d * wt[i];
                 s[0] += wdy[i];
                 s[1] = fmaf(wdy[i], xh[i], s[1]);
             }
-        fetch(row + step);
+        if constexpr (!kLean) fetch(row + step);
         team_sum<TEAM>(s, red[odd]);
         odd ^= 1;   // the other buffer: a wave may still read this one
         const float c1 = s[0] * inv, c2 = s[1] * inv;
+        if constexpr (kLean) {
+            // values that the compiler cannot tell from new ones, lest it keep
+            // the row's products
+            float mu_again = mu;
+            asm volatile("" : "+v"(mu_again));
 #pragma unroll
-        for (int i = 0; i < CH * 8; ++i) wdy[i] = rs * (wdy[i] - c1 - xh[i] * c2);
+            for (int u = 0; u < CH; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = u * 8 + e;
+                    const float again = (x.get(u, e) - mu_again) * rs;
+                    wdy[i] = rs * (fmaf(dy.get(u, e), wt[i], -c1) - again * c2);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH * 8; ++i) wdy[i] = rs * (wdy[i] - c1 - xh[i] * c2);
+        }
         P::store(a.dx, (row < a.rows ? row * a.groups + grp : 0) * n, row < a.rows ? n : 0, lane, wdy);
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return;
@@ -363,9 +383,14 @@ struct Team {
     int lanes, runs;
 };
 
-Team team_for(int64_t n, int64_t parts) {
+// The backward pass, which holds more per value, takes more lanes for the widest
+// parts, sooner for those that are loaded value by value (fp32, 2000 x 5001: 34
+// us with 512 lanes, 47 with 256).
+Team team_for(int64_t n, int64_t parts, bool bwd) {
     const int64_t wave = parts < kFewParts ? 1024 : 1536;
-    const int lanes = n <= 384 ? 16 : (n <= wave ? 64 : (n <= 6144 ? 256 : 512));
+    int lanes = n <= 384 ? 16 : (n <= wave ? 64 : (n <= 6144 ? 256 : 512));
+    if (bwd && n > 4096 && n % 8 != 0) lanes = 512;
+    if (bwd && n > (n % 8 == 0 ? 12288 : 8192)) lanes = 1024;
     return {lanes, static_cast<int>((n + 8 * lanes - 1) / (8 * lanes))};
 }
 
@@ -386,7 +411,7 @@ BwdGrid bwd_grid(int64_t rows, int64_t groups, int lanes, int cu) {
     if (threads < lanes) threads = lanes;
     const int64_t teams = threads / lanes;
     const int64_t most = (rows + teams - 1) / teams;
-    const int64_t per_cu = kNormBwdThreads / threads;
+    const int64_t per_cu = threads < kNormBwdThreads ? kNormBwdThreads / threads : 1;
     int64_t slots = (per_cu * cu + groups - 1) / groups;
     if (slots > most) slots = most;
     return {threads, static_cast<int>(slots < 1 ? 1 : slots)};
@@ -395,14 +420,16 @@ BwdGrid bwd_grid(int64_t rows, int64_t groups, int lanes, int cu) {
 template <int IO, int TEAM, int CH, bool VEC>
 hipError_t launch_norm(const NormArgs& a, bool bwd, int threads, int slots, float* partial, hipStream_t s) {
     if (!bwd) {
-        constexpr int TEAMS = (TEAM > 256 ? TEAM : 256) / TEAM;
-        const int64_t most = (a.rows + TEAMS - 1) / TEAMS;
-        const int turns = kFwdWorkgroups / static_cast<int>(a.groups < kFwdWorkgroups ? a.groups : kFwdWorkgroups);
-        const int row_slots = static_cast<int>(most < turns ? most : turns);
-        hipLaunchKernelGGL((layer_norm_fwd_kernel<IO, TEAM, CH, VEC>),
-                           dim3(static_cast<unsigned>(row_slots * a.groups)), dim3(TEAM > 256 ? TEAM : 256), 0, s,
-                           a, row_slots);
-    } else {
+        if constexpr (TEAM <= 512) {
+            constexpr int TEAMS = (TEAM > 256 ? TEAM : 256) / TEAM;
+            const int64_t most = (a.rows + TEAMS - 1) / TEAMS;
+            const int turns = kFwdWorkgroups / static_cast<int>(a.groups < kFwdWorkgroups ? a.groups : kFwdWorkgroups);
+            const int row_slots = static_cast<int>(most < turns ? most : turns);
+            hipLaunchKernelGGL((layer_norm_fwd_kernel<IO, TEAM, CH, VEC>),
+                               dim3(static_cast<unsigned>(row_slots * a.groups)), dim3(TEAM > 256 ? TEAM : 256), 0,
+                               s, a, row_slots);
+        }
+    } else if constexpr (CH <= 2 || TEAM < 256 || (VEC && CH == 3)) {   // what team_for gives
         hipLaunchKernelGGL((layer_norm_bwd_kernel<IO, TEAM, CH, VEC>),
                            dim3(static_cast<unsigned>(slots * a.groups)), dim3(threads), 0, s, a, slots, partial);
     }
@@ -425,13 +452,14 @@ hipError_t launch_norm_team(const NormArgs& a, Team t, bool bwd, int threads, in
         case 512 * 8 + 2: return launch_norm<IO, 512, 2, VEC>(a, bwd, threads, slots, partial, s);
         case 512 * 8 + 3: return launch_norm<IO, 512, 3, VEC>(a, bwd, threads, slots, partial, s);
         case 512 * 8 + 4: return launch_norm<IO, 512, 4, VEC>(a, bwd, threads, slots, partial, s);
+        case 1024 * 8 + 2: return launch_norm<IO, 1024, 2, VEC>(a, bwd, threads, slots, partial, s);
     }
     return hipErrorInvalidValue;
 }
 
 hipError_t launch_norm_any(const NormArgs& a, bool bwd, int threads, int slots, float* partial, hipStream_t s) {
     const int64_t n = a.dim / a.groups;
-    const Team t = team_for(n, a.rows * a.groups);
+    const Team t = team_for(n, a.rows * a.groups, bwd);
     const bool vec = n % 8 == 0;
     if (a.io == kIoF32)
         return vec ? launch_norm_team<kIoF32, true>(a, t, bwd, threads, slots, partial, s)
@@ -448,7 +476,7 @@ hipError_t launch_layer_norm_fwd(const NormArgs& a, hipStream_t s) {
 
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups, int cu) {
     if (rows == 0 || dim == 0) return 0;
-    const BwdGrid g = bwd_grid(rows, groups, team_for(dim / groups, rows * groups).lanes, cu);
+    const BwdGrid g = bwd_grid(rows, groups, team_for(dim / groups, rows * groups, true).lanes, cu);
     return g.slots > 1 ? static_cast<size_t>(g.slots) * dim * 2 * sizeof(float) : 0;
 }
 
@@ -458,7 +486,7 @@ hipError_t launch_layer_norm_bwd(const NormArgs& a, int cu, void* ws, hipStream_
                            0, s, a.dim, a.dweight, a.dbias);
         return hipGetLastError();
     }
-    const BwdGrid g = bwd_grid(a.rows, a.groups, team_for(a.dim / a.groups, a.rows * a.groups).lanes, cu);
+    const BwdGrid g = bwd_grid(a.rows, a.groups, team_for(a.dim / a.groups, a.rows * a.groups, true).lanes, cu);
     float* partial = static_cast<float*>(ws);
     const hipError_t e = launch_norm_any(a, true, g.threads, g.slots, partial, s);
     if (e != hipSuccess || g.slots == 1 || (a.dweight == nullptr && a.dbias == nullptr)) return e;

@@ -86,7 +86,7 @@ def _check(x, dy, w, b, groups, what, eps=1e-5):
 
 # widths at the edges of every team of lanes, odd ones, one value
 WIDTHS = [1, 2, 7, 8, 64, 120, 128, 129, 256, 384, 385, 392, 512, 1000, 1024, 1531, 1536, 1537, 1544,
-          2048, 4095, 4096, 5120, 6144, 6145, 6152, 8192, 10001, 12288, 16383, 16384]
+          2048, 4095, 4096, 5120, 6144, 6145, 6152, 8192, 10001, 12288, 12289, 12296, 14223, 16383, 16384]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
