@@ -53,7 +53,7 @@
 // the state, P v) wait for each other at two barriers a chunk, with the matrix
 // cores 25% busy, the vector units 27% and LDS 31%. Cutting it into segments
 // for a second workgroup costs the states' pass more than the waiting (105 us).
-// The gradients (263 us, 87 by their bytes) hold two workgroups on a unit:
+// The gradients (250 us, 87 by their bytes) hold two workgroups on a unit:
 // matrix cores 31%, vector units 40% busy, much of it the terms' splitting.
 #pragma once
 
