@@ -232,8 +232,8 @@ struct Tile {
 
     // This thread's offset from a chunk's first token (walked backwards: from
     // its last), columns col0 on.
-    static __device__ __forceinline__ int offset(const HeadRows& h, int col0, bool rev) {
-        const int i = threadIdx.x / VPR, col = (col0 + threadIdx.x % VPR * kVec) * static_cast<int>(sizeof(T));
+    static __device__ __forceinline__ int offset(const HeadRows& h, int tid, int col0, bool rev) {
+        const int i = tid / VPR, col = (col0 + tid % VPR * kVec) * static_cast<int>(sizeof(T));
         return col < h.width ? (rev ? -i : i) * h.stride + col : kPastEnd;
     }
     __device__ __forceinline__ void load(const HeadRows& h, int off, int64_t first, int cnt, bool rev) {
@@ -244,8 +244,8 @@ struct Tile {
             r[u] = __builtin_bit_cast(
                 uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + (start + u * step), 0, 0));
     }
-    __device__ __forceinline__ void stage(T* lds) const {
-        T* p = lds + threadIdx.x / VPR * kRow + threadIdx.x % VPR * kVec;
+    __device__ __forceinline__ void stage(T* lds, int tid) const {
+        T* p = lds + tid / VPR * kRow + tid % VPR * kVec;
 #pragma unroll
         for (int u = 0; u < COUNT; ++u) *reinterpret_cast<uint4*>(p + u * ROWS * kRow) = r[u];
     }
@@ -303,8 +303,8 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t nblocks) {
 // One workgroup's walk: column block blk of pass ip over segment seg of (row,
 // head) bh. ALT: bf16: the state enters with three terms; fp32: blocks of 32
 // state rows past the head's width are left out. DG: the pass also forms the
-// decay's gradient.
-template <int IO, int DC, int MODE, bool ALT, bool DG>
+// decay's gradient. FAST: half of a state or less survives a chunk.
+template <int IO, int DC, int MODE, bool ALT, bool DG, bool FAST>
 __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC, MODE>& lds, const int ip,
                                                  const int blk, int seg, const int64_t bh, const int64_t b,
                                                  const int hd) {
@@ -324,7 +324,12 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     constexpr bool EXACT = O::kSplit && ALT, SKIP = !O::kSplit && ALT;
     typedef LinLds<IO, DC, MODE> Lds;
     constexpr int RK = Lds::TileK::kRow, RV = Lds::TileV::kRow, RQ = Lds::TileQ::kRow, RX = Lds::TileX::kRow;
-    const int tid = threadIdx.x;
+    // each form's own thread index: derived from one, a thread's places would be
+    // worked out in front of the branch between the forms and held from there
+    // (gradients of 4 x 4096 x 24 heads of 32 x 64 in fp32: 388 us against 422; of
+    // 8 x 2048 x 32 heads of 64 in bf16: 200 against 208)
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid) : "n"(FAST));
     const int lane = tid & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int c = lane & 15, g = lane >> 4;
@@ -374,8 +379,8 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     const HeadRows rv(ps.v, row0, ps.hv, ps.hv == a.heads ? hd : shared, dout, sizeof(T));
     const HeadRows rq(ps.q, row0, ps.hq, ps.hq == a.heads ? hd : shared, dc, sizeof(T));
     const HeadRows rx(ps.x, row0, a.heads, hd, dout, sizeof(T));
-    const int ok = Lds::TileK::offset(rk, 0, rev), ov = Lds::TileV::offset(rv, p0, rev);
-    const int oq = Lds::TileQ::offset(rq, 0, rev), ox = Lds::TileX::offset(rx, p0, rev);
+    const int ok = Lds::TileK::offset(rk, tid, 0, rev), ov = Lds::TileV::offset(rv, tid, p0, rev);
+    const int oq = Lds::TileQ::offset(rq, tid, 0, rev), ox = Lds::TileX::offset(rx, tid, p0, rev);
     const int64_t nchunks = (ntok + C - 1) / C;
     // chunk ch of the walk: its first token in the segment and count (0 past
     // the end); both directions cut at the same tokens
@@ -474,10 +479,16 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
 #pragma unroll
         for (int it = 0; it < NT; ++it) eo[it] = ps.out_scale * lds.pow[16 * it + c + 1 - r];
     }
-    // lam^cnt - 1 of whole chunks and of a short one
-    const int short_cnt = static_cast<int>(ntok % C);
-    const float em_full = uniform(g1 == 0.0f ? 0.0f : expm1f(g1 * static_cast<float>(C)));
-    const float em_short = uniform(g1 == 0.0f || short_cnt == 0 ? 0.0f : expm1f(g1 * static_cast<float>(short_cnt)));
+    // what a chunk makes of the state it is entered with: lam^cnt S (FAST), whose
+    // factor is off by its own rounding, gone with the state after few chunks; or
+    // S + (lam^cnt - 1) S, which rounds only the change (a factor next to 1 applied
+    // chunk after chunk would drift, and a change next to -1 rounds at the old
+    // state's size where a far smaller one is to be left)
+    auto change = [&](int cnt) {
+        if (FAST) return uniform(lds.pow[cnt]);
+        return uniform(g1 == 0.0f || cnt == 0 ? 0.0f : expm1f(g1 * static_cast<float>(cnt)));
+    };
+    const float change_full = change(C), change_short = change(static_cast<int>(ntok % C));
     // where this lane's outputs go: token 16 it + c, columns 4 g .. + 3 of the
     // wave's
     const bool wide = IO == kIoF32 || (kBwd && ps.out32);
@@ -535,10 +546,10 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         int cnt;
         chunk_at(ch, first, cnt);
         // (1) stage. The tiles' last readers passed the barrier before P V.
-        tk.stage(lds.K);
-        if constexpr (!kState) tq.stage(lds.Q);
-        tv.stage(lds.V);
-        if constexpr (DG) tx.stage(lds.X);
+        tk.stage(lds.K, tid);
+        if constexpr (!kState) tq.stage(lds.Q, tid);
+        tv.stage(lds.V, tid);
+        if constexpr (DG) tx.stage(lds.X, tid);
         if (cnt != wcnt) {
             wcnt = cnt;
             weigh(cnt);
@@ -683,22 +694,22 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
 #pragma unroll
         for (int s = 0; s < NS; ++s) vf[s] = O::template tr<RV, 4>(lds.V, 32 * s, kLinCols * wc, c, g);
 
-        // (4) the state: S + (lam^cnt - 1) S, which rounds only the change (a
-        // factor next to 1 applied chunk after chunk would drift by its own
-        // rounding), then the chunk's tokens
-        const float em = cnt == C ? em_full : em_short;
+        // (4) the state: what is left of it, then the chunk's tokens
+        const float kept = cnt == C ? change_full : change_short;
         if constexpr (DG) {
             // the derivative, with the steps that the state takes here
-            const float f = uniform(static_cast<float>(cnt) * lds.pow[cnt]);
+            const float f = uniform(FAST ? static_cast<float>(cnt) : static_cast<float>(cnt) * lds.pow[cnt]);
 #pragma unroll
             for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) D[nt][v] = fmaf(S[nt][v], f, fmaf(D[nt][v], em, D[nt][v]));
+                for (int v = 0; v < 4; ++v)
+                    D[nt][v] = FAST ? fmaf(S[nt][v], f, D[nt][v]) * kept
+                                    : fmaf(S[nt][v], f, fmaf(D[nt][v], kept, D[nt][v]));
         }
 #pragma unroll
         for (int nt = 0; nt < NN; ++nt)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) S[nt][v] = fmaf(S[nt][v], em, S[nt][v]);
+            for (int v = 0; v < 4; ++v) S[nt][v] = FAST ? S[nt][v] * kept : fmaf(S[nt][v], kept, S[nt][v]);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const f32x4 w0 = *reinterpret_cast<const f32x4*>(&lds.W[32 * s + 8 * g]);
@@ -789,23 +800,8 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
         }
     }
 
-    if (!DG && sout != nullptr) {   // the pass of dq leaves no state
-        // A fast head's chunks leave S + em S, em within 2^-25 of lam^cnt - 1, of
-        // the entering state, an error of 2^-25 of it where it should be down to
-        // lam^cnt: put right here, since a large entering state may show through
-        // what little a short sequence adds (later chunks wipe it out)
-        const float kept_full = 1.0f + em_full, kept_short = 1.0f + em_short;   // exact below a half
-        if (!kState && sin != nullptr && ntok > 0 && (kept_full <= 0.5f || kept_short <= 0.5f)) {
-            float kept = kept_short;
-            for (int64_t n = ntok / C; n > 0 && kept > 1e-37f; --n) kept *= kept_full;
-            const float missing = decay_power(g1, ntok < 65536 ? static_cast<int>(ntok) : 65536) - kept;
-            load_state(sin, [&](int nt, f32x4 x) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) S[nt][v] = fmaf(x[v], missing, S[nt][v]);
-            });
-        }
+    if (!DG && sout != nullptr)   // the pass of dq leaves no state
         store_state(sout + (kState ? bh * a.nseg + seg : bh) * state_elems);
-    }
     if constexpr (!kState) {
         // rows behind the sequence's end: zeros
         const int64_t z0 = end > seg0 ? end : seg0;
@@ -840,8 +836,30 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
     }
 }
 
+// The walk in the form that fits the head's decay, the same for all its chunks:
+// chosen once, it costs the loop no operation (both forms as keep S + change S,
+// one operation more per value of the state: fp32, 2 x 2048 x 8 heads of 200 x
+// 168, 135 us against 130, gradients 476 against 466).
+template <int IO, int DC, int MODE, bool ALT, bool DG>
+__device__ __forceinline__ void linear_attn_walk_any(const LinArgs& a, LinLds<IO, DC, MODE>& lds, const int ip,
+                                                     const int blk, int seg, const int64_t bh, const int64_t b,
+                                                     const int hd) {
+    if (a.log_decay[hd] * static_cast<float>(LinOps<IO>::kChunk) <= -0.6931472f)
+        linear_attn_walk<IO, DC, MODE, ALT, DG, true>(a, lds, ip, blk, seg, bh, b, hd);
+    else
+        linear_attn_walk<IO, DC, MODE, ALT, DG, false>(a, lds, ip, blk, seg, bh, b, hd);
+}
+
+// Waves that a SIMD holds at least. fp32 gradients of heads of 64 fit three, which
+// the compiler misses by a few registers left to itself (8 x 2048 x 32 heads of
+// 64: 437 us against 448).
+constexpr int lin_waves_per_simd(int io, int dc, int mode) {
+    return io == kIoF32 && dc == 64 && mode == kLinBwd ? 3 : 2;
+}
+
 template <int IO, int DC, int MODE>
-__global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(LinArgs a) {
+__global__ __launch_bounds__(lin_waves(DC) * kWave,
+                             lin_waves_per_simd(IO, DC, MODE)) void linear_attn_kernel(LinArgs a) {
     __shared__ LinLds<IO, DC, MODE> lds;
     // which (row, head, segment, pass, column block); neighbours in this
     // order read the same rows and share an XCD's L2. The pass that forms the
@@ -875,18 +893,18 @@ __global__ __launch_bounds__(lin_waves(DC) * kWave, 2) void linear_attn_kernel(L
     if constexpr (MODE == kLinBwd) {
         if (first) {
             if (IO == kIoBF16 || unused)
-                linear_attn_walk<IO, DC, MODE, true, true>(a, lds, ip, blk, seg, up, row, hd);
+                linear_attn_walk_any<IO, DC, MODE, true, true>(a, lds, ip, blk, seg, up, row, hd);
             else
-                linear_attn_walk<IO, DC, MODE, IO == kIoBF16, true>(a, lds, ip, blk, seg, up, row, hd);
+                linear_attn_walk_any<IO, DC, MODE, IO == kIoBF16, true>(a, lds, ip, blk, seg, up, row, hd);
             return;
         }
     }
     // a state that the caller gets
     const bool leaves = ps.s_out != nullptr && seg == (ps.rev ? 0 : a.nseg - 1);
     if (IO == kIoBF16 ? (MODE == kLinState ? a.exact != 0 : leaves) : unused)
-        linear_attn_walk<IO, DC, MODE, true, false>(a, lds, ip, blk, seg, up, row, hd);
+        linear_attn_walk_any<IO, DC, MODE, true, false>(a, lds, ip, blk, seg, up, row, hd);
     else
-        linear_attn_walk<IO, DC, MODE, false, false>(a, lds, ip, blk, seg, up, row, hd);
+        linear_attn_walk_any<IO, DC, MODE, false, false>(a, lds, ip, blk, seg, up, row, hd);
 }
 
 }  // namespace
