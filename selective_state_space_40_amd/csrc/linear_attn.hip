@@ -20,12 +20,17 @@ struct Decay {
 
     __device__ __forceinline__ Decay(float g, int64_t n) : keep(1.0f), change(0.0f) {
         if (g == 0.0f || n == 0) return;
-        const float p = g * static_cast<float>(n);
+        // the exponent's rounding, put back as a factor 1 + e
+        const float steps = static_cast<float>(n);
+        const float p = g * steps;
+        const float e = fmaf(g, steps, -p) + g * static_cast<float>(n - static_cast<int64_t>(steps));
         if (p > -0.6931472f) {
             change = expm1f(p);
+            change = fmaf(e, 1.0f + change, change);
         } else {
+            const float x = expf(p);   // 0 for g = -inf, where e is none
             keep = 0.0f;
-            change = expf(p);
+            change = x > 0.0f ? fmaf(x, e, x) : x;
         }
     }
     __device__ __forceinline__ float of(float s) const { return fmaf(s, change, keep * s); }

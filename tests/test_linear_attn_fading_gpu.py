@@ -183,3 +183,22 @@ def test_one_large_token_at_a_chunks_edge(factor, dtype):
     i["v"][:, edge - 1] *= factor
     i["do"][:, 128 - edge] *= factor
     _check(_place(i), f"one token {factor} {dtype}", (0, 64, 128))
+
+
+def test_remainders_across_a_whole_segment():
+    # decays whose product with the segment's 192 tokens rounds by up to 3.8e-6 in
+    # fp32: as an exponent that would be as much of the state itself, past the bound
+    decays = [-0.4321, -0.4299, -0.436]
+    i = _make(385, 64, 64, F32, 11, decays=decays)
+    i["k"][:, :188] = 0.0
+    i["k"][:, 192:] = 0.0
+    i = _place(i)
+    lam = i["log_decay"].double().cpu().exp()
+    k, v = i["k"].double().cpu(), i["v"].double().cpu()
+    want = sum(lam.view(1, 3, 1, 1) ** (384 - t) * k[:, t, :, :, None] * v[:, t, :, None, :]
+               for t in range(188, 192))
+    for seg in (192, 448):
+        print(f"case whole segment segment_len={seg}", flush=True)
+        _, hL = ms.linear_attn_fwd(i["q"], i["k"], i["v"], i["log_decay"], segment_len=seg)
+        err = (hL.double().cpu() - want).flatten(2).norm(dim=-1) / want.flatten(2).norm(dim=-1)
+        assert (err <= STATE).all(), f"segment_len {seg}: {err.tolist()}"
