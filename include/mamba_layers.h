@@ -65,7 +65,10 @@ extern "C" {
  * MAMBA_ERR_UNSUPPORTED). What stands behind a row's length is never read.
  * Inside it a NaN or infinite value may, since the chunk products multiply the
  * causal mask's zeros by it, reach the earlier outputs of its own chunk of 64
- * tokens, in its own row and head. Sums and states are fp32; with bf16 I/O the
+ * tokens, in its own row and head, and gradients the later tokens' as well; and
+ * where the definition has an infinity, from infinite values or a state that
+ * overflows, NaN may come out. A row without tokens keeps an infinite h0 or dhL,
+ * and linear_attn_update an infinite h. Sums and states are fp32; with bf16 I/O the
  * products' operands are bf16; what reaches a state or a decay gradient that
  * the caller gets is carried as three bf16 terms, with fp32's accuracy.
  */

@@ -14,11 +14,13 @@ typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 
 // A state's decay over n steps of log decay g, as keep s + change s: a slow one
 // by its difference from 1, which rounds only the change, a fast one as a
-// factor, whose difference from 1 would round at the state's size.
+// factor, whose difference from 1 would round at the state's size. An infinity
+// stays one (inf - inf and 0 inf would be NaN) unless the decay is zero.
 struct Decay {
     float keep, change;
+    bool zero;
 
-    __device__ __forceinline__ Decay(float g, int64_t n) : keep(1.0f), change(0.0f) {
+    __device__ __forceinline__ Decay(float g, int64_t n) : keep(1.0f), change(0.0f), zero(false) {
         if (g == 0.0f || n == 0) return;
         // the exponent's rounding, put back as a factor 1 + e
         const float steps = static_cast<float>(n);
@@ -31,9 +33,12 @@ struct Decay {
             const float x = expf(p);   // 0 for g = -inf, where e is none
             keep = 0.0f;
             change = x > 0.0f ? fmaf(x, e, x) : x;
+            zero = p == -__builtin_inff();
         }
     }
-    __device__ __forceinline__ float of(float s) const { return fmaf(s, change, keep * s); }
+    __device__ __forceinline__ float of(float s) const {
+        return fabsf(s) == __builtin_inff() && !zero ? s : fmaf(s, change, keep * s);
+    }
 };
 
 // Join of the segments, in place: on entry seg[(b, h), s] holds what segment

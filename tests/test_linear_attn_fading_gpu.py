@@ -202,3 +202,28 @@ def test_remainders_across_a_whole_segment():
         _, hL = ms.linear_attn_fwd(i["q"], i["k"], i["v"], i["log_decay"], segment_len=seg)
         err = (hL.double().cpu() - want).flatten(2).norm(dim=-1) / want.flatten(2).norm(dim=-1)
         assert (err <= STATE).all(), f"segment_len {seg}: {err.tolist()}"
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-3, -0.3, -2.0])
+def test_infinite_states_of_rows_that_end_and_of_single_tokens(decay):
+    # a decay above zero times an infinity is that infinity: a row without tokens
+    # keeps its state as it is, whole or cut, and a token adds to it
+    inf = float("inf")
+    i = _place(_make(130, 16, 24, F32, 12, decays=[decay, 0.5 * decay], state=True))
+    h0 = i["h0"].clone()
+    h0[0, 0, 3, 5], h0[0, 1, 7, 0] = inf, -inf
+    none = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for seg in (0, 64, 192):
+        _, hL = ms.linear_attn_fwd(i["q"], i["k"], i["v"], i["log_decay"], h0, lengths=none, segment_len=seg)
+        assert torch.equal(hL, h0), f"segment_len {seg}"
+    got = ms.linear_attn_bwd(i["q"], i["k"], i["v"], i["log_decay"], i["h0"], do=i["do"], dhL=h0, lengths=none,
+                             segment_len=64)
+    assert torch.equal(got["dh0"], h0)
+    h, clean = h0.clone(), i["h0"].clone()
+    tok = [i[n][:, 0].contiguous() for n in ("q", "k", "v")]
+    ms.linear_attn_update(clean, *tok, i["log_decay"])
+    ms.linear_attn_update(h, *tok, i["log_decay"])
+    torch.cuda.synchronize()
+    assert h[0, 0, 3, 5] == inf and h[0, 1, 7, 0] == -inf
+    same = torch.isfinite(h0)
+    assert torch.equal(h[same], clean[same])
