@@ -16,7 +16,8 @@ namespace {
 using mamba::LinearAttnCall;
 using mamba::LinPlan;
 
-static_assert(mamba::kLinMaxDim == MAMBA_LINATTN_MAX_DIM, "head width limit");
+static_assert(mamba::kLinMaxDim == MAMBA_LINATTN_MAX_DIM && mamba::kLinMaxHeads == MAMBA_LINATTN_MAX_HEADS,
+              "limits of heads");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

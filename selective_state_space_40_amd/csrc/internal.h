@@ -163,7 +163,7 @@ hipError_t launch_ssd_fwd(const SsdArgs& a, hipStream_t stream);
 
 // Linear attention with a decay for each head (linear_attn_kernel.h).
 constexpr int kLinFwd = 0, kLinBwd = 1, kLinState = 2;      // kernel modes
-constexpr int kLinMaxDim = 256;   // widest head
+constexpr int kLinMaxDim = 256, kLinMaxHeads = 4096;   // widest head, most heads
 // Output columns of a workgroup; its waves have 16 each. Of heads wider than 128
 // two waves share 16 columns, each with half of the state's rows, since a wave
 // that holds all 256 leaves no registers (12 x 1500 x 10 heads of 192 x 72: 77 us

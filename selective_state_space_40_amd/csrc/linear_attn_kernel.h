@@ -195,8 +195,11 @@ struct LinOps<kIoF32> {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_rsrc(const void* p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
-// An offset past the end of every resource.
-constexpr int kPastEnd = static_cast<int>(0x80000000u);
+// The most bytes of a chunk's rows, and an offset past the end of every resource
+// that stays past it a chunk's rows on or, walked backwards, back, inside an int.
+constexpr int kChunkBytes = kLinChunkBF16 * kLinMaxHeads * kLinMaxDim * 4;
+constexpr int kPastEnd = 1 << 30;
+static_assert(kPastEnd - kChunkBytes >= kChunkBytes && kPastEnd + kChunkBytes > kPastEnd, "past the end both ways");
 
 // One head's rows of a (batch, seqlen, heads, dim) tensor from a segment's
 // first token on. A chunk's resource ends with its last valid token, so rows
