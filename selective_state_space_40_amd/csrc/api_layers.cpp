@@ -18,6 +18,7 @@ using mamba::LinPlan;
 
 static_assert(mamba::kLinMaxDim == MAMBA_LINATTN_MAX_DIM && mamba::kLinMaxHeads == MAMBA_LINATTN_MAX_HEADS,
               "limits of heads");
+static_assert(mamba::kNormMaxDim == MAMBA_NORM_MAX_DIM, "widest part of a norm");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

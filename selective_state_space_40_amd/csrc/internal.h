@@ -262,6 +262,8 @@ struct LinUpdateArgs {
 hipError_t launch_linear_attn_update(const LinUpdateArgs& a, hipStream_t s);
 
 // Layer norm over each of the `groups` equal parts of a row.
+constexpr int kNormMaxDim = 16384;   // widest part
+
 struct NormArgs {
     int64_t rows, dim, groups;
     int io;

@@ -386,13 +386,35 @@ struct Team {
 // The backward pass, which holds more per value, takes more lanes for the widest
 // parts, sooner for those that are loaded value by value (fp32, 2000 x 5001: 34
 // us with 512 lanes, 47 with 256).
-Team team_for(int64_t n, int64_t parts, bool bwd) {
+constexpr Team team_for(int64_t n, int64_t parts, bool bwd) {
     const int64_t wave = parts < kFewParts ? 1024 : 1536;
     int lanes = n <= 384 ? 16 : (n <= wave ? 64 : (n <= 6144 ? 256 : 512));
     if (bwd && n > 4096 && n % 8 != 0) lanes = 512;
     if (bwd && n > (n % 8 == 0 ? 12288 : 8192)) lanes = 1024;
     return {lanes, static_cast<int>((n + 8 * lanes - 1) / (8 * lanes))};
 }
+
+// Which teams' kernels are built: those that team_for gives for some part.
+constexpr bool norm_built(int lanes, int runs, bool vec, bool bwd) {
+    if (lanes == 16 || lanes == 64) return runs <= 3;
+    if (!bwd) return lanes == 256 ? runs <= 3 : lanes == 512 && runs >= 2 && runs <= 4;
+    if (lanes == 1024) return runs == 2;
+    return (lanes == 256 || lanes == 512) && (runs <= 2 || (vec && runs == 3));
+}
+
+// Parts of 8 k and of 8 k - 1 values stand for all: every bound in team_for is a
+// multiple of 8.
+constexpr bool teams_are_built() {
+    for (int64_t n = 8; n <= kNormMaxDim; n += 8)
+        for (int few = 0; few < 2; ++few)
+            for (int bwd = 0; bwd < 2; ++bwd) {
+                const int64_t parts = few ? 1 : int64_t(1) << 30;
+                const Team v = team_for(n, parts, bwd), o = team_for(n - 1, parts, bwd);
+                if (!norm_built(v.lanes, v.runs, true, bwd) || !norm_built(o.lanes, o.runs, false, bwd)) return false;
+            }
+    return true;
+}
+static_assert(teams_are_built(), "a kernel for every part");
 
 // Workgroups of the forward pass, when there are rows for them: several rounds
 // of what the chip holds, so that the last one's idle part is small.
@@ -419,8 +441,9 @@ BwdGrid bwd_grid(int64_t rows, int64_t groups, int lanes, int cu) {
 
 template <int IO, int TEAM, int CH, bool VEC>
 hipError_t launch_norm(const NormArgs& a, bool bwd, int threads, int slots, float* partial, hipStream_t s) {
+    if (!norm_built(TEAM, CH, VEC, bwd)) return hipErrorInvalidValue;
     if (!bwd) {
-        if constexpr (TEAM <= 512) {
+        if constexpr (norm_built(TEAM, CH, VEC, false)) {
             constexpr int TEAMS = (TEAM > 256 ? TEAM : 256) / TEAM;
             const int64_t most = (a.rows + TEAMS - 1) / TEAMS;
             const int turns = kFwdWorkgroups / static_cast<int>(a.groups < kFwdWorkgroups ? a.groups : kFwdWorkgroups);
@@ -429,7 +452,7 @@ hipError_t launch_norm(const NormArgs& a, bool bwd, int threads, int slots, floa
                                dim3(static_cast<unsigned>(row_slots * a.groups)), dim3(TEAM > 256 ? TEAM : 256), 0,
                                s, a, row_slots);
         }
-    } else if constexpr (CH <= 2 || TEAM < 256 || (VEC && CH == 3)) {   // what team_for gives
+    } else if constexpr (norm_built(TEAM, CH, VEC, true)) {
         hipLaunchKernelGGL((layer_norm_bwd_kernel<IO, TEAM, CH, VEC>),
                            dim3(static_cast<unsigned>(slots * a.groups)), dim3(threads), 0, s, a, slots, partial);
     }
