@@ -216,8 +216,8 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_fwd_kernel
 // (slot, column) pair per workgroup goes to `partial` (2, slots, dim), from
 // which layer_norm_columns_kernel adds the slots in order.
 // The widest parts take teams of 1024 lanes, whose 128 registers hold neither the
-// next row's loads nor a row's products: those are formed again after the sums
-// (bf16, 2665 x 15734: 203 us, 523 with 512 lanes of 32 values, spilled; of
+// next row's loads nor a row's products: those are formed again after the sums,
+// and of the columns' sums 20 to 24 values are spilled all the same (bf16, 2665 x 15734: 203 us, 523 with 512 lanes of 32 values, spilled; of
 // 12288 values that 512 lanes hold as 24 each: 48 us against 69).
 constexpr int kNormBwdThreads = 512;
 
@@ -421,15 +421,21 @@ static_assert(teams_are_built(), "a kernel for every part");
 constexpr int kFwdWorkgroups = 4096;
 
 // Threads per workgroup of the backward pass and slots (workgroups per group
-// of columns): about one workgroup of 512 per compute unit when there are
-// rows enough, smaller workgroups when there are not.
+// of columns): one workgroup of 512 per compute unit when there are rows enough.
+// More, smaller ones leave more partial sums than they save time (2000 x 1024 in
+// bf16: 9.9 us, with workgroups of 256, two to a unit, 13.4; 500 x 5120: 19 against
+// 28), but for teams of 16, of which few parts fill few workgroups (500 x 384: 7.3
+// us against 7.9; 2000 x 384 7.9 against 8.2, 4000 x 128 7.1 against 6.6), unless one
+// of 512 holds all rows and writes the sums itself (32 x 16 parts of 128: 4.1 us
+// against 5.6).
 struct BwdGrid {
     int threads, slots;
 };
 
 BwdGrid bwd_grid(int64_t rows, int64_t groups, int lanes, int cu) {
     int threads = kNormBwdThreads;
-    while (threads > 256 && threads > lanes && rows * groups * lanes / threads < cu) threads /= 2;
+    const bool one_holds_all = rows > 256 / 16 && rows <= kNormBwdThreads / 16;   // and a smaller one does not
+    if (lanes == 16 && !one_holds_all && rows * groups < 2048) threads = 256;
     if (threads < lanes) threads = lanes;
     const int64_t teams = threads / lanes;
     const int64_t most = (rows + teams - 1) / teams;
