@@ -375,9 +375,19 @@ __global__ __launch_bounds__(256) void layer_norm_zero_kernel(int64_t dim, float
 
 // Lanes and 8-value runs per lane for parts of n values. Between 1024 and 1536
 // values a wave with 24 values a lane moves most, but four waves end sooner where
-// there are few parts (gradients in fp32, 1000 x 1531: 12.6 us against 15.5;
-// 16000 x 1531: 74 against 57).
-constexpr int64_t kFewParts = 2048;
+// fewer parts than the chip has units leave it idle: up to one part for each where
+// lanes load 16 bytes, up to four where they load value by value, 24 loads to a
+// lane. In bf16, four waves against one, forward and gradients:
+//     200 x 1280   3.3 us against 3.6,   8.0 against 8.3
+//     400 x 1280   3.5 against 3.7,      9.3 against 8.5
+//     1000 x 1280  4.3 against 3.9,      10.7 against 9.5
+//     400 x 1300   4.4 against 6.1,      10.0 against 11.6
+//     1000 x 1300  5.4 against 6.3,      12.0 against 12.5
+//     2000 x 1300  7.9 against 7.0,      14.8 against 14.3
+// (1032 to 1536 and 1030 to 1531 alike, fp32 within 0.5 us of that). A wave with
+// 16 values a lane or fewer is never behind by more than 0.3 us (1000 x 760: 3.4
+// us against 4.1, gradients 7.9 against 10.0).
+constexpr int64_t kFewParts = 256, kFewOddParts = 4 * kFewParts;
 
 struct Team {
     int lanes, runs;
@@ -387,7 +397,7 @@ struct Team {
 // parts, sooner for those that are loaded value by value (fp32, 2000 x 5001: 34
 // us with 512 lanes, 47 with 256).
 constexpr Team team_for(int64_t n, int64_t parts, bool bwd) {
-    const int64_t wave = parts < kFewParts ? 1024 : 1536;
+    const int64_t wave = parts < (n % 8 == 0 ? kFewParts : kFewOddParts) ? 1024 : 1536;
     int lanes = n <= 384 ? 16 : (n <= wave ? 64 : (n <= 6144 ? 256 : 512));
     if (bwd && n > 4096 && n % 8 != 0) lanes = 512;
     if (bwd && n > (n % 8 == 0 ? 12288 : 8192)) lanes = 1024;
