@@ -181,12 +181,9 @@ int make_attn_plan(const LinearAttnCall& c, int passes, int64_t segment_len, Lin
     }
     const int64_t threads = passes * blocks * mamba::lin_waves(dc_pad) * mamba::kWave;
     if (c.batch * c.heads * p->nseg > kMaxThreads / threads) return MAMBA_ERR_UNSUPPORTED;
-    // the join's launch holds (row, head) in a 16-bit grid dimension
-    if (p->nseg > 1 && c.batch * c.heads > 65535) {
-        if (segment_len != 0) return MAMBA_ERR_UNSUPPORTED;
-        p->nseg = 1;
-        p->seg_len = c.seqlen;
-    }
+    // the join's launch holds (row, head) in a 16-bit grid dimension; the automatic
+    // division cuts calls of a few per compute unit only
+    if (p->nseg > 1 && c.batch * c.heads > 65535) return MAMBA_ERR_UNSUPPORTED;
     return MAMBA_OK;
 }
 
