@@ -76,9 +76,11 @@ def _reference(i):
     o, o_size, hL, states, squares = _walk(q, k, v, lam, h0, scale)
     dq, dq_size, *_ = _walk(do, v, k, lam, None if h0 is None else h0.transpose(-1, -2), scale)
     back = lambda x: x.flip(1)   # noqa: E731
-    dv, dv_size, first, adj, adj_squares = _walk(back(k), back(q), back(do), lam, None, scale)
-    dk, dk_size, *_ = _walk(back(v), back(do), back(q), lam, None, scale)
-    # _walk scales the output only: the adjoint is scale times its state
+    # _walk scales the output only: the adjoint is scale times its state, and
+    # enters the last token without that token's decay
+    end = None if i.get("dhL") is None else i["dhL"].double().cpu() / (scale * lam.view(1, h, 1, 1))
+    dv, dv_size, first, adj, adj_squares = _walk(back(k), back(q), back(do), lam, end, scale)
+    dk, dk_size, *_ = _walk(back(v), back(do), back(q), lam, None if end is None else end.transpose(-1, -2), scale)
     dh0 = scale * lam.view(1, h, 1, 1) * first
     adj, adj_squares = adj[::-1], adj_squares[::-1]
     dg = torch.zeros(h, dtype=torch.float64)
