@@ -72,6 +72,7 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(JoinArgs a) {
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
     if (a.init[dir] != nullptr)
         s = reinterpret_cast<const f32x4*>(a.init[dir] + bh * a.state_elems)[e];
+    const Decay full(g, a.seg_len);
     constexpr int U = 8;   // loads in flight
     for (int k0 = 0; k0 < a.nseg; k0 += U) {
         f32x4 add[U];
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(JoinArgs a) {
             seg[sg * quads] = s;
             int64_t n = len - sg * a.seg_len;
             n = n < 0 ? 0 : (n < a.seg_len ? n : a.seg_len);
-            const Decay decay(g, n);
+            const Decay decay = n == a.seg_len ? full : Decay(g, n);
 #pragma unroll
             for (int v = 0; v < 4; ++v) s[v] = decay.of(s[v]) + add[u][v];
         }
