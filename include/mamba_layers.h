@@ -70,7 +70,8 @@ extern "C" {
  * overflows, NaN may come out. A row without tokens keeps an infinite h0 or dhL,
  * and linear_attn_update an infinite h. Sums and states are fp32; with bf16 I/O the
  * products' operands are bf16; what reaches a state or a decay gradient that
- * the caller gets is carried as three bf16 terms, with fp32's accuracy.
+ * the caller gets is carried as three bf16 terms, with fp32's accuracy. Powers of
+ * the decay below 2^-126, the least normal fp32 number, may count as zero.
  */
 int linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
                                    int64_t dk, int64_t dv, int dtype, int64_t segment_len,

@@ -73,13 +73,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // formed, takes `longest` for 64 tokens and goes first, the other two passes
 // run beside and behind it (whether that gradient is wanted is not known here).
 // Microseconds measured on MI355X with one workgroup per unit; examples, cut
-// by this rule against not cut: one sequence of 65536, 16 heads of 128: 364 us
-// with 16 segments against 2.9 ms; 8 x 2048 x 16 heads of 128: 77 us whole
-// against 105 with 2, gradients 267 whole against 300 with 2; 4 x 1024 x 16
-// heads of 64: 27 us whole against 30 with 2, gradients 58 with 4 against 67;
-// gradients in fp32 of 2 x 333 x 6 heads: 40 us with 6 against 77; 2 x 2048 x
-// 8 heads of 200 x 168: 51 us with 5 against 98, gradients 158 with 2 against
-// 225.
+// by this rule against not cut: one sequence of 65536, 16 heads of 128: 365 us
+// with 16 segments against 1.79 ms; 8 x 2048 x 16 heads of 128: 73 us whole
+// against 103 with 2, gradients 255 whole against 314 with 2; 4 x 1024 x 16
+// heads of 64: 27 us whole against 31 with 2, gradients 53 with 4 against 66;
+// gradients in fp32 of 2 x 333 x 6 heads: 36 us with 6 against 71; 2 x 2048 x
+// 8 heads of 200 x 168: 53 us with 5 against 98, gradients 171 as cut, 156 with 2,
+// 222 whole.
 struct PlanCost {
     double chunk[2][3];   // [fp32, bf16][head width 64, 128, 256]
     double entry[3];

@@ -51,7 +51,10 @@ __device__ __forceinline__ void team_sum(float (&v)[NV], float* slot) {
 
 // A lane's CH x 8 values of a part of n. With VEC a lane holds runs of 8
 // consecutive values (the part is then a multiple of 8 values and starts on
-// 16 bytes); otherwise single values TEAM apart, for odd widths.
+// 16 bytes); otherwise single values TEAM apart, for odd widths, which an access
+// of 2 or 4 bytes a lane holds to a fraction of the memory's rate (gradients in
+// bf16: 2665 x 15734 203 us, 46 by its bytes; in fp32: 2000 x 5001 34 us, 22 by
+// them).
 template <int IO, int TEAM, int CH, bool VEC>
 struct Part {
     static constexpr int kWords = VEC ? (IO == kIoF32 ? 2 : 1) : 0;

@@ -51,10 +51,13 @@
 // against 50 for its bytes at the rate of a large copy. It is a workgroup per
 // compute unit: each SIMD has one wave, whose steps (staging, q k^T and q S, P,
 // the state, P v) wait for each other at two barriers a chunk, with the matrix
-// cores 25% busy, the vector units 27% and LDS 31%. Cutting it into segments
-// for a second workgroup costs the states' pass more than the waiting (105 us).
-// The gradients (250 us, 87 by their bytes) hold two workgroups on a unit:
-// matrix cores 31%, vector units 40% busy, much of it the terms' splitting.
+// cores 25% busy, the vector units 26% and LDS 31%. Cutting it into segments
+// for a second workgroup costs the states' pass more than the waiting (103 us).
+// The gradients (255 us, 87 by their bytes) hold two workgroups on a unit:
+// matrix cores 33%, vector units 41% busy, much of it the terms' splitting.
+// fp32 takes the exact fp32 instruction (137 TFLOP/s in a large product, bf16
+// 1196) and forms P for every 64 columns and every pass anew: 2 x 2048 x 8 heads of
+// 200 x 168 in 131 us forward and 466 with gradients, 32 and 80 by their operations.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -842,7 +845,7 @@ __device__ __forceinline__ void linear_attn_walk(const LinArgs& a, LinLds<IO, DC
 // The walk in the form that fits the head's decay, the same for all its chunks:
 // chosen once, it costs the loop no operation (both forms as keep S + change S,
 // one operation more per value of the state: fp32, 2 x 2048 x 8 heads of 200 x
-// 168, 135 us against 130, gradients 476 against 466).
+// 168, 135 us against 131, gradients 476 against 466).
 template <int IO, int DC, int MODE, bool ALT, bool DG>
 __device__ __forceinline__ void linear_attn_walk_any(const LinArgs& a, LinLds<IO, DC, MODE>& lds, const int ip,
                                                      const int blk, int seg, const int64_t bh, const int64_t b,
