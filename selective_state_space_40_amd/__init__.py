@@ -762,14 +762,14 @@ def _norm_checked(x, groups):
     if x.dim() < 1:
         raise ValueError("x must be (..., dim)")
     dim = x.shape[-1]
-    if groups < 1 or dim % groups:
+    if groups < 1 or dim % groups or dim == 0:
         raise ValueError(f"{dim} channels do not split into {groups} groups")
     if x.dtype not in _DTYPES:
         raise ValueError(f"unsupported I/O dtype {x.dtype}")
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("tensors must be on a GPU device")
-    return x.numel() // dim if dim else 0, dim, _require(x, "x", x.shape, x.dtype, dev)
+    return x.numel() // dim, dim, _require(x, "x", x.shape, x.dtype, dev)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, *, groups=1, eps=1e-5, out=None):

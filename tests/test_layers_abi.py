@@ -213,3 +213,13 @@ def test_binding_checks_its_arguments():
         ms.layer_norm_fwd(t(4, 10).double())
     with pytest.raises(TypeError):
         ms.layer_norm_fwd(None)
+
+
+def test_binding_refuses_a_norm_without_channels():
+    # its mean has no value, which the call would leave unwritten
+    for shape in ((4, 0), (0,), (2, 3, 0)):
+        with pytest.raises(ValueError, match="channels"):
+            ms.layer_norm_fwd(torch.zeros(*shape))
+        with pytest.raises(ValueError, match="channels"):
+            ms.layer_norm_bwd(torch.zeros(*shape), None, torch.zeros(*shape[:-1], 1), torch.zeros(*shape[:-1], 1),
+                              dy=torch.zeros(*shape))
