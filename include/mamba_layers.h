@@ -141,7 +141,7 @@ int linear_attn_update(int64_t batch, int64_t heads, int64_t kv_heads, int64_t d
  * mean, rstd   (rows, groups) fp32        optional: what the backward pass reads
  * dim is a multiple of groups (else MAMBA_ERR_INVALID_ARG) and dim / groups at
  * most MAMBA_NORM_MAX_DIM, dim at most 2^27, groups 2^22 and rows * groups 2^30
- * (else MAMBA_ERR_UNSUPPORTED). rows == 0 is a no-op.
+ * (else MAMBA_ERR_UNSUPPORTED). rows == 0 or dim == 0 is a no-op.
  */
 int layer_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int dtype, const void* x,
                    const float* weight, const float* bias, float eps, void* y, float* mean,
