@@ -1,7 +1,7 @@
 """Selective state-space scan for AMD Instinct MI355X (gfx950).
 
-Python binding of the C ABI in include/mamba_scan.h and
-include/mamba_layers.h. It only marshals
+Python binding of the C ABI in include/mamba_scan.h, include/mamba_layers.h
+and include/mamba_gated.h. It only marshals
 arguments: it checks shapes and dtypes, allocates outputs and scratch with
 torch on the tensors' device, and passes raw device pointers and the current
 HIP stream to libmamba_scan.so, whose kernels do every step of the scan.
@@ -22,6 +22,14 @@ There is no other code path: without the built library every call raises.
     o = linear_attn_update(h, q, k, v, log_decay)              # h updated in place
     y, mean, rstd = layer_norm_fwd(x, weight=None, bias=None, groups=1)
     grads = layer_norm_bwd(x, weight, mean, rstd, dy=dy, groups=1)
+    y, hL, block_states = gated_scan_fwd(x, decay_gate, log_decay, input_gate=None, h0=None)
+    grads = gated_scan_bwd(x, decay_gate, log_decay, input_gate, block_states=block_states,
+                           dy=dy, dhL=None)
+    y = gated_scan_update(h, x, decay_gate, log_decay, input_gate=None)   # h updated in place
+    y, rstd = gated_norm_fwd(x, z=None, weight=None, groups=1, gate_first=True)
+    grads = gated_norm_bwd(x, z, weight, rstd, dy=dy, groups=1, gate_first=True)
+    y, total, rstd = residual_norm_fwd(x, residual, scale=None, weight=None)
+    grads = residual_norm_bwd(total, weight, rstd, x, scale, dy=dy, dtotal=None)
 
 Shapes (row-major, contiguous): x, delta, z, y (batch, L, dim); B, C
 (batch, L, N); A (dim, N) fp32; D and delta_bias (dim,) fp32; h0, hL
@@ -33,7 +41,12 @@ x, delta, z, B and C share one dtype, float32 or bfloat16, and y has it too.
 Linear attention takes q, o (batch, L, heads, dk or dv), k, v (batch, L,
 kv_heads, dk or dv), log_decay (heads,) fp32, states (batch, heads, dk, dv) fp32
 and lengths (batch,) int32; layer norm x, y (..., dim), weight and bias (dim,)
-fp32, mean and rstd (..., groups) fp32.
+fp32, mean and rstd (..., groups) fp32. The gated recurrence takes x, gates and y
+(batch, L, dim), log_decay (dim,) fp32 and states (batch, dim) fp32; the gated
+norm x, z, y (..., dim), weight (dim,) fp32, rstd (..., groups) fp32; the residual
+norm x, y (..., dim), the residual stream (..., dim) in the dtype of x or fp32,
+scale and weight (dim,) fp32. x, z and the gates of the gated operators may be
+slices of a wider tensor's channels (rows a fixed stride apart).
 """
 import collections
 import ctypes
@@ -44,12 +57,15 @@ import torch
 
 __all__ = ["scan_fwd", "scan_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "scan_bwd", "ssd_fwd", "state_update", "conv1d_fwd", "conv1d_update",
            "linear_attn_fwd", "linear_attn_bwd", "linear_attn_update", "layer_norm_fwd",
-           "layer_norm_bwd", "workspace_size", "resolve_plan", "library_path",
+           "layer_norm_bwd", "gated_scan_fwd", "gated_scan_bwd", "gated_scan_update",
+           "GATED_SCAN_BLOCK", "gated_norm_fwd", "gated_norm_bwd", "residual_norm_fwd",
+           "residual_norm_bwd", "workspace_size", "resolve_plan", "library_path",
            "load_library", "MambaScanError", "MAX_DSTATE", "ScanPlan", "ScanOptions", "Plan",
            "CARRY_AUTO", "CARRY_RERUN", "CARRY_REPAIR", "HALVES_AUTO", "HALVES_NONE"]
 
 MAX_DSTATE = 16
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # MAMBA_NOALLOC_SCRATCH_BYTES
+GATED_SCAN_BLOCK = 64   # MAMBA_GATED_SCAN_BLOCK: tokens between block_states
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -145,6 +161,30 @@ def load_library():
     lib.layer_norm_bwd_workspace_size.restype = i32
     lib.layer_norm_bwd.argtypes = [i64] * 3 + [i32] + [vp] * 9 + [sz, vp]
     lib.layer_norm_bwd.restype = i32
+    psz = ctypes.POINTER(sz)
+    for fn in (lib.gated_scan_fwd_workspace_size, lib.gated_scan_bwd_workspace_size):
+        fn.argtypes = [i64] * 3 + [i32, psz]
+        fn.restype = i32
+    gates = [vp, i64, vp, i64, vp, vp, i64]   # x, decay_gate, log_decay, input_gate, strides
+    lib.gated_scan_fwd.argtypes = [i64] * 3 + [i32] + gates + [vp] * 5 + [vp, sz, vp]
+    lib.gated_scan_fwd.restype = i32
+    lib.gated_scan_bwd.argtypes = [i64] * 3 + [i32] + gates + [vp] * 9 + [vp, sz, vp]
+    lib.gated_scan_bwd.restype = i32
+    lib.gated_scan_update.argtypes = [i64] * 2 + [i32, vp] + gates + [vp, vp]
+    lib.gated_scan_update.restype = i32
+    lib.gated_norm_fwd.argtypes = [i64] * 3 + [i32] * 2 + [vp, i64, vp, i64, vp, f32] + [vp] * 3
+    lib.gated_norm_fwd.restype = i32
+    lib.gated_norm_bwd_workspace_size.argtypes = [i64] * 3 + [i32, psz]
+    lib.gated_norm_bwd_workspace_size.restype = i32
+    lib.gated_norm_bwd.argtypes = ([i64] * 3 + [i32] * 2 + [vp, i64, vp, i64] + [vp] * 6 +
+                                   [vp, sz, vp])
+    lib.gated_norm_bwd.restype = i32
+    lib.residual_norm_fwd.argtypes = [i64] * 2 + [i32] * 2 + [vp] * 4 + [f32] + [vp] * 4
+    lib.residual_norm_fwd.restype = i32
+    lib.residual_norm_bwd_workspace_size.argtypes = [i64] * 2 + [i32] * 2 + [psz]
+    lib.residual_norm_bwd_workspace_size.restype = i32
+    lib.residual_norm_bwd.argtypes = [i64] * 2 + [i32] * 2 + [vp] * 11 + [vp, sz, vp]
+    lib.residual_norm_bwd.restype = i32
     lib.mamba_status_string.argtypes = [i32]
     lib.mamba_status_string.restype = ctypes.c_char_p
     _LIB = lib
@@ -820,3 +860,293 @@ def layer_norm_bwd(x, weight, mean, rstd, *, dy, groups=1, want_dbias=True, out=
     if st:
         _check(st, "layer_norm_bwd")
     return dict(dx=dx, dweight=dw, dbias=db)
+
+
+def _rows(t, name, shape, dtype, dev):
+    """The address of an input and the elements between its rows of channels: a
+    dense tensor, or a slice of a wider one's channels. The cheap test comes
+    first, _rows_checked says what is wrong."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
+                and t.is_contiguous()):
+            return t.data_ptr(), shape[-1]
+    except AttributeError:
+        pass
+    return _rows_checked(t, name, shape, dtype, dev)
+
+
+def _rows_checked(t, name, shape, dtype, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _need(t, name, shape, dtype, dev)
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.numel() == 0:
+        return t.data_ptr(), shape[-1]
+    at, step, size = t.stride(), None, 1
+    for n, stride in zip(reversed(shape[:-1]), reversed(at[:-1])):
+        if n != 1:
+            if step is None:
+                step = stride // size if stride % size == 0 else -1
+            if stride != step * size:
+                step = -1
+            if step < shape[-1]:
+                break
+        size *= n
+    step = shape[-1] if step is None else step
+    if (at[-1] != 1 and shape[-1] != 1) or step < shape[-1]:
+        raise ValueError(f"{name}: rows of neighbouring channels a fixed stride apart are needed, "
+                         f"strides are {at}")
+    return t.data_ptr(), step
+
+
+def _gated_shape(x, ndim):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() != ndim:
+        raise ValueError(f"x must be (batch, {'L, ' if ndim == 3 else ''}dim)")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported I/O dtype {x.dtype}")
+    if x.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    return x.shape
+
+
+def _gates(x, decay_gate, log_decay, input_gate, shape, dt, dev):
+    """The arguments of a recurrence that its three calls share."""
+    i = (None, 0) if input_gate is None else _rows(input_gate, "input_gate", shape, dt, dev)
+    return (*_rows(x, "x", shape, dt, dev), *_rows(decay_gate, "decay_gate", shape, dt, dev),
+            _must(log_decay, "log_decay", shape[-1:], torch.float32, dev), *i)
+
+
+def gated_scan_fwd(x, decay_gate, log_decay, input_gate=None, h0=None, *, lengths=None,
+                   return_state=True, return_block_states=False, out=None, state_out=None):
+    """Gated linear recurrence over whole sequences: h_t = a_t h_(t-1) + sqrt(1 -
+    a_t^2) sigmoid(input_gate_t) x_t with a_t = exp(log_decay sigmoid(decay_gate_t)).
+    x and the gates (batch, L, dim), input_gate None: 1; log_decay (dim,) fp32,
+    <= 0; h0 (batch, dim) fp32; `lengths` (batch,) int32 the tokens of each row
+    (None: L), behind which y is zero. Returns (y, hL, block_states): y the states
+    in the dtype of x, hL (batch, dim) fp32 the one after each row's last token (None
+    when return_state is False; state_out may be h0), block_states (batch, ceil(L /
+    64), dim) fp32 those entering every 64 tokens, which gated_scan_bwd takes (None
+    unless wanted)."""
+    lib = load_library()
+    shape = _gated_shape(x, 3)
+    batch, seqlen, dim = shape
+    dev, dt = x.device, x.dtype
+    gates = _gates(x, decay_gate, log_decay, input_gate, shape, dt, dev)
+    pl = _require(lengths, "lengths", (batch,), torch.int32, dev)
+    p0 = _require(h0, "h0", (batch, dim), torch.float32, dev)
+    y, py = _output(out, "out", shape, dt, dev)
+    hL = ph = states = ps = None
+    if return_state:
+        hL, ph = _output(state_out, "state_out", (batch, dim), torch.float32, dev)
+    if return_block_states:
+        states, ps = _output(None, "block_states", (batch, -(-seqlen // GATED_SCAN_BLOCK), dim),
+                             torch.float32, dev)
+    code = _DTYPES[dt]
+    with _on(dev):
+        nbytes = _scratch_bytes("gated_scan_fwd_workspace_size", dev.index, batch, seqlen, dim, code)
+        ws = _scratch(dev, nbytes)
+        st = lib.gated_scan_fwd(batch, seqlen, dim, code, *gates, pl, p0, py, ph, ps,
+                                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "gated_scan_fwd")
+    return y, hL, states
+
+
+def gated_scan_bwd(x, decay_gate, log_decay, input_gate=None, *, block_states, dy, dhL=None,
+                   lengths=None, want_dlog_decay=True, want_dh0=True):
+    """Gradients of sum(dy * y) + sum(dhL * hL) for the gated_scan_fwd call with the
+    same inputs, block_states from it. Returns a dict: dx, ddecay_gate, dinput_gate
+    (like x; zero behind a row's length; dinput_gate None without an input gate),
+    dlog_decay (dim,) fp32 and dh0 (batch, dim) fp32, None when not wanted."""
+    lib = load_library()
+    shape = _gated_shape(x, 3)
+    batch, seqlen, dim = shape
+    dev, dt = x.device, x.dtype
+    gates = _gates(x, decay_gate, log_decay, input_gate, shape, dt, dev)
+    pl = _require(lengths, "lengths", (batch,), torch.int32, dev)
+    ps = _must(block_states, "block_states", (batch, -(-seqlen // GATED_SCAN_BLOCK), dim),
+               torch.float32, dev)
+    pdy = _must(dy, "dy", shape, dt, dev)
+    pdh = _require(dhL, "dhL", (batch, dim), torch.float32, dev)
+
+    def new(*size, dtype=torch.float32, wanted=True):
+        return torch.empty(size, dtype=dtype, device=dev) if wanted else None
+
+    g = dict(dx=new(*shape, dtype=dt), ddecay_gate=new(*shape, dtype=dt),
+             dinput_gate=new(*shape, dtype=dt, wanted=input_gate is not None),
+             dlog_decay=new(dim, wanted=want_dlog_decay), dh0=new(batch, dim, wanted=want_dh0))
+    code = _DTYPES[dt]
+    with _on(dev):
+        nbytes = _scratch_bytes("gated_scan_bwd_workspace_size", dev.index, batch, seqlen, dim, code)
+        ws = _scratch(dev, nbytes)
+        st = lib.gated_scan_bwd(batch, seqlen, dim, code, *gates, pl, ps, pdy, pdh,
+                                *(None if t is None else t.data_ptr() for t in g.values()),
+                                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "gated_scan_bwd")
+    return g
+
+
+def gated_scan_update(h, x, decay_gate, log_decay, input_gate=None, *, out=None):
+    """One token of the gated recurrence: h (batch, dim) fp32 is updated in place;
+    x and the gates (batch, dim); returns y (batch, dim), the new state in the dtype
+    of x."""
+    lib = load_library()
+    shape = _gated_shape(x, 2)
+    dev, dt = x.device, x.dtype
+    gates = _gates(x, decay_gate, log_decay, input_gate, shape, dt, dev)
+    ph = _must(h, "h", shape, torch.float32, dev)
+    y, py = _output(out, "out", shape, dt, dev)
+    with _on(dev):
+        st = lib.gated_scan_update(*shape, _DTYPES[dt], ph, *gates, py, _raw_stream(dev))
+    if st:
+        _check(st, "gated_scan_update")
+    return y
+
+
+def _norm_rows(x, groups):
+    """(rows, dim) of a norm's input, whose rows may be a stride apart."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() < 1:
+        raise ValueError("x must be (..., dim)")
+    dim = x.shape[-1]
+    if groups < 1 or dim == 0 or dim % groups:
+        raise ValueError(f"{dim} channels do not split into {groups} groups")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported I/O dtype {x.dtype}")
+    if x.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device")
+    return x.numel() // dim, dim
+
+
+def _gate_code(z, gate_first):
+    return 0 if z is None else 1 if gate_first else 2   # mamba_norm_gate
+
+
+def gated_norm_fwd(x, z=None, weight=None, *, groups=1, eps=1e-5, gate_first=True, out=None):
+    """The norm behind a block with its gate, over each of the `groups` equal parts
+    of the last dimension: y = v * rstd * weight with v = x * silu(z) and rstd =
+    (mean(v^2) + eps) ** -0.5; with gate_first False v = x and y = v * rstd * weight *
+    silu(z); without z no gate. weight (dim,) fp32. Returns (y, rstd), rstd (...,
+    groups) fp32, which gated_norm_bwd takes; out may be x or z where that is
+    dense."""
+    lib = load_library()
+    rows, dim = _norm_rows(x, groups)
+    dev, dt, shape = x.device, x.dtype, x.shape
+    px = _rows(x, "x", shape, dt, dev)
+    pz = (None, 0) if z is None else _rows(z, "z", shape, dt, dev)
+    pw = _require(weight, "weight", (dim,), torch.float32, dev)
+    y, py = _output(out, "out", shape, dt, dev)
+    rstd = torch.empty((*shape[:-1], groups), dtype=torch.float32, device=dev)
+    with _on(dev):
+        st = lib.gated_norm_fwd(rows, dim, groups, _DTYPES[dt], _gate_code(z, gate_first), *px, *pz,
+                                pw, eps, py, rstd.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "gated_norm_fwd")
+    return y, rstd
+
+
+def gated_norm_bwd(x, z, weight, rstd, *, dy, groups=1, gate_first=True, out=None):
+    """Gradients of sum(dy * y) for the gated_norm_fwd call with the same x, z and
+    weight, rstd from it. Returns a dict: dx (like x; out may be dy), dz (None without
+    z) and dweight (dim,) fp32 (None without a weight)."""
+    lib = load_library()
+    rows, dim = _norm_rows(x, groups)
+    dev, dt, shape = x.device, x.dtype, x.shape
+    px = _rows(x, "x", shape, dt, dev)
+    pz = (None, 0) if z is None else _rows(z, "z", shape, dt, dev)
+    pw = _require(weight, "weight", (dim,), torch.float32, dev)
+    pr = _must(rstd, "rstd", (*shape[:-1], groups), torch.float32, dev)
+    pdy = _must(dy, "dy", shape, dt, dev)
+    dx, pdx = _output(out, "out", shape, dt, dev)
+    dz = None if z is None else torch.empty(shape, dtype=dt, device=dev)
+    dw = None if weight is None else torch.empty(dim, dtype=torch.float32, device=dev)
+    code = _DTYPES[dt]
+    with _on(dev):
+        nbytes = 0
+        if dw is not None:
+            nbytes = _scratch_bytes("gated_norm_bwd_workspace_size", dev.index, rows, dim, groups, code)
+        ws = _scratch(dev, nbytes)
+        st = lib.gated_norm_bwd(rows, dim, groups, code, _gate_code(z, gate_first), *px, *pz, pw, pr,
+                                pdy, pdx, None if dz is None else dz.data_ptr(),
+                                None if dw is None else dw.data_ptr(),
+                                None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "gated_norm_bwd")
+    return dict(dx=dx, dz=dz, dweight=dw)
+
+
+def _stream_dtype(t, name, dt):
+    """The dtype code of the residual stream: the I/O dtype or fp32."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dt and t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be {dt} or torch.float32, is {t.dtype}")
+    return t.dtype
+
+
+def residual_norm_fwd(x, residual, scale=None, weight=None, *, eps=1e-5, out=None, total_out=None):
+    """The norm before a block with the residual sum: total = residual + scale * x,
+    y = total * rstd * weight with rstd = (mean(total^2) + eps) ** -0.5 over the last
+    dimension. residual (..., dim) in the dtype of x or fp32; scale and weight (dim,)
+    fp32, None: ones. Returns (y, total, rstd): y in the dtype of x, total in that of
+    residual, rstd (..., 1) fp32; residual_norm_bwd takes the last two. out may be x,
+    total_out residual."""
+    lib = load_library()
+    rows, dim = _norm_rows(x, 1)
+    dev, dt, shape = x.device, x.dtype, x.shape
+    px = _must(x, "x", shape, dt, dev)
+    rt = _stream_dtype(residual, "residual", dt)
+    pres = _must(residual, "residual", shape, rt, dev)
+    psc = _require(scale, "scale", (dim,), torch.float32, dev)
+    pw = _require(weight, "weight", (dim,), torch.float32, dev)
+    y, py = _output(out, "out", shape, dt, dev)
+    total, pt = _output(total_out, "total_out", shape, rt, dev)
+    rstd = torch.empty((*shape[:-1], 1), dtype=torch.float32, device=dev)
+    with _on(dev):
+        st = lib.residual_norm_fwd(rows, dim, _DTYPES[dt], _DTYPES[rt], px, pres, psc, pw, eps, py, pt,
+                                   rstd.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "residual_norm_fwd")
+    return y, total, rstd
+
+
+def residual_norm_bwd(total, weight, rstd, x=None, scale=None, *, dy, dtotal=None):
+    """Gradients of sum(dy * y) + sum(dtotal * total) for the residual_norm_fwd call
+    that gave total and rstd; x and scale as given to it (x is looked at with a scale
+    only). Returns a dict: dx (like dy), dresidual (like total), dscale (dim,) fp32
+    (None without a scale) and dweight (dim,) fp32 (None without a weight). Without a
+    scale and with a total in the dtype of dy, dx is dresidual, the same tensor."""
+    lib = load_library()
+    rows, dim = _norm_rows(dy, 1)
+    dev, dt, shape = dy.device, dy.dtype, dy.shape
+    pdy = _must(dy, "dy", shape, dt, dev)
+    rt = _stream_dtype(total, "total", dt)
+    pt = _must(total, "total", shape, rt, dev)
+    pw = _require(weight, "weight", (dim,), torch.float32, dev)
+    pr = _must(rstd, "rstd", (*shape[:-1], 1), torch.float32, dev)
+    psc = _require(scale, "scale", (dim,), torch.float32, dev)
+    px = None if scale is None else _must(x, "x", shape, dt, dev)
+    pdt = _require(dtotal, "dtotal", shape, rt, dev)
+    dres = torch.empty(shape, dtype=rt, device=dev)
+    dx = dres if scale is None and rt is dt else torch.empty(shape, dtype=dt, device=dev)
+    dsc = None if scale is None else torch.empty(dim, dtype=torch.float32, device=dev)
+    dw = None if weight is None else torch.empty(dim, dtype=torch.float32, device=dev)
+    codes = _DTYPES[dt], _DTYPES[rt]
+    with _on(dev):
+        nbytes = 0
+        if dsc is not None or dw is not None:
+            nbytes = _scratch_bytes("residual_norm_bwd_workspace_size", dev.index, rows, dim, *codes)
+        ws = _scratch(dev, nbytes)
+        st = lib.residual_norm_bwd(rows, dim, *codes, pt, pw, pr, px, psc, pdy, pdt,
+                                   None if dx is dres else dx.data_ptr(), dres.data_ptr(),
+                                   None if dsc is None else dsc.data_ptr(),
+                                   None if dw is None else dw.data_ptr(),
+                                   None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "residual_norm_bwd")
+    return dict(dx=dx, dresidual=dres, dscale=dsc, dweight=dw)

@@ -26,7 +26,8 @@ UNITS = [("api", "api.cpp", ()), ("noalloc", "noalloc.hip", ()), ("launch", "lau
      (f"-DMAMBA_VARIANT_IO={io}", f"-DMAMBA_VARIANT_SP={sp}", f"-DMAMBA_VARIANT_PART={part}"))
     for io in (0, 1) for sp in (0, 1) for part in (0, 1)] + [
     ("api_layers", "api_layers.cpp", ()), ("linear_attn", "linear_attn.hip", ()),
-    ("layer_norm", "layer_norm.hip", ())] + [
+    ("layer_norm", "layer_norm.hip", ()), ("api_gated", "api_gated.cpp", ()),
+    ("gated_scan", "gated_scan.hip", ()), ("gated_norm", "gated_norm.hip", ())] + [
     (f"linear_attn_io{io}_m{mode}", "linear_attn_variant.hip",
      (f"-DMAMBA_VARIANT_IO={io}", f"-DMAMBA_VARIANT_MODE={mode}"))
     for io in (0, 1) for mode in (0, 1, 2)]

@@ -284,6 +284,72 @@ hipError_t launch_layer_norm_fwd(const NormArgs& a, hipStream_t s);
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups, int cu);
 hipError_t launch_layer_norm_bwd(const NormArgs& a, int cu, void* ws, hipStream_t s);
 
+// The gated linear recurrence. Strides are elements between tokens (between
+// rows for the single token).
+constexpr int kGatedBlock = 64;   // tokens between the states kept for the backward pass
+
+struct GatedScanArgs {
+    int64_t batch, seqlen, dim;
+    int io;
+    int64_t x_stride, decay_stride, input_stride;
+    const void *x, *decay_gate, *input_gate;
+    const float* log_decay;
+    const int32_t* lengths;
+    const float* h0;
+    void* y;
+    float* hL;
+    float* states;       // (batch, blocks, dim): written forward, read backward
+    const void* dy;
+    const float* dhL;
+    void *dx, *ddecay, *dinput;
+    float *dlog_decay, *dh0;
+    float* h;            // the single token's state
+};
+
+size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a);
+size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a);
+hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, void* ws, hipStream_t s);
+hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, void* ws, hipStream_t s);
+hipError_t launch_gated_scan_update(const GatedScanArgs& a, hipStream_t s);
+
+// The norms around a block: gated (over parts of a row) and residual.
+constexpr int kGateNone = 0, kGateFirst = 1, kGateBehind = 2;
+constexpr int kGatedNormMaxDim = 16384;   // widest part
+
+struct GatedNormArgs {
+    int64_t rows, dim, groups;
+    int io, gate;
+    int64_t x_stride, z_stride;
+    float eps;
+    const void *x, *z;
+    const float* weight;
+    void* y;
+    float* rstd;         // (rows, groups), read by the backward pass
+    const void* dy;
+    void *dx, *dz;
+    float* dweight;
+};
+
+struct ResidualNormArgs {
+    int64_t rows, dim;
+    int io, total_io;
+    float eps;
+    const void *x, *residual;
+    const float *scale, *weight;
+    void *y, *total;     // total is read by the backward pass
+    float* rstd;         // (rows)
+    const void *dy, *dtotal;
+    void *dx, *dresidual;
+    float *dscale, *dweight;
+};
+
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, int cu, hipStream_t s);
+size_t gated_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups, int cu);
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, int cu, void* ws, hipStream_t s);
+hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a, int cu, hipStream_t s);
+size_t residual_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int cu);
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, int cu, void* ws, hipStream_t s);
+
 // Compute units of the current device, cached per device; a mamba_status.
 int current_cu_count(int* cu);
 
