@@ -8,13 +8,13 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "internal.h"
 
 namespace mamba {
 namespace {
-
-constexpr int kGsChannels = 64;   // channels of a workgroup
 
 // 2^x - 1 = 2^(x/2) 2 sinh(x ln2 / 2), by the odd series of sinh: for x in
 // (-1, 0] the terms left out are below 1e-9 of the value, which keeps its
@@ -61,117 +61,143 @@ __device__ __forceinline__ float sigmoid(float v) {
 
 // sigmoid(v) and 1 - sigmoid(v), each to its own accuracy.
 __device__ __forceinline__ void sigmoid_both(float v, float& p, float& rest) {
-    const float e = fast_exp2(fminf(-v * kLog2e, 126.0f));
+    const float x = -v * kLog2e;
+    const float e = fast_exp2(x > 126.0f ? 126.0f : x);   // a NaN stays one
     p = fast_rcp(1.0f + e);
     rest = e * p;
-    if (v != v) p = rest = v;   // the minimum above drops a NaN
 }
 
-constexpr int words_of(int io, int v) { return io == kIoF32 ? v : (v + 1) / 2; }
+// A value that is formed here and not later from what it is made of, which is
+// more to keep.
+__device__ __forceinline__ void formed(float& v) { asm volatile("" : "+v"(v)); }
 
-// A lane's V neighbouring channels of T tokens, as loaded.
-template <int IO, int V, int T>
-struct Raw {
-    static constexpr int K = words_of(IO, V);
-    uint32_t w[T][K];
+// An offset that the compiler takes for a new one, lest it keep the offsets of all
+// of a tile's tokens in registers from tile to tile.
+__device__ __forceinline__ uint32_t fresh(uint32_t at) {
+    asm volatile("" : "+v"(at));
+    return at;
+}
 
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t row_bytes) {
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int off = static_cast<int>(at + t * row_bytes);
-            if constexpr (IO == kIoBF16 && V == 1) {
-                w[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0);
-            } else if constexpr (K == 1) {
-                w[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
-            } else {
-                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                static_assert(K == 2, "words of a token");
-                const u32x2 r = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
-                w[t][0] = r[0];
-                w[t][1] = r[1];
-            }
-        }
-    }
-    __device__ __forceinline__ float get(int t, int v) const {
-        if constexpr (IO == kIoF32) return __uint_as_float(w[t][v]);
-        const uint32_t r = w[t][v / 2];
-        return __uint_as_float(v % 2 ? r & 0xffff0000u : r << 16);
-    }
-};
+#ifndef GS_FENCE
+#define GS_FENCE 2
+#endif
+// Keeps the arithmetic of a few tokens together, lest all of a segment's
+// intermediate values be alive at once.
+__device__ __forceinline__ void token_fence(int t) {
+    if (t % GS_FENCE == GS_FENCE - 1) __builtin_amdgcn_sched_barrier(0);
+}
 
-// Stores V neighbouring channels of one token.
+template <int IO>
+constexpr int size_of() { return IO == kIoF32 ? 4 : 2; }
+
+// V neighbouring channels of one token, in one access of at most 4 bytes: fp32 one,
+// bf16 one or two.
 template <int IO, int V>
-__device__ __forceinline__ void store_channels(__amdgpu_buffer_rsrc_t rs, uint32_t at, const float (&v)[V]) {
-    const int off = static_cast<int>(at);
-    if constexpr (IO == kIoBF16 && V == 1) {
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(v[0])), rs, off,
-                                              0, 0);
+__device__ __forceinline__ uint32_t load_value(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t row) {
+    static_assert(size_of<IO>() * V <= 4, "a token is one access");
+    if constexpr (size_of<IO>() * V == 4)
+        return __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(at), static_cast<int>(row), 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b16(rs, static_cast<int>(at), static_cast<int>(row), 0);
+}
+
+template <int IO>
+__device__ __forceinline__ float value(uint32_t w, int v) {
+    return v == 0 ? raw_to_f32<IO>(w) : __uint_as_float(w & 0xffff0000u);
+}
+
+template <int IO, int V>
+__device__ __forceinline__ void store_value(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t row, const float (&v)[V]) {
+    if constexpr (IO == kIoF32) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), rs, static_cast<int>(at), static_cast<int>(row), 0);
+    } else if constexpr (V == 1) {
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, static_cast<__bf16>(v[0])), rs,
+                                              static_cast<int>(at), static_cast<int>(row), 0);
     } else {
-        uint32_t w[words_of(IO, V)];
-#pragma unroll
-        for (int i = 0; i < words_of(IO, V); ++i) {
-            if constexpr (IO == kIoF32) {
-                w[i] = __float_as_uint(v[i]);
-            } else {
-                const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * i]));
-                const uint32_t hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * i + 1]));
-                w[i] = lo | hi << 16;
-            }
-        }
-        if constexpr (words_of(IO, V) == 1) {
-            __builtin_amdgcn_raw_buffer_store_b32(w[0], rs, off, 0, 0);
-        } else {
-            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0], w[1]}, rs, off, 0, 0);
-        }
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 o = __builtin_convertvector((f32x2{v[0], v[V - 1]}), bf16x2);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, o), rs, static_cast<int>(at),
+                                              static_cast<int>(row), 0);
     }
 }
 
 __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t seqlen) {
     if (lengths == nullptr) return seqlen;
-    const int64_t n = lengths[b];
+    // a scalar load: nothing writes lengths, and a vector one would wait behind all others
+    const int64_t n = ((const __attribute__((address_space(4))) int32_t*)lengths)[b];
     return n < 0 ? 0 : (n < seqlen ? n : seqlen);
 }
 
-// A workgroup's place: the tile of TILE tokens by 64 channels is cut into S
-// segments of T consecutive tokens, V of them side by side in a wave whose 64 / V
-// lanes hold V channels each. The buffer resources span a tile's rows, so loads
-// behind the row's last token give zeros and stores behind the sequence are
-// dropped; a lane without channels has an offset past every resource.
-template <int IO, int V, int T, int W>
+// A workgroup's place: 64 channels by W V segments of T consecutive tokens. Of a
+// wave, 64 / V lanes hold V channels each of one segment, the next lanes the next.
+constexpr int kGsChannels = kWave;
+
+template <int V>
 struct Place {
-    static constexpr int S = W * V, TILE = S * T;
-    static constexpr int SIZE = IO == kIoF32 ? 4 : 2;
-    static constexpr uint32_t kNowhere = 0x80000000u;
-    static_assert(TILE % kGatedBlock == 0 && kGatedBlock % T == 0, "blocks of states at segments");
-    int wave, sub, cl, seg, ch;   // ch: the lane's first channel; cl: within the workgroup
+    int wave, lane, sub, cl, ch;   // sub: the lane's segment in its wave; cl: its first channel in the workgroup, ch: of all
     bool in;
 
     __device__ __forceinline__ Place(int64_t dim, int64_t group) {
-        const int lane = threadIdx.x % kWave;
-        wave = threadIdx.x / kWave;
-        sub = lane / (kWave / V);
-        cl = lane % (kWave / V) * V;
-        seg = wave * V + sub;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        lane = threadIdx.x % kWave;
+        sub = V == 1 ? 0 : lane / (kWave / V);
+        cl = V == 1 ? lane : lane % (kWave / V) * V;
         ch = static_cast<int>(group * kGsChannels) + cl;
         in = ch < dim;
     }
-    __device__ __forceinline__ uint32_t offset(int64_t stride) const {
-        return in ? static_cast<uint32_t>((seg * T * stride + ch) * SIZE) : kNowhere;
+    __device__ __forceinline__ int segment() const { return wave * V + sub; }
+};
+
+// One tensor's tile as a wave walks its tokens: a buffer resource that spans the
+// tile's rows, so that loads behind the row's last token give zeros and stores
+// behind the sequence are dropped; a lane without a channel has an offset past every
+// resource. FULL: all of the tile's tokens are there, and the token's place goes into
+// the scalar offset, which costs no vector instruction; else into the lane's, as the
+// bounds check need not look at the scalar one.
+template <int IO, int V, int T, int W, bool FULL>
+struct Rows {
+    static constexpr int TILE = W * V * T;
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t at, row, step;
+
+    __device__ __forceinline__ Rows(const Place<V>& place, const void* p, int64_t first, int64_t stride, int64_t dim,
+                                    int64_t count) {
+        const int n = static_cast<int>(FULL || count > TILE ? TILE : count);
+        const int ld = static_cast<int>(stride);
+        rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(static_cast<const char*>(p) + first * stride * size_of<IO>()), 0,
+            n > 0 ? ((n - 1) * ld + static_cast<int>(dim)) * size_of<IO>() : 0, 0x00020000);
+        step = static_cast<uint32_t>(ld) * size_of<IO>();
+        uint32_t lane = static_cast<uint32_t>(place.ch) * size_of<IO>();
+        if (V > 1) lane += place.sub * T * step;
+        const uint32_t tokens = place.wave * V * T * step;
+        if (FULL) {
+            at = place.in ? lane : 0x80000000u;
+            row = tokens;
+        } else {
+            at = fresh(place.in ? lane + tokens : 0x80000000u);
+            row = 0;
+        }
     }
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* p, int64_t first, int64_t stride,
-                                                                  int64_t dim, int64_t count) {
-        const int64_t n = count < TILE ? count : TILE;
-        return __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(static_cast<const char*>(p) + first * stride * SIZE), 0,
-            n > 0 ? static_cast<int>(((n - 1) * stride + dim) * SIZE) : 0, 0x00020000);
+    __device__ __forceinline__ uint32_t load() const { return load_value<IO, V>(rs, at, row); }
+    __device__ __forceinline__ void store(const float (&v)[V]) const { store_value<IO, V>(rs, at, row, v); }
+    __device__ __forceinline__ void go(int tokens) {
+        if (FULL) row += tokens * step;
+        else at += tokens * step;
     }
 };
 
-// What precedes a lane's segment in its wave, and the wave's whole: a state c
-// that enters the wave enters the segment as 2^G c + h. BACK goes from the
-// last segment to the first.
-template <int V, bool BACK>
+// How many of a segment's T tokens lie before the row's end, `left` tokens away from
+// the tile's start.
+template <int T, int TILE>
+__device__ __forceinline__ int live_tokens(int segment, int64_t left) {
+    return static_cast<int>(left < TILE ? left : TILE) - segment * T;
+}
+
+// What precedes a lane's segment in its wave, and the wave's whole: a state c that
+// enters the wave enters the segment as P c + h.
+template <int V>
 struct Before {
     float P[V], h[V];
 
@@ -183,7 +209,7 @@ struct Before {
         }
 #pragma unroll
         for (int m = 1; m < V; m *= 2) {
-            const bool later = ((sub & m) != 0) != BACK;
+            const bool later = (sub & m) != 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float oP = __shfl_xor(allP[v], m * (kWave / V)), oh = __shfl_xor(allh[v], m * (kWave / V));
@@ -200,325 +226,763 @@ struct Before {
     }
 };
 
-// The forward pass. A workgroup walks one row's tiles; the state entering a
-// tile is known to every lane.
-template <int IO, int V, int T, int W, bool GATED>
-__global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs a, int64_t groups) {
-    typedef Place<IO, V, T, W> P;
-    typedef Raw<IO, V, T> R;
-    __shared__ float2 sums[2][W][kGsChannels];
-    const int64_t b = blockIdx.x / groups;
-    const P at(a.dim, blockIdx.x - b * groups);
-    const int64_t len = row_length(a.lengths, b, a.seqlen);
-    const int64_t blocks = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
-    float lam2[V], c[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        lam2[v] = at.in ? a.log_decay[at.ch + v] * kLog2e : 0.0f;
-        c[v] = at.in && a.h0 != nullptr ? a.h0[b * a.dim + at.ch + v] : 0.0f;
+// (G, h) of tokens followed by those of a next segment.
+__device__ __forceinline__ void append(float& G, float& h, float nextG, float nexth) {
+    h = fmaf(fast_exp2(nextG), h, nexth);
+    G += nextG;
+}
+
+// ---------------------------------------------------------------------------
+// How a tile learns the state that enters it. A workgroup that walks a row knows
+// it; where rows and channels are too few to fill the chip, tiles go to the
+// workgroups one by one (a chain), in the order of tickets taken from a counter:
+// all rows' and groups' first tiles, then all second ones. A tile's sum over its
+// tokens (G, h) is published at once, and what enters it is folded, always in the
+// same order, from the sums of the up to 7 tiles before it in its run of 8, of the
+// up to 7 runs before that in their stretch of 8 runs, and the state that enters
+// the stretch, which the stretch before publishes at its end. One of the workgroup's
+// waves does this, a lane for each channel.
+//
+// Every wait ends: a tile waits for words of tiles of smaller tickets only. A
+// ticket is taken by a workgroup that runs, running workgroups keep their place, and
+// a workgroup works on its tickets in their order. So the workgroup that holds the
+// smallest unfinished ticket of all is at work on it, and what that tile waits for
+// has been published by finished ones; it ends, and then the next.
+//
+// A word is one 64-bit access and carries its own mark, so no order between words
+// is needed: its high half is G, or 0 for a state, and all ones before it is
+// written, which no G is (a NaN is written as 0x7fc00000).
+constexpr int kRun = 8, kStretch = 64;
+
+typedef unsigned long long Word;
+constexpr Word kNoWord = ~0ull;
+
+__device__ __forceinline__ Word word_of(float G, float h) {
+    const uint32_t hi = G == G ? __float_as_uint(G) : 0x7fc00000u;
+    return static_cast<Word>(hi) << 32 | __float_as_uint(h);
+}
+__device__ __forceinline__ float word_G(Word w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
+__device__ __forceinline__ float word_h(Word w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+
+__device__ __forceinline__ void publish(Word* at, Word w) {
+    __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ Word look(const Word* at) {
+    return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ Word await(const Word* at, Word w) {
+#ifdef GS_SPIN
+    int limit = GS_SPIN;
+#endif
+    while (static_cast<uint32_t>(w >> 32) == 0xffffffffu) {
+#ifdef GS_SPIN
+        if (--limit == 0) break;
+#endif
+        __builtin_amdgcn_s_sleep(1);
+        w = look(at);
     }
-    const uint32_t off_x = at.offset(a.x_stride), off_d = at.offset(a.decay_stride),
-                   off_i = at.offset(a.input_stride), off_y = at.offset(a.dim);
-    const uint32_t step_x = static_cast<uint32_t>(a.x_stride) * P::SIZE,
-                   step_d = static_cast<uint32_t>(a.decay_stride) * P::SIZE,
-                   step_i = static_cast<uint32_t>(a.input_stride) * P::SIZE,
-                   step_y = static_cast<uint32_t>(a.dim) * P::SIZE;
-    R x, d, i;
-    auto fetch = [&](int64_t t0) {
-        const int64_t first = b * a.seqlen + t0;
-        d.load(P::rows(a.decay_gate, first, a.decay_stride, a.dim, len - t0), off_d, step_d);
-        if constexpr (GATED) i.load(P::rows(a.input_gate, first, a.input_stride, a.dim, len - t0), off_i, step_i);
-        x.load(P::rows(a.x, first, a.x_stride, a.dim, len - t0), off_x, step_x);
+    return w;
+}
+
+// The chain's scratch: a counter (256 bytes), then words for every (row, tile),
+// (row, run) and (row, stretch) of all channels.
+struct Chain {
+    uint32_t* ticket;
+    Word *tile, *run, *stretch;
+    uint32_t groups, columns, tiles, runs, stretches;
+    bool once;   // a workgroup for every tile
+    int64_t width;
+
+    __host__ __device__ Chain(void* ws, int64_t batch, int64_t seqlen, int64_t channel_groups, int tile_tokens) {
+        groups = static_cast<uint32_t>(channel_groups);
+        columns = static_cast<uint32_t>(batch * channel_groups);
+        tiles = static_cast<uint32_t>((seqlen + tile_tokens - 1) / tile_tokens);
+        runs = (tiles + kRun - 1) / kRun;
+        stretches = (tiles + kStretch - 1) / kStretch;
+        once = false;
+        width = channel_groups * kGsChannels;
+        ticket = static_cast<uint32_t*>(ws);
+        tile = reinterpret_cast<Word*>(static_cast<char*>(ws) + 256);
+        run = tile + batch * tiles * width;
+        stretch = run + batch * runs * width;
+    }
+    __host__ __device__ int64_t words() const {
+        return static_cast<int64_t>(columns / groups) * (static_cast<int64_t>(tiles) + runs + stretches) * width;
+    }
+};
+
+__global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint32_t* ticket, Word* words, int64_t pairs) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i == 0) *ticket = 0;
+    if (i < pairs) reinterpret_cast<ulonglong2*>(words)[i] = make_ulonglong2(kNoWord, kNoWord);
+}
+
+// The next ticket. (Through an address that the compiler takes for a lane's own: for
+// one that all lanes share it adds up their requests first and waits for the answer
+// at once, behind all loads on their way.)
+__device__ __forceinline__ uint32_t take_ticket(uint32_t* counter) {
+    uint32_t none = 0;
+    asm volatile("" : "+v"(none));
+    return __hip_atomic_fetch_add(counter + none, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// A ticket's place in the chain.
+constexpr uint32_t kNoTicket = 0xffffffffu;
+
+struct Link {
+    uint32_t j, b, group;   // position in the row, row, group of channels
+    bool any;
+
+    __device__ __forceinline__ Link(const Chain& ch, uint32_t n) {
+        j = n / ch.columns;
+        const uint32_t r = n - j * ch.columns;
+        b = r / ch.groups;
+        group = r - b * ch.groups;
+        any = n != kNoTicket && j < ch.tiles;
+    }
+};
+
+// The state that enters a tile, for the lane's channel col; the tile's own sum
+// (G, h) is published on the way. `start` enters the row (it is looked at in the
+// first stretch only), `out` leaves the tile.
+__device__ __forceinline__ float enter_tile(const Chain& ch, const Link& at, int64_t col, float G, float h,
+                                            float start, float& out) {
+    const int kt = at.j % kRun, kr = at.j % kStretch / kRun;
+    Word* tile = ch.tile + (static_cast<int64_t>(at.b) * ch.tiles + at.j) * ch.width + col;
+    Word* run = ch.run + (static_cast<int64_t>(at.b) * ch.runs + at.j / kRun) * ch.width + col;
+    Word* stretch = ch.stretch + (static_cast<int64_t>(at.b) * ch.stretches + at.j / kStretch) * ch.width + col;
+    publish(tile, word_of(G, h));
+    Word wt[kRun - 1], wr[kRun - 1], ws = word_of(0.0f, start);
+    const Word none = word_of(0.0f, 0.0f);
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u) wt[u] = u < kt ? look(tile - (kt - u) * ch.width) : none;
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u) wr[u] = u < kr ? look(run - (kr - u) * ch.width) : none;
+    if (at.j >= kStretch) ws = look(stretch);
+    float Gt = 0.0f, ht = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u)
+        if (u < kt) {
+            const Word w = await(tile - (kt - u) * ch.width, wt[u]);
+            append(Gt, ht, word_G(w), word_h(w));
+        }
+    if (kt == kRun - 1) {   // the run's last: its sum, before what enters it is known
+        float Ga = Gt, ha = ht;
+        append(Ga, ha, G, h);
+        publish(run, word_of(Ga, ha));
+    }
+    float Gr = 0.0f, hr = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kRun - 1; ++u)
+        if (u < kr) {
+            const Word w = await(run - (kr - u) * ch.width, wr[u]);
+            append(Gr, hr, word_G(w), word_h(w));
+        }
+    append(Gr, hr, Gt, ht);
+    const float c = carried(word_h(await(stretch, ws)), Gr, hr);
+    out = carried(c, G, h);
+    if (at.j % kStretch == kStretch - 1 && at.j + 1 < ch.tiles) publish(stretch + ch.width, word_of(0.0f, out));
+    return c;
+}
+
+// A tile of the forward pass.
+template <int IO, int V, int T, int W, bool GATED>
+struct FwdTile {
+    static constexpr int TILE = T * V * W;
+    static_assert(TILE % kGatedBlock == 0 && kGatedBlock % T == 0, "blocks of states at segments");
+    typedef Rows<IO, V, T, W, false> R;
+    typedef Place<V> P;
+    uint32_t x[T], d[T], i[T];
+    float ca[T][V], cu[T][V];
+    float P0[V], h0[V];   // what precedes the lane's segment in its wave
+
+    // Where the inputs of a tile are; `left` <= 0: nowhere.
+    struct In {
+        R d, i, x;
+        __device__ __forceinline__ In(const GatedScanArgs& a, const P& at, int64_t b, int64_t t0, int64_t left)
+            : d(at, a.decay_gate, b * a.seqlen + t0, a.decay_stride, a.dim, left),
+              i(at, a.input_gate, b * a.seqlen + t0, a.input_stride, a.dim, GATED ? left : 0),
+              x(at, a.x, b * a.seqlen + t0, a.x_stride, a.dim, left) {}
     };
-    int odd = 0;
-    if (len > 0) fetch(0);
-    for (int64_t t0 = 0; t0 < len; t0 += P::TILE) {
-        const int64_t left = len - t0;
-        const bool full = left >= P::TILE;
-        float ca[T][V], cu[T][V], G[V], hl[V];
+    __device__ __forceinline__ void load(int t, In& in) {
+        d[t] = in.d.load();
+        in.d.go(1);
+        if constexpr (GATED) {
+            i[t] = in.i.load();
+            in.i.go(1);
+        }
+        x[t] = in.x.load();
+        in.x.go(1);
+    }
+    // In the order of work()'s loads: a wait for one counts those behind it.
+    __device__ __forceinline__ void load_all(In in) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            load(t, in);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // Each token's inputs are used up and the next tile's loaded in their place, so
+    // that loads are on their way all the time. Tokens behind the row's end have no
+    // decay, so a = 1 and w = 0. The wave's sums go to LDS.
+    __device__ __forceinline__ void work(const P& at, const float (&lam2)[V], int64_t left, In next,
+                                         float2 (&sums)[W][kGsChannels]) {
+        const int live = live_tokens<T, TILE>(at.segment(), left);
+        float G[V], hl[V], P1[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) G[v] = hl[v] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < T; ++t) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const Decay1 e(sigmoid(d.get(t, v)), lam2[v]);
+                const Decay1 e(sigmoid(value<IO>(d[t], v)), t < live ? lam2[v] : 0.0f);
                 float w = __builtin_amdgcn_sqrtf(e.s);
-                if constexpr (GATED) w *= sigmoid(i.get(t, v));
+                if constexpr (GATED) w *= sigmoid(value<IO>(i[t], v));
                 ca[t][v] = e.a;
-                cu[t][v] = w * x.get(t, v);
-                float g = e.g2;
-                if (!full && at.seg * T + t >= left) {   // behind the row's end: the state stays
-                    ca[t][v] = 1.0f;
-                    cu[t][v] = g = 0.0f;
-                }
-                G[v] += g;
+                cu[t][v] = w * value<IO>(x[t], v);
+                formed(ca[t][v]);
+                formed(cu[t][v]);
+                G[v] += e.g2;
                 hl[v] = fmaf(ca[t][v], hl[v], cu[t][v]);
             }
-        if (t0 + P::TILE < len) fetch(t0 + P::TILE);
-        float wP[V], wG[V];
+            load(t, next);
+            token_fence(t);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            wP[v] = fast_exp2(G[v]);
-            wG[v] = G[v];
+            P1[v] = V > 1 ? fast_exp2(G[v]) : 1.0f;
 #pragma unroll
-            for (int m = 1; m < V; m *= 2) wG[v] += __shfl_xor(wG[v], m * (kWave / V));
+            for (int m = 1; m < V; m *= 2) G[v] += __shfl_xor(G[v], m * (kWave / V));
         }
-        const Before<V, false> before(at.sub, wP, hl);
-        if (at.sub == 0) {
+        const Before<V> before(at.sub, P1, hl);
 #pragma unroll
-            for (int v = 0; v < V; ++v) sums[odd][at.wave][at.cl + v] = make_float2(wG[v], hl[v]);
+        for (int v = 0; v < V; ++v) {
+            P0[v] = before.P[v];
+            h0[v] = before.h[v];
+            if (at.sub == 0) sums[at.wave][at.cl + v] = make_float2(G[v], hl[v]);
         }
-        __syncthreads();
+    }
+    // The outputs, from the states entering the tile.
+    __device__ __forceinline__ void finish(const GatedScanArgs& a, const P& at, int64_t b, int64_t t0, int64_t len,
+                                           const float2 (&sums)[W][kGsChannels], const float (&enter)[kGsChannels]) {
         float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float Gz = 0.0f, hz = 0.0f, Gw = 0.0f, hw = 0.0f;   // of the waves so far; before this wave
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float2 e = sums[odd][w][at.cl + v];
-                if (w == at.wave) {
-                    Gw = Gz;
-                    hw = hz;
-                }
-                hz = fmaf(fast_exp2(e.x), hz, e.y);
-                Gz += e.x;
-            }
-            h[v] = fmaf(before.P[v], carried(c[v], Gw, hw), before.h[v]);
-            c[v] = carried(c[v], Gz, hz);
+            float G = 0.0f, s = 0.0f;
+            for (int w = 0; w < at.wave; ++w) append(G, s, sums[w][at.cl + v].x, sums[w][at.cl + v].y);
+            h[v] = fmaf(P0[v], carried(enter[at.cl + v], G, s), h0[v]);
         }
-        odd ^= 1;
-        const int64_t tseg = t0 + at.seg * T;
-        if (a.states != nullptr && at.seg * T % kGatedBlock == 0 && tseg < len && at.in) {
-            float* s = a.states + (b * blocks + tseg / kGatedBlock) * a.dim + at.ch;
+        const int64_t tseg = t0 + at.segment() * T;
+        if (a.states != nullptr && at.segment() * T % kGatedBlock == 0 && tseg < len && at.in) {
+            const int64_t blocks = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
+            float* to = a.states + (b * blocks + tseg / kGatedBlock) * a.dim + at.ch;
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = h[v];
+            for (int v = 0; v < V; ++v) to[v] = h[v];
         }
-        const __amdgpu_buffer_rsrc_t out = P::rows(a.y, b * a.seqlen + t0, a.dim, a.dim, a.seqlen - t0);
+        R y(at, a.y, b * a.seqlen + t0, a.dim, a.dim, a.seqlen - t0);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            float y[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[v] = fmaf(ca[t][v], h[v], cu[t][v]);
-                y[v] = !full && at.seg * T + t >= left ? 0.0f : h[v];
-            }
-            store_channels<IO, V>(out, off_y + t * step_y, y);
+            for (int v = 0; v < V; ++v) h[v] = fmaf(ca[t][v], h[v], cu[t][v]);
+            y.store(h);
+            y.go(1);
+        }
+        if (len - t0 < TILE) none(a, at, b, t0, live_tokens<T, TILE>(at.segment(), len - t0));
+    }
+    // Zeros for a tile's tokens behind the row's last one, from the segment's `from`-th
+    // on (over what is there, which a lane's own stores are in order with).
+    static __device__ __forceinline__ void none(const GatedScanArgs& a, const P& at, int64_t b, int64_t t0, int from) {
+        R y(at, a.y, b * a.seqlen + t0, a.dim, a.dim, a.seqlen - t0);
+        const float zero[V] = {};
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            if (t >= from) y.store(zero);
+            y.go(1);
         }
     }
-    if (a.hL != nullptr && at.in && at.seg == 0) {
+};
+
+// The log decays of a lane's channels, as loaded; zero where there is none.
+template <int V>
+__device__ __forceinline__ void load_log_decay(const GatedScanArgs& a, const Place<V>& at, uint32_t (&w)[V]) {
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(a.log_decay), 0, static_cast<int>(a.dim) * 4, 0x00020000);
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.hL[b * a.dim + at.ch + v] = c[v];
+    for (int v = 0; v < V; ++v) w[v] = __builtin_amdgcn_raw_buffer_load_b32(rs, (at.ch + v) * 4, 0, 0);
+}
+
+template <int V>
+__device__ __forceinline__ void log2_decay(const uint32_t (&w)[V], float (&lam2)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) lam2[v] = __uint_as_float(w[v]) * kLog2e;
+}
+
+// One channel of (rows, dim), or zero.
+__device__ __forceinline__ float load_state(const float* p, int64_t row, int64_t dim, int64_t col) {
+    return p != nullptr && col < dim ? p[row * dim + col] : 0.0f;
+}
+
+// A tile's whole sum for one of the workgroup's channels.
+template <int W>
+__device__ __forceinline__ float2 tile_sum(const float2 (&sums)[W][kGsChannels], int cl) {
+    float G = 0.0f, h = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) append(G, h, sums[w][cl].x, sums[w][cl].y);
+    return make_float2(G, h);
+}
+
+#ifndef GS_CF
+#define GS_CF 0
+#endif
+#ifndef GS_FWD_WAVES
+#define GS_FWD_WAVES 1
+#endif
+// The forward pass, a workgroup walking one row's tiles. The waves take turns in
+// carrying the state over a tile, a lane for each channel.
+template <int IO, int V, int T, int W, bool GATED>
+__global__ __launch_bounds__(W* kWave, GS_FWD_WAVES) void gated_scan_fwd_kernel(GatedScanArgs a, int64_t groups) {
+    typedef FwdTile<IO, V, T, W, GATED> Tile;
+    typedef typename Tile::In In;
+    __shared__ float2 sums[2][W][kGsChannels];   // by turns, so that one barrier a tile is enough
+    __shared__ float enter[2][kGsChannels];
+    const int64_t b = blockIdx.x / groups, group = blockIdx.x - b * groups;
+    const Place<V> at(a.dim, group);
+    const int64_t len = row_length(a.lengths, b, a.seqlen), col = group * kGsChannels + at.lane;
+    float lam2[V];
+    uint32_t decays[V];
+    load_log_decay(a, at, decays);
+    log2_decay(decays, lam2);
+    if (at.wave == 0) enter[0][at.lane] = load_state(a.h0, b, a.dim, col);
+    Tile tile;
+    tile.load_all(In(a, at, b, 0, len));
+    int k = 0;
+    int64_t t0 = 0;
+    for (; t0 < len; t0 += Tile::TILE, ++k) {
+        const int odd = k & 1;
+        tile.work(at, lam2, len - t0, In(a, at, b, t0 + Tile::TILE, len - t0 - Tile::TILE), sums[odd]);
+        __syncthreads();
+        if (at.wave == k % W) {
+            const float2 all = tile_sum<W>(sums[odd], at.lane);
+            enter[odd ^ 1][at.lane] = carried(enter[odd][at.lane], all.x, all.y);
+        }
+        tile.finish(a, at, b, t0, len, sums[odd], enter[odd]);
     }
-    for (int64_t t0 = (len + P::TILE - 1) / P::TILE * P::TILE; t0 < a.seqlen; t0 += P::TILE) {
-        const __amdgpu_buffer_rsrc_t out = P::rows(a.y, b * a.seqlen + t0, a.dim, a.dim, a.seqlen - t0);
-        const float none[V] = {};
+    __syncthreads();
+    if (a.hL != nullptr && at.wave == 0 && col < a.dim) a.hL[b * a.dim + col] = enter[k & 1][at.lane];
+    for (; t0 < a.seqlen; t0 += Tile::TILE) Tile::none(a, at, b, t0, 0);
+}
+
+// The forward pass as a chain. A workgroup takes tickets until none is left, one
+// ahead of the tile whose inputs are being loaded.
+template <int IO, int V, int T, int W, bool GATED>
+__global__ __launch_bounds__(W* kWave, GS_FWD_WAVES) void gated_scan_fwd_chain_kernel(GatedScanArgs a, Chain ch) {
+    typedef FwdTile<IO, V, T, W, GATED> Tile;
+    typedef typename Tile::In In;
+    __shared__ float2 sums[2][W][kGsChannels];   // by turns: read behind a tile's second barrier
+    __shared__ float enter[kGsChannels];
+    __shared__ uint32_t taken[2];
+    if (threadIdx.x == 0) {
+        taken[0] = take_ticket(ch.ticket);
+        taken[1] = ch.once ? kNoTicket : take_ticket(ch.ticket);
+    }
+    __syncthreads();
+    Link at(ch, __builtin_amdgcn_readfirstlane(taken[0])), next(ch, __builtin_amdgcn_readfirstlane(taken[1]));
+    __syncthreads();
+    Tile tile;
+    auto left_of = [&](const Link& l) {
+        return l.any ? row_length(a.lengths, l.b, a.seqlen) - static_cast<int64_t>(l.j) * Tile::TILE : int64_t(0);
+    };
+    auto in_of = [&](const Link& l, int64_t left) {
+        return In(a, Place<V>(a.dim, l.group), l.b, static_cast<int64_t>(l.j) * Tile::TILE, left);
+    };
+    int64_t left = left_of(at);
+    uint32_t decays[V], next_decays[V];   // loaded ahead of the inputs: a wait for them would else be for all of those
+    load_log_decay(a, Place<V>(a.dim, at.group), decays);
+    tile.load_all(in_of(at, left));
+    for (int k = 0; at.any; ++k) {
+        const Place<V> place(a.dim, at.group);
+        load_log_decay(a, Place<V>(a.dim, next.group), next_decays);
+        const int64_t b = at.b, t0 = static_cast<int64_t>(at.j) * Tile::TILE, len = t0 + left,
+                      next_left = left_of(next), col = static_cast<int64_t>(at.group) * kGsChannels + place.lane;
+        uint32_t mine = kNoTicket;
+        if (threadIdx.x == 0 && !ch.once) mine = take_ticket(ch.ticket);
+        if (left > 0) {
+            float lam2[V];
+            log2_decay(decays, lam2);
+            const bool looks = place.wave == k % W;
+            tile.work(place, lam2, left, in_of(next, next_left), sums[k & 1]);
+            __syncthreads();
+            if (looks) {
+                const float2 all = tile_sum<W>(sums[k & 1], place.lane);
+                float out;
+                enter[place.lane] = enter_tile(ch, at, col, all.x, all.y, load_state(a.h0, b, a.dim, col), out);
+                if (a.hL != nullptr && left <= Tile::TILE && col < a.dim) a.hL[b * a.dim + col] = out;
+            }
+            if (threadIdx.x == 0) taken[0] = mine;
+            __syncthreads();
+            tile.finish(a, place, b, t0, len, sums[k & 1], enter);
+        } else {
+            tile.load_all(in_of(next, next_left));
+            Tile::none(a, place, b, t0, 0);
+            if (at.j == 0 && a.hL != nullptr && place.wave == 0 && col < a.dim)   // a row without tokens
+                a.hL[b * a.dim + col] = load_state(a.h0, b, a.dim, col);
+            __syncthreads();   // the ticket before this one has been read
+            if (threadIdx.x == 0) taken[0] = mine;
+            __syncthreads();
+        }
+        at = next;
+        left = next_left;
 #pragma unroll
-        for (int t = 0; t < T; ++t) store_channels<IO, V>(out, off_y + t * step_y, none);
+        for (int v = 0; v < V; ++v) decays[v] = next_decays[v];
+        next = Link(ch, __builtin_amdgcn_readfirstlane(taken[0]));
     }
 }
 
-// The backward pass: tiles from the last to the first. The state entering a
-// tile comes from the forward pass, the adjoint entering it from behind is known
-// to every lane.
-template <int IO, int V, int T, int W, bool GATED>
-__global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
-                                                                  double* partial) {
-    typedef Place<IO, V, T, W> P;
-    typedef Raw<IO, V, T> R;
-    __shared__ float4 sums[2][W][kGsChannels];   // G, what the tokens add to the state, to the adjoint
-    const int64_t b = blockIdx.x / groups;
-    const P at(a.dim, blockIdx.x - b * groups);
-    const int64_t len = row_length(a.lengths, b, a.seqlen);
-    const int64_t blocks = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
-    float lam2[V], D[V];
-    double dl[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        lam2[v] = at.in ? a.log_decay[at.ch + v] * kLog2e : 0.0f;
-        D[v] = at.in && a.dhL != nullptr ? a.dhL[b * a.dim + at.ch + v] : 0.0f;
-        dl[v] = 0.0;
+// A tile of the backward pass.
+template <int IO, int T, int W, bool GATED>
+struct BwdTile {
+    static constexpr int TILE = T * W;
+    static_assert(TILE % kGatedBlock == 0, "tiles start at kept states");
+    uint32_t x[T], d[T], i[T], dy[T];
+    float state;   // entering the tile
+    float ca[T], cw[T], cu[T], cp[T], cgr[T], cir[T], ck[T];
+
+    template <bool FULL>
+    struct In {
+        typedef Rows<IO, 1, T, W, FULL> R;
+        R d, i, x, dy;
+        const float* state;
+        __device__ __forceinline__ In(const GatedScanArgs& a, const Place<1>& at, int64_t b, int64_t t0, int64_t left)
+            : d(at, a.decay_gate, b * a.seqlen + t0, a.decay_stride, a.dim, left),
+              i(at, a.input_gate, b * a.seqlen + t0, a.input_stride, a.dim, left),
+              x(at, a.x, b * a.seqlen + t0, a.x_stride, a.dim, left),
+              dy(at, a.dy, b * a.seqlen + t0, a.dim, a.dim, left),
+              state(left > 0 && at.in
+                        ? a.states + (b * ((a.seqlen + kGatedBlock - 1) / kGatedBlock) + t0 / kGatedBlock) * a.dim + at.ch
+                        : nullptr) {}
+    };
+    template <bool FULL>
+    __device__ __forceinline__ void load(int t, In<FULL>& in) {
+        d[t] = in.d.load();
+        in.d.go(1);
+        if constexpr (GATED) {
+            i[t] = in.i.load();
+            in.i.go(1);
+        }
+        x[t] = in.x.load();
+        in.x.go(1);
     }
-    const uint32_t off_x = at.offset(a.x_stride), off_d = at.offset(a.decay_stride),
-                   off_i = at.offset(a.input_stride), off_y = at.offset(a.dim);
-    const uint32_t step_x = static_cast<uint32_t>(a.x_stride) * P::SIZE,
-                   step_d = static_cast<uint32_t>(a.decay_stride) * P::SIZE,
-                   step_i = static_cast<uint32_t>(a.input_stride) * P::SIZE,
-                   step_y = static_cast<uint32_t>(a.dim) * P::SIZE;
-    int odd = 0;
-    const int64_t tiles = (len + P::TILE - 1) / P::TILE;
-    for (int64_t t0 = (tiles - 1) * P::TILE; t0 >= 0; t0 -= P::TILE) {
-        const int64_t left = len - t0, first = b * a.seqlen + t0;
-        const bool full = left >= P::TILE;
-        R x, d, i, dy;
-        d.load(P::rows(a.decay_gate, first, a.decay_stride, a.dim, left), off_d, step_d);
-        dy.load(P::rows(a.dy, first, a.dim, a.dim, left), off_y, step_y);
-        if constexpr (GATED) i.load(P::rows(a.input_gate, first, a.input_stride, a.dim, left), off_i, step_i);
-        x.load(P::rows(a.x, first, a.x_stride, a.dim, left), off_x, step_x);
-        float c[V];
+    // In the order of the loads of work() and finish(): a wait for one counts those
+    // behind it.
+    __device__ __forceinline__ void load_all(In<false> in) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            c[v] = at.in ? a.states[(b * blocks + t0 / kGatedBlock) * a.dim + at.ch + v] : 0.0f;
-        float ca[T][V], cw[T][V], cp[T][V], cgr[T][V], cir[T][V], ck[T][V], G[V], hl[V], El[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) G[v] = hl[v] = El[v] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float p, rest;
-                sigmoid_both(d.get(t, v), p, rest);
-                const Decay1 e(p, lam2[v]);
-                const float rb = e.s > 1.1754944e-38f ? __builtin_amdgcn_rsqf(e.s) : (e.s == e.s ? 0.0f : e.s);
-                const float xv = x.get(t, v);
-                float w = e.s * rb, qx = xv;
-                if constexpr (GATED) {
-                    float q, qrest;
-                    sigmoid_both(i.get(t, v), q, qrest);
-                    w *= q;
-                    qx *= q;
-                    cir[t][v] = w * xv * qrest;
-                }
-                ca[t][v] = e.a;
-                cw[t][v] = w;
-                cp[t][v] = p;
-                cgr[t][v] = e.g2 * kLn2 * rest;
-                ck[t][v] = qx * (e.a * rb);
-                float g = e.g2, u = w * xv;
-                if (!full && at.seg * T + t >= left) {
-                    ca[t][v] = 1.0f;
-                    u = g = 0.0f;
-                }
-                G[v] += g;
-                hl[v] = fmaf(ca[t][v], hl[v], u);
-            }
-#pragma unroll
-        for (int t = T - 1; t >= 0; --t)
-#pragma unroll
-            for (int v = 0; v < V; ++v) El[v] = ca[t][v] * (dy.get(t, v) + El[v]);
-        float wP[V], wPb[V], wG[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            wP[v] = wPb[v] = fast_exp2(G[v]);
-            wG[v] = G[v];
-#pragma unroll
-            for (int m = 1; m < V; m *= 2) wG[v] += __shfl_xor(wG[v], m * (kWave / V));
+        for (int t = 0; t < T; ++t) {
+            load(t, in);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const Before<V, false> before(at.sub, wP, hl);
-        const Before<V, true> behind(at.sub, wPb, El);
-        if (at.sub == 0) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) sums[odd][at.wave][at.cl + v] = make_float4(wG[v], hl[v], El[v], 0.0f);
-        }
-        __syncthreads();
-        float h[V], A[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float Gz = 0.0f, hz = 0.0f, Gw = 0.0f, hw = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float4 e = sums[odd][w][at.cl + v];
-                if (w == at.wave) {
-                    Gw = Gz;
-                    hw = hz;
-                }
-                hz = fmaf(fast_exp2(e.x), hz, e.y);
-                Gz += e.x;
-            }
-            h[v] = fmaf(before.P[v], carried(c[v], Gw, hw), before.h[v]);
-            float Ez = 0.0f, Ew = 0.0f;
-            Gz = 0.0f;
-#pragma unroll
-            for (int w = W - 1; w >= 0; --w) {
-                const float4 e = sums[odd][w][at.cl + v];
-                if (w == at.wave) {
-                    Gw = Gz;
-                    Ew = Ez;
-                }
-                Ez = fmaf(fast_exp2(e.x), Ez, e.z);
-                Gz += e.x;
-            }
-            A[v] = fmaf(behind.P[v], carried(D[v], Gw, Ew), behind.h[v]);
-            D[v] = carried(D[v], Gz, Ez);
-        }
-        odd ^= 1;
-        float sum[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-        // ck becomes h_{t-1} - q x a / b
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                ck[t][v] = h[v] - ck[t][v];
-                h[v] = fmaf(ca[t][v], h[v], cw[t][v] * x.get(t, v));
-            }
-        const __amdgpu_buffer_rsrc_t ox = P::rows(a.dx, first, a.dim, a.dim, a.seqlen - t0),
-                                     od = P::rows(a.ddecay, first, a.dim, a.dim, a.seqlen - t0),
-                                     oi = P::rows(a.dinput, first, a.dim, a.dim, GATED ? a.seqlen - t0 : 0);
+        state = in.state != nullptr ? *in.state : 0.0f;
+        in.dy.go(T - 1);
 #pragma unroll
         for (int t = T - 1; t >= 0; --t) {
-            float vx[V], vd[V], vi[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const bool gone = !full && at.seg * T + t >= left;
-                const float At = dy.get(t, v) + A[v];
-                A[v] = ca[t][v] * At;
-                const float dg = gone ? 0.0f : A[v] * ck[t][v];
-                vx[v] = gone ? 0.0f : At * cw[t][v];
-                vd[v] = gone ? 0.0f : dg * cgr[t][v];
-                if constexpr (GATED) vi[v] = gone ? 0.0f : At * cir[t][v];
-                sum[v] = fmaf(dg, cp[t][v], sum[v]);
-            }
-            store_channels<IO, V>(ox, off_y + t * step_y, vx);
-            store_channels<IO, V>(od, off_y + t * step_y, vd);
-            if constexpr (GATED) store_channels<IO, V>(oi, off_y + t * step_y, vi);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) dl[v] += static_cast<double>(sum[v]);
-    }
-    if (a.dh0 != nullptr && at.in && at.seg == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.dh0[b * a.dim + at.ch + v] = D[v];
-    }
-    if (partial != nullptr) {
-        __shared__ double all[P::S][kGsChannels];
-#pragma unroll
-        for (int v = 0; v < V; ++v) all[at.seg][at.cl + v] = dl[v];
-        __syncthreads();
-        if (at.seg == 0 && at.in) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                double s = 0.0;
-#pragma unroll
-                for (int k = 0; k < P::S; ++k) s += all[k][at.cl + v];
-                partial[b * a.dim + at.ch + v] = s;
-            }
+            dy[t] = in.dy.load();
+            in.dy.go(-1);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    for (int64_t t0 = tiles * P::TILE; t0 < a.seqlen; t0 += P::TILE) {
-        const int64_t first = b * a.seqlen + t0;
-        const __amdgpu_buffer_rsrc_t ox = P::rows(a.dx, first, a.dim, a.dim, a.seqlen - t0),
-                                     od = P::rows(a.ddecay, first, a.dim, a.dim, a.seqlen - t0),
-                                     oi = P::rows(a.dinput, first, a.dim, a.dim, GATED ? a.seqlen - t0 : 0);
-        const float none[V] = {};
+    // As forward; the next tile's dy is loaded by finish(), which needs this one's.
+    template <bool FULL>
+    __device__ __forceinline__ void work(const Place<1>& at, float lam2, int64_t left, In<FULL>& next,
+                                         float2 (&sums)[W][kGsChannels], float2 (&backs)[W][kGsChannels]) {
+        const int live = FULL ? T : live_tokens<T, TILE>(at.wave, left);
+        float G = 0.0f, hl = 0.0f, El = 0.0f;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            store_channels<IO, V>(ox, off_y + t * step_y, none);
-            store_channels<IO, V>(od, off_y + t * step_y, none);
-            if constexpr (GATED) store_channels<IO, V>(oi, off_y + t * step_y, none);
+            float p, rest;
+            sigmoid_both(raw_to_f32<IO>(d[t]), p, rest);
+            const Decay1 e(p, t < live ? lam2 : 0.0f);
+            const float r = __builtin_amdgcn_rsqf(e.s);
+            const float rb = e.s < 1.1754944e-38f ? 0.0f : r;   // nothing enters: no derivative
+            const float xv = raw_to_f32<IO>(x[t]);
+            float w = e.s * rb, qx = xv;
+            if constexpr (GATED) {
+                float q, qrest;
+                sigmoid_both(raw_to_f32<IO>(i[t]), q, qrest);
+                w *= q;
+                qx *= q;
+                cir[t] = w * xv * qrest;
+                formed(cir[t]);
+            }
+            ca[t] = e.a;
+            cw[t] = w;
+            cu[t] = w * xv;
+            cp[t] = t < live ? p : 0.0f;
+            cgr[t] = e.g2 * kLn2 * rest;
+            ck[t] = qx * (e.a * rb);
+            formed(ca[t]);
+            formed(cw[t]);
+            formed(cu[t]);
+            formed(cp[t]);
+            formed(cgr[t]);
+            formed(ck[t]);
+            G += e.g2;
+            hl = fmaf(ca[t], hl, cu[t]);
+            load(t, next);
+            token_fence(t);
+        }
+#pragma unroll
+        for (int t = T - 1; t >= 0; --t) El = ca[t] * (raw_to_f32<IO>(dy[t]) + El);
+        sums[at.wave][at.lane] = make_float2(G, hl);
+        backs[W - 1 - at.wave][at.lane] = make_float2(G, El);   // in the order of the walk back
+    }
+    // The gradients, from the adjoints entering the tile from behind. Returns the
+    // wave's share of the decay's gradient.
+    template <bool FULL>
+    __device__ __forceinline__ float finish(const GatedScanArgs& a, const Place<1>& at, int64_t b, int64_t t0,
+                                            int64_t left, In<FULL>& next, const float2 (&sums)[W][kGsChannels],
+                                            const float2 (&backs)[W][kGsChannels],
+                                            const float (&enter)[kGsChannels]) {
+        typedef Rows<IO, 1, T, W, FULL> R;
+        const int64_t first = b * a.seqlen + t0;
+        float G = 0.0f, s = 0.0f;
+        for (int w = 0; w < at.wave; ++w) append(G, s, sums[w][at.lane].x, sums[w][at.lane].y);
+        float h = carried(state, G, s);
+        G = s = 0.0f;
+        for (int w = 0; w < W - 1 - at.wave; ++w) append(G, s, backs[w][at.lane].x, backs[w][at.lane].y);
+        float A = carried(enter[at.lane], G, s), sum = 0.0f;
+        state = next.state != nullptr ? *next.state : 0.0f;
+        // ck becomes h_{t-1} - q x a / b
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            ck[t] = h - ck[t];
+            h = fmaf(ca[t], h, cu[t]);
+        }
+        R ox(at, a.dx, first, a.dim, a.dim, a.seqlen - t0), od(at, a.ddecay, first, a.dim, a.dim, a.seqlen - t0),
+            oi(at, a.dinput, first, a.dim, a.dim, a.seqlen - t0);
+        ox.go(T - 1);
+        next.dy.go(T - 1);
+#pragma unroll
+        for (int t = T - 1; t >= 0; --t) {
+            const float At = raw_to_f32<IO>(dy[t]) + A;
+            A = ca[t] * At;
+            const float dg = A * ck[t];
+            sum = fmaf(dg, cp[t], sum);
+            dy[t] = next.dy.load();
+            next.dy.go(-1);
+            ox.store({At * cw[t]});
+            store_value<IO, 1>(od.rs, ox.at, ox.row, {dg * cgr[t]});
+            if constexpr (GATED) store_value<IO, 1>(oi.rs, ox.at, ox.row, {At * cir[t]});
+            ox.go(-1);
+            token_fence(t);
+        }
+        if (!FULL && left < TILE) none(a, at, b, t0, live_tokens<T, TILE>(at.wave, left));
+        return sum;
+    }
+    static __device__ __forceinline__ void none(const GatedScanArgs& a, const Place<1>& at, int64_t b, int64_t t0,
+                                                int from) {
+        typedef Rows<IO, 1, T, W, false> R;
+        const int64_t first = b * a.seqlen + t0;
+        R ox(at, a.dx, first, a.dim, a.dim, a.seqlen - t0), od(at, a.ddecay, first, a.dim, a.dim, a.seqlen - t0),
+            oi(at, a.dinput, first, a.dim, a.dim, a.seqlen - t0);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            if (t >= from) {
+                ox.store({0.0f});
+                store_value<IO, 1>(od.rs, ox.at, ox.row, {0.0f});
+                if constexpr (GATED) store_value<IO, 1>(oi.rs, ox.at, ox.row, {0.0f});
+            }
+            ox.go(1);
         }
     }
+};
+
+#ifndef GS_BWD_WAVES
+#define GS_BWD_WAVES 1
+#endif
+// The backward pass, a workgroup walking one row's tiles from the last to the
+// first. The state entering a tile comes from the forward pass.
+template <int IO, int T, int W, bool GATED>
+__global__ __launch_bounds__(W* kWave, GS_BWD_WAVES) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
+                                                                               double* partial) {
+    typedef BwdTile<IO, T, W, GATED> Tile;
+    __shared__ float2 sums[2][W][kGsChannels], backs[2][W][kGsChannels];
+    __shared__ float enter[2][kGsChannels];
+    const int64_t b = blockIdx.x / groups;
+    const Place<1> at(a.dim, blockIdx.x - b * groups);
+    const int64_t len = row_length(a.lengths, b, a.seqlen), live = (len + Tile::TILE - 1) / Tile::TILE;
+    float lam2[1];
+    uint32_t decays[1];
+    load_log_decay(a, at, decays);
+    log2_decay(decays, lam2);
+    double dl = 0.0;
+    if (at.wave == 0) enter[0][at.lane] = load_state(a.dhL, b, a.dim, at.ch);
+    Tile tile;
+    int64_t t0 = (live - 1) * Tile::TILE;
+    if (live > 0) tile.load_all(typename Tile::template In<false>(a, at, b, t0, len - t0));
+    int k = 0;
+    auto step = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        const int odd = k & 1;
+        typename Tile::template In<FULL> next(a, at, b, t0 - Tile::TILE, t0 > 0 ? Tile::TILE : 0);
+        tile.template work<FULL>(at, lam2[0], len - t0, next, sums[odd], backs[odd]);
+        __syncthreads();
+        if (at.wave == k % W) {
+            const float2 all = tile_sum<W>(backs[odd], at.lane);
+            enter[odd ^ 1][at.lane] = carried(enter[odd][at.lane], all.x, all.y);
+        }
+        dl += static_cast<double>(
+            tile.template finish<FULL>(a, at, b, t0, len - t0, next, sums[odd], backs[odd], enter[odd]));
+        t0 -= Tile::TILE;
+        ++k;
+    };
+    if (t0 >= 0) step(std::false_type());
+    while (t0 > 0) step(std::true_type());
+    if (t0 == 0) step(std::false_type());
+    __syncthreads();
+    if (a.dh0 != nullptr && at.wave == 0 && at.in) a.dh0[b * a.dim + at.ch] = enter[k & 1][at.lane];
+    if (partial != nullptr) {
+        __shared__ double all[W][kGsChannels];
+        all[at.wave][at.lane] = dl;
+        __syncthreads();
+        if (at.wave == 0 && at.in) {
+            double s = 0.0;
+#pragma unroll
+            for (int q = 0; q < W; ++q) s += all[q][at.lane];
+            partial[b * a.dim + at.ch] = s;
+        }
+    }
+    for (t0 = live * Tile::TILE; t0 < a.seqlen; t0 += Tile::TILE) Tile::none(a, at, b, t0, 0);
 }
 
-// The rows' sums of d(log_decay), in order.
-__global__ __launch_bounds__(256) void gated_scan_sum_kernel(int64_t rows, int64_t dim, const double* partial,
-                                                             float* out) {
-    const int64_t ch = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (ch >= dim) return;
+// The backward pass as a chain: position j of a row is its j-th tile from the
+// last one with tokens. `partial` holds the decay's gradient of every (row, tile),
+// zeros for tiles without tokens.
+template <int IO, int T, int W, bool GATED>
+__global__ __launch_bounds__(W* kWave, GS_BWD_WAVES) void gated_scan_bwd_chain_kernel(GatedScanArgs a, Chain ch,
+                                                                                     float* partial) {
+    typedef BwdTile<IO, T, W, GATED> Tile;
+    typedef typename Tile::template In<false> AnyIn;
+    __shared__ float2 sums[2][W][kGsChannels], backs[2][W][kGsChannels];   // by turns, as forward
+    __shared__ float enter[kGsChannels], shares[W][kGsChannels];
+    __shared__ uint32_t taken[2];
+    if (threadIdx.x == 0) {
+        taken[0] = take_ticket(ch.ticket);
+        taken[1] = ch.once ? kNoTicket : take_ticket(ch.ticket);
+    }
+    __syncthreads();
+    Link at(ch, __builtin_amdgcn_readfirstlane(taken[0])), next(ch, __builtin_amdgcn_readfirstlane(taken[1]));
+    __syncthreads();
+    Tile tile;
+    // a link's first token, -1 for one without tokens
+    auto first_of = [&](const Link& l) {
+        const int64_t len = row_length(a.lengths, l.b, a.seqlen);
+        const int64_t t0 = ((len + Tile::TILE - 1) / Tile::TILE - 1 - static_cast<int64_t>(l.j)) * Tile::TILE;
+        return l.any && t0 >= 0 ? t0 : int64_t(-1);
+    };
+    // The waves' shares of the decay's gradient are added up behind the next barrier.
+    float* due = nullptr;
+    auto put_share = [&](const Place<1>& place, int k) {
+        if (due != nullptr && place.wave == k % W) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) s += shares[q][place.lane];
+            *due = s;
+        }
+        due = nullptr;
+    };
+    auto left_of = [&](const Link& l, int64_t t0) {
+        return t0 < 0 ? int64_t(0) : row_length(a.lengths, l.b, a.seqlen) - t0;
+    };
+    int64_t t0 = first_of(at);
+    uint32_t decays[1], next_decays[1];   // as forward
+    load_log_decay(a, Place<1>(a.dim, at.group), decays);
+    tile.load_all(AnyIn(a, Place<1>(a.dim, at.group), at.b, t0, left_of(at, t0)));
+    int k = 0;
+    for (; at.any; ++k) {
+        const Place<1> place(a.dim, at.group), next_place(a.dim, next.group);
+        load_log_decay(a, next_place, next_decays);
+        const int64_t b = at.b, left = left_of(at, t0), next_t0 = first_of(next), next_left = left_of(next, next_t0);
+        uint32_t mine = kNoTicket;
+        if (threadIdx.x == 0 && !ch.once) mine = take_ticket(ch.ticket);
+        float* share = partial == nullptr || !place.in ? nullptr : partial + (b * ch.tiles + at.j) * a.dim + place.ch;
+        auto step = [&](auto full) {
+            constexpr bool FULL = decltype(full)::value;
+            typename Tile::template In<FULL> in(a, next_place, next.b, next_t0, next_left);
+            float lam2[1];
+            log2_decay(decays, lam2);
+            tile.template work<FULL>(place, lam2[0], left, in, sums[k & 1], backs[k & 1]);
+            __syncthreads();
+            put_share(place, k + 1);   // a wave that has not the chain's next word to find
+            if (place.wave == k % W) {
+                const float2 all = tile_sum<W>(backs[k & 1], place.lane);
+                float out;
+                enter[place.lane] =
+                    enter_tile(ch, at, place.ch, all.x, all.y, load_state(a.dhL, b, a.dim, place.ch), out);
+                if (a.dh0 != nullptr && t0 == 0 && place.in) a.dh0[b * a.dim + place.ch] = out;
+            }
+            if (threadIdx.x == 0) taken[0] = mine;
+            __syncthreads();
+            shares[place.wave][place.lane] =
+                tile.template finish<FULL>(a, place, b, t0, left, in, sums[k & 1], backs[k & 1], enter);
+            due = share;
+        };
+        if (GS_CF && left >= Tile::TILE && next_left >= Tile::TILE) {
+            step(std::true_type());
+        } else if (left > 0) {
+            step(std::false_type());
+        } else {
+            tile.load_all(AnyIn(a, next_place, next.b, next_t0, next_left));
+            Tile::none(a, place, b, static_cast<int64_t>(at.j) * Tile::TILE, 0);
+            if (at.j == 0 && a.dh0 != nullptr && place.wave == 0 && place.in)   // a row without tokens
+                a.dh0[b * a.dim + place.ch] = load_state(a.dhL, b, a.dim, place.ch);
+            if (share != nullptr && place.wave == 0) *share = 0.0f;
+            __syncthreads();   // the ticket before this one has been read
+            put_share(place, k + 1);
+            if (threadIdx.x == 0) taken[0] = mine;
+            __syncthreads();
+        }
+        at = next;
+        t0 = next_t0;
+        decays[0] = next_decays[0];
+        next = Link(ch, __builtin_amdgcn_readfirstlane(taken[0]));
+    }
+    __syncthreads();
+    put_share(Place<1>(a.dim, 0), 0);
+}
+
+// The sums of d(log_decay) over `slots` partial ones, in 64 bits and a fixed
+// order: 64 channels per workgroup, its 16 waves a sixteenth of the slots each, 4
+// loads in flight.
+constexpr int kSumWaves = 16;
+
+template <typename F>
+__global__ __launch_bounds__(kSumWaves* kWave) void gated_scan_sum_kernel(int64_t slots, int64_t dim, const F* partial,
+                                                                         float* out) {
+    __shared__ double red[kSumWaves][kWave];
+    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+    const int64_t ch = static_cast<int64_t>(blockIdx.x) * kWave + lane;
     double s = 0.0;
-    for (int64_t r = 0; r < rows; ++r) s += partial[r * dim + ch];
-    out[ch] = static_cast<float>(s);
+    if (ch < dim) {
+        constexpr int U = 4;
+        for (int64_t k0 = w; k0 < slots; k0 += U * kSumWaves) {
+            F x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t k = k0 + u * kSumWaves;
+                x[u] = k < slots ? partial[k * dim + ch] : F(0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) s += static_cast<double>(x[u]);
+        }
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && ch < dim) {
+        double t = 0.0;
+#pragma unroll
+        for (int k = 0; k < kSumWaves; ++k) t += red[k][lane];
+        out[ch] = static_cast<float>(t);
+    }
 }
 
 // Without tokens: dh0 = dhL, no gradient of the decay.
@@ -530,6 +994,8 @@ __global__ __launch_bounds__(256) void gated_scan_empty_kernel(int64_t state, in
         if (zero != nullptr && i < dim) zero[i] = 0.0f;
     }
 }
+
+constexpr int words_of(int io, int v) { return io == kIoF32 ? v : (v + 1) / 2; }
 
 // One token: V channels to a lane.
 template <int IO, int V>
@@ -590,28 +1056,134 @@ bool divides(const GatedScanArgs& a, int64_t v) {
            (a.input_gate == nullptr || a.input_stride % v == 0);
 }
 
+#ifndef GS_GRID
+#define GS_GRID 256
+#endif
+#ifndef GS_BGRID
+#define GS_BGRID 256
+#endif
+#ifndef GS_ONCE
+#define GS_ONCE 1024
+#endif
+#ifndef GS_FT
+#define GS_FT 16
+#define GS_FW 8
+#endif
+#ifndef GS_FCV
+#define GS_FCV 2
+#define GS_FCT 16
+#define GS_FCW 8
+#endif
+#ifndef GS_BT
+#define GS_BT 8
+#define GS_BW 8
+#endif
+#ifndef GS_BCT
+#define GS_BCT 16
+#define GS_BCW 8
+#endif
+#ifndef GS_CHAIN
+#define GS_CHAIN 256
+#endif
 int64_t groups_of(const GatedScanArgs& a) { return (a.dim + kGsChannels - 1) / kGsChannels; }
 
-template <int IO, int V, int T, int W>
-hipError_t launch_fwd(const GatedScanArgs& a, hipStream_t s) {
-    const int64_t groups = groups_of(a);
-    const dim3 grid(static_cast<unsigned>(a.batch * groups)), block(W * kWave);
-    if (a.input_gate != nullptr)
-        hipLaunchKernelGGL((gated_scan_fwd_kernel<IO, V, T, W, true>), grid, block, 0, s, a, groups);
-    else
-        hipLaunchKernelGGL((gated_scan_fwd_kernel<IO, V, T, W, false>), grid, block, 0, s, a, groups);
+// The kernels' shapes: V channels to a lane, T tokens to a segment, W waves.
+template <int IO_, int V_, int T_, int W_>
+struct Shape {
+    static constexpr int IO = IO_, V = V_, T = T_, W = W_, TILE = W * V * T;
+};
+
+template <int IO> using FwdWalk = Shape<IO, 1, GS_FT, GS_FW>;
+template <int IO, int V> using FwdChain = Shape<IO, V, V == 1 ? 16 : GS_FCT, V == 1 ? 8 : GS_FCW>;
+template <int IO> using BwdWalk = Shape<IO, 1, GS_BT, GS_BW>;
+template <int IO> using BwdChain = Shape<IO, 1, GS_BCT, GS_BCW>;
+
+// Channels to a lane of the forward chain.
+int fwd_chain_channels(const GatedScanArgs& a) { return a.io == kIoBF16 && divides(a, GS_FCV) ? GS_FCV : 1; }
+
+int chain_tile(const GatedScanArgs& a, bool bwd) {
+    if (bwd) return BwdChain<kIoF32>::TILE;
+    return fwd_chain_channels(a) == 1 ? FwdChain<kIoF32, 1>::TILE : FwdChain<kIoBF16, GS_FCV>::TILE;
+}
+
+// Whether a call runs as a chain.
+bool chained(const GatedScanArgs& a, bool bwd) {
+    return a.seqlen > chain_tile(a, bwd) && a.batch * groups_of(a) < GS_CHAIN;
+}
+
+Chain chain_of(const GatedScanArgs& a, void* ws, bool bwd) {
+    return Chain(ws, a.batch, a.seqlen, groups_of(a), chain_tile(a, bwd));
+}
+
+size_t chain_bytes(const Chain& ch) { return 256 + static_cast<size_t>(ch.words()) * sizeof(Word); }
+
+// Clears the chain's words; sets its grid.
+hipError_t begin_chain(Chain& ch, unsigned resident, unsigned* grid, hipStream_t s) {
+    const int64_t pairs = ch.words() / 2, total = static_cast<int64_t>(ch.columns) * ch.tiles;
+    ch.once = total <= GS_ONCE;
+    *grid = ch.once ? static_cast<unsigned>(total) : resident;
+    hipLaunchKernelGGL(gated_scan_clear_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, s,
+                       ch.ticket, ch.tile, pairs);
     return hipGetLastError();
 }
 
-template <int IO, int V, int T, int W>
-hipError_t launch_bwd(const GatedScanArgs& a, double* partial, hipStream_t s) {
-    const int64_t groups = groups_of(a);
-    const dim3 grid(static_cast<unsigned>(a.batch * groups)), block(W * kWave);
-    if (a.input_gate != nullptr)
-        hipLaunchKernelGGL((gated_scan_bwd_kernel<IO, V, T, W, true>), grid, block, 0, s, a, groups, partial);
-    else
-        hipLaunchKernelGGL((gated_scan_bwd_kernel<IO, V, T, W, false>), grid, block, 0, s, a, groups, partial);
+template <typename S, bool GATED>
+hipError_t launch_fwd_chain(const GatedScanArgs& a, void* ws, hipStream_t s) {
+    Chain ch = chain_of(a, ws, false);
+    unsigned grid = 0;
+    const hipError_t e = begin_chain(ch, GS_GRID, &grid, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<S::IO, S::V, S::T, S::W, GATED>), dim3(grid), dim3(S::W * kWave),
+                       0, s, a, ch);
     return hipGetLastError();
+}
+
+template <int IO, bool GATED>
+hipError_t launch_fwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
+    if (chained(a, false)) {
+        if constexpr (IO == kIoBF16)
+            if (fwd_chain_channels(a) > 1) return launch_fwd_chain<FwdChain<IO, GS_FCV>, GATED>(a, ws, s);
+        return launch_fwd_chain<FwdChain<IO, 1>, GATED>(a, ws, s);
+    }
+    typedef FwdWalk<IO> S;
+    const int64_t groups = groups_of(a);
+    hipLaunchKernelGGL((gated_scan_fwd_kernel<S::IO, S::V, S::T, S::W, GATED>),
+                       dim3(static_cast<unsigned>(a.batch * groups)), dim3(S::W * kWave), 0, s, a, groups);
+    return hipGetLastError();
+}
+
+template <typename F>
+hipError_t launch_sum(int64_t slots, int64_t dim, const F* partial, float* out, hipStream_t s) {
+    hipLaunchKernelGGL((gated_scan_sum_kernel<F>), dim3(static_cast<unsigned>((dim + kWave - 1) / kWave)),
+                       dim3(kSumWaves * kWave), 0, s, slots, dim, partial, out);
+    return hipGetLastError();
+}
+
+template <int IO, bool GATED>
+hipError_t launch_bwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
+    hipError_t e;
+    if (chained(a, true)) {
+        typedef BwdChain<IO> S;
+        Chain ch = chain_of(a, ws, true);
+        unsigned grid = 0;
+        float* partial = a.dlog_decay == nullptr
+                             ? nullptr
+                             : reinterpret_cast<float*>(static_cast<char*>(ws) + chain_bytes(ch));
+        e = begin_chain(ch, GS_BGRID, &grid, s);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<S::IO, S::T, S::W, GATED>), dim3(grid), dim3(S::W * kWave), 0,
+                           s, a, ch, partial);
+        e = hipGetLastError();
+        if (e != hipSuccess || partial == nullptr) return e;
+        return launch_sum(a.batch * ch.tiles, a.dim, partial, a.dlog_decay, s);
+    }
+    typedef BwdWalk<IO> S;
+    const int64_t groups = groups_of(a);
+    double* partial = a.dlog_decay != nullptr ? static_cast<double*>(ws) : nullptr;
+    hipLaunchKernelGGL((gated_scan_bwd_kernel<S::IO, S::T, S::W, GATED>),
+                       dim3(static_cast<unsigned>(a.batch * groups)), dim3(S::W * kWave), 0, s, a, groups, partial);
+    e = hipGetLastError();
+    return e != hipSuccess || partial == nullptr ? e : launch_sum(a.batch, a.dim, partial, a.dlog_decay, s);
 }
 
 template <int IO, int V>
@@ -623,15 +1195,24 @@ hipError_t launch_update(const GatedScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs&) { return 0; }
-
-size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a) {
-    return static_cast<size_t>(a.batch) * a.dim * sizeof(double);
+// Without regard to the strides, which are not known when the scratch is asked for:
+// that of the shortest tiles a chain may take.
+size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a) {
+    constexpr int shortest = FwdChain<kIoF32, 1>::TILE;
+    static_assert(shortest <= FwdChain<kIoBF16, GS_FCV>::TILE, "shortest tiles of a chain");
+    return a.seqlen > shortest ? chain_bytes(Chain(nullptr, a.batch, a.seqlen, groups_of(a), shortest)) : 0;
 }
 
-hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, void*, hipStream_t s) {
-    if (a.io == kIoF32) return launch_fwd<kIoF32, 1, 16, 8>(a, s);
-    return divides(a, 2) ? launch_fwd<kIoBF16, 2, 16, 4>(a, s) : launch_fwd<kIoBF16, 1, 16, 8>(a, s);
+size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a) {
+    if (!chained(a, true)) return static_cast<size_t>(a.batch) * a.dim * sizeof(double);
+    const Chain ch = chain_of(a, nullptr, true);
+    return chain_bytes(ch) + static_cast<size_t>(a.batch) * ch.tiles * a.dim * sizeof(float);
+}
+
+hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
+    if (a.io == kIoF32)
+        return a.input_gate != nullptr ? launch_fwd<kIoF32, true>(a, ws, s) : launch_fwd<kIoF32, false>(a, ws, s);
+    return a.input_gate != nullptr ? launch_fwd<kIoBF16, true>(a, ws, s) : launch_fwd<kIoBF16, false>(a, ws, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
@@ -642,14 +1223,9 @@ hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, void* ws, hipStream_t s
                            state, a.dim, a.dhL, a.dh0, a.dlog_decay);
         return hipGetLastError();
     }
-    double* partial = a.dlog_decay != nullptr ? static_cast<double*>(ws) : nullptr;
-    const hipError_t e = a.io == kIoF32 ? launch_bwd<kIoF32, 1, 8, 8>(a, partial, s)
-                         : divides(a, 2) ? launch_bwd<kIoBF16, 2, 8, 4>(a, partial, s)
-                                         : launch_bwd<kIoBF16, 1, 8, 8>(a, partial, s);
-    if (e != hipSuccess || partial == nullptr) return e;
-    hipLaunchKernelGGL(gated_scan_sum_kernel, dim3(static_cast<unsigned>((a.dim + 255) / 256)), dim3(256), 0, s,
-                       a.batch, a.dim, partial, a.dlog_decay);
-    return hipGetLastError();
+    if (a.io == kIoF32)
+        return a.input_gate != nullptr ? launch_bwd<kIoF32, true>(a, ws, s) : launch_bwd<kIoF32, false>(a, ws, s);
+    return a.input_gate != nullptr ? launch_bwd<kIoBF16, true>(a, ws, s) : launch_bwd<kIoBF16, false>(a, ws, s);
 }
 
 hipError_t launch_gated_scan_update(const GatedScanArgs& a, hipStream_t s) {
