@@ -87,7 +87,10 @@ int scan_workspace(int64_t batch, int64_t seqlen, int64_t dim, int dtype, bool b
     *bytes = 0;
     if (batch == 0 || seqlen == 0 || dim == 0) return MAMBA_OK;
     const mamba::GatedScanArgs a = scan_args(batch, seqlen, dim, dtype);
-    *bytes = bwd ? mamba::gated_scan_bwd_workspace_bytes(a) : mamba::gated_scan_fwd_workspace_bytes(a);
+    int cu = 0;
+    const int got = mamba::current_cu_count(&cu);
+    if (got != MAMBA_OK) return got;
+    *bytes = bwd ? mamba::gated_scan_bwd_workspace_bytes(a, cu) : mamba::gated_scan_fwd_workspace_bytes(a, cu);
     return MAMBA_OK;
 }
 
@@ -150,7 +153,10 @@ int gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
     st = check_aligned(ptrs);
     if (st != MAMBA_OK) return st;
     if (seqlen == 0 && hL == nullptr) return MAMBA_OK;
-    const size_t need = seqlen > 0 ? mamba::gated_scan_fwd_workspace_bytes(a) : 0;
+    int cu = 0;
+    st = mamba::current_cu_count(&cu);
+    if (st != MAMBA_OK) return st;
+    const size_t need = seqlen > 0 ? mamba::gated_scan_fwd_workspace_bytes(a, cu) : 0;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
     set_inputs(&a, x, x_stride, decay_gate, decay_stride, log_decay, input_gate, input_stride);
     a.lengths = lengths;
@@ -158,7 +164,7 @@ int gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
     a.y = y;
     a.hL = hL;
     a.states = block_states;
-    return mamba::launch_gated_scan_fwd(a, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+    return mamba::launch_gated_scan_fwd(a, cu, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
 int gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x,
@@ -184,8 +190,11 @@ int gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
                                 dhL, dx,          ddecay_gate, dinput_gate, dlog_decay, dh0,      workspace};
     st = check_aligned(ptrs);
     if (st != MAMBA_OK) return st;
+    int cu = 1;
     if (tokens) {
-        const size_t need = mamba::gated_scan_bwd_workspace_bytes(a);
+        st = mamba::current_cu_count(&cu);
+        if (st != MAMBA_OK) return st;
+        const size_t need = mamba::gated_scan_bwd_workspace_bytes(a, cu);
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
     } else if (dlog_decay == nullptr && dh0 == nullptr) {
         return MAMBA_OK;
@@ -200,7 +209,7 @@ int gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
     a.dinput = dinput_gate;
     a.dlog_decay = dlog_decay;
     a.dh0 = dh0;
-    return mamba::launch_gated_scan_bwd(a, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+    return mamba::launch_gated_scan_bwd(a, cu, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
 int gated_scan_update(int64_t batch, int64_t dim, int dtype, float* h, const void* x,

@@ -6,6 +6,7 @@
 //     dg = A a (h_{t-1} - q x a / b)
 //     d(decay gate) = dg g (1 - p)       d(log_decay) = sum of dg p
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -78,22 +79,24 @@ __device__ __forceinline__ uint32_t fresh(uint32_t at) {
     return at;
 }
 
-#ifndef GS_FENCE
-#define GS_FENCE 2
-#endif
 // Keeps the arithmetic of a few tokens together, lest all of a segment's
 // intermediate values be alive at once.
 __device__ __forceinline__ void token_fence(int t) {
-    if (t % GS_FENCE == GS_FENCE - 1) __builtin_amdgcn_sched_barrier(0);
+    if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int IO>
 constexpr int size_of() { return IO == kIoF32 ? 4 : 2; }
 
 // V neighbouring channels of one token, in one access of at most 4 bytes: fp32 one,
-// bf16 one or two.
+// bf16 one or two. A single bf16 value is kept as 16 bits until use, where a shift
+// takes it: as 32 the compiler would clear the upper half of each loaded value, and
+// wait for it, long before.
 template <int IO, int V>
-__device__ __forceinline__ uint32_t load_value(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t row) {
+using Token = std::conditional_t<size_of<IO>() * V == 4, uint32_t, uint16_t>;
+
+template <int IO, int V>
+__device__ __forceinline__ Token<IO, V> load_value(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t row) {
     static_assert(size_of<IO>() * V <= 4, "a token is one access");
     if constexpr (size_of<IO>() * V == 4)
         return __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(at), static_cast<int>(row), 0);
@@ -101,8 +104,8 @@ __device__ __forceinline__ uint32_t load_value(__amdgpu_buffer_rsrc_t rs, uint32
         return __builtin_amdgcn_raw_buffer_load_b16(rs, static_cast<int>(at), static_cast<int>(row), 0);
 }
 
-template <int IO>
-__device__ __forceinline__ float value(uint32_t w, int v) {
+template <int IO, typename W>
+__device__ __forceinline__ float value(W w, int v) {
     return v == 0 ? raw_to_f32<IO>(w) : __uint_as_float(w & 0xffff0000u);
 }
 
@@ -180,7 +183,7 @@ struct Rows {
             row = 0;
         }
     }
-    __device__ __forceinline__ uint32_t load() const { return load_value<IO, V>(rs, at, row); }
+    __device__ __forceinline__ Token<IO, V> load() const { return load_value<IO, V>(rs, at, row); }
     __device__ __forceinline__ void store(const float (&v)[V]) const { store_value<IO, V>(rs, at, row, v); }
     __device__ __forceinline__ void go(int tokens) {
         if (FULL) row += tokens * step;
@@ -271,13 +274,7 @@ __device__ __forceinline__ Word look(const Word* at) {
     return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ Word await(const Word* at, Word w) {
-#ifdef GS_SPIN
-    int limit = GS_SPIN;
-#endif
     while (static_cast<uint32_t>(w >> 32) == 0xffffffffu) {
-#ifdef GS_SPIN
-        if (--limit == 0) break;
-#endif
         __builtin_amdgcn_s_sleep(1);
         w = look(at);
     }
@@ -342,23 +339,34 @@ struct Link {
     }
 };
 
+// One channel of (rows, dim), or zero.
+__device__ __forceinline__ float load_state(const float* p, int64_t row, int64_t dim, int64_t col) {
+    return p != nullptr && col < dim ? p[row * dim + col] : 0.0f;
+}
+
 // The state that enters a tile, for the lane's channel col; the tile's own sum
-// (G, h) is published on the way. `start` enters the row (it is looked at in the
-// first stretch only), `out` leaves the tile.
-__device__ __forceinline__ float enter_tile(const Chain& ch, const Link& at, int64_t col, float G, float h,
-                                            float start, float& out) {
+// (G, h) is published on the way. `start` enters the row; the first tile alone reads
+// it and publishes it as what enters the first stretch, since the last tile may write
+// its result to the same memory. `out` leaves the tile.
+__device__ __forceinline__ float enter_tile(const Chain& ch, const Link& at, int64_t dim, int64_t col, float G,
+                                            float h, const float* start, float& out) {
     const int kt = at.j % kRun, kr = at.j % kStretch / kRun;
     Word* tile = ch.tile + (static_cast<int64_t>(at.b) * ch.tiles + at.j) * ch.width + col;
     Word* run = ch.run + (static_cast<int64_t>(at.b) * ch.runs + at.j / kRun) * ch.width + col;
     Word* stretch = ch.stretch + (static_cast<int64_t>(at.b) * ch.stretches + at.j / kStretch) * ch.width + col;
     publish(tile, word_of(G, h));
-    Word wt[kRun - 1], wr[kRun - 1], ws = word_of(0.0f, start);
+    Word wt[kRun - 1], wr[kRun - 1], ws;
     const Word none = word_of(0.0f, 0.0f);
 #pragma unroll
     for (int u = 0; u < kRun - 1; ++u) wt[u] = u < kt ? look(tile - (kt - u) * ch.width) : none;
 #pragma unroll
     for (int u = 0; u < kRun - 1; ++u) wr[u] = u < kr ? look(run - (kr - u) * ch.width) : none;
-    if (at.j >= kStretch) ws = look(stretch);
+    if (at.j > 0) {
+        ws = look(stretch);
+    } else {
+        ws = word_of(0.0f, load_state(start, at.b, dim, col));
+        if (ch.tiles > 1) publish(stretch, ws);
+    }
     float Gt = 0.0f, ht = 0.0f;
 #pragma unroll
     for (int u = 0; u < kRun - 1; ++u)
@@ -392,7 +400,7 @@ struct FwdTile {
     static_assert(TILE % kGatedBlock == 0 && kGatedBlock % T == 0, "blocks of states at segments");
     typedef Rows<IO, V, T, W, false> R;
     typedef Place<V> P;
-    uint32_t x[T], d[T], i[T];
+    Token<IO, V> x[T], d[T], i[T];
     float ca[T][V], cu[T][V];
     float P0[V], h0[V];   // what precedes the lane's segment in its wave
 
@@ -517,11 +525,6 @@ __device__ __forceinline__ void log2_decay(const uint32_t (&w)[V], float (&lam2)
     for (int v = 0; v < V; ++v) lam2[v] = __uint_as_float(w[v]) * kLog2e;
 }
 
-// One channel of (rows, dim), or zero.
-__device__ __forceinline__ float load_state(const float* p, int64_t row, int64_t dim, int64_t col) {
-    return p != nullptr && col < dim ? p[row * dim + col] : 0.0f;
-}
-
 // A tile's whole sum for one of the workgroup's channels.
 template <int W>
 __device__ __forceinline__ float2 tile_sum(const float2 (&sums)[W][kGsChannels], int cl) {
@@ -531,16 +534,10 @@ __device__ __forceinline__ float2 tile_sum(const float2 (&sums)[W][kGsChannels],
     return make_float2(G, h);
 }
 
-#ifndef GS_CF
-#define GS_CF 0
-#endif
-#ifndef GS_FWD_WAVES
-#define GS_FWD_WAVES 1
-#endif
 // The forward pass, a workgroup walking one row's tiles. The waves take turns in
 // carrying the state over a tile, a lane for each channel.
 template <int IO, int V, int T, int W, bool GATED>
-__global__ __launch_bounds__(W* kWave, GS_FWD_WAVES) void gated_scan_fwd_kernel(GatedScanArgs a, int64_t groups) {
+__global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs a, int64_t groups) {
     typedef FwdTile<IO, V, T, W, GATED> Tile;
     typedef typename Tile::In In;
     __shared__ float2 sums[2][W][kGsChannels];   // by turns, so that one barrier a tile is enough
@@ -575,7 +572,7 @@ __global__ __launch_bounds__(W* kWave, GS_FWD_WAVES) void gated_scan_fwd_kernel(
 // The forward pass as a chain. A workgroup takes tickets until none is left, one
 // ahead of the tile whose inputs are being loaded.
 template <int IO, int V, int T, int W, bool GATED>
-__global__ __launch_bounds__(W* kWave, GS_FWD_WAVES) void gated_scan_fwd_chain_kernel(GatedScanArgs a, Chain ch) {
+__global__ __launch_bounds__(W* kWave) void gated_scan_fwd_chain_kernel(GatedScanArgs a, Chain ch) {
     typedef FwdTile<IO, V, T, W, GATED> Tile;
     typedef typename Tile::In In;
     __shared__ float2 sums[2][W][kGsChannels];   // by turns: read behind a tile's second barrier
@@ -615,7 +612,7 @@ __global__ __launch_bounds__(W* kWave, GS_FWD_WAVES) void gated_scan_fwd_chain_k
             if (looks) {
                 const float2 all = tile_sum<W>(sums[k & 1], place.lane);
                 float out;
-                enter[place.lane] = enter_tile(ch, at, col, all.x, all.y, load_state(a.h0, b, a.dim, col), out);
+                enter[place.lane] = enter_tile(ch, at, a.dim, col, all.x, all.y, a.h0, out);
                 if (a.hL != nullptr && left <= Tile::TILE && col < a.dim) a.hL[b * a.dim + col] = out;
             }
             if (threadIdx.x == 0) taken[0] = mine;
@@ -643,7 +640,7 @@ template <int IO, int T, int W, bool GATED>
 struct BwdTile {
     static constexpr int TILE = T * W;
     static_assert(TILE % kGatedBlock == 0, "tiles start at kept states");
-    uint32_t x[T], d[T], i[T], dy[T];
+    Token<IO, 1> x[T], d[T], i[T], dy[T];
     float state;   // entering the tile
     float ca[T], cw[T], cu[T], cp[T], cgr[T], cir[T], ck[T];
 
@@ -796,14 +793,11 @@ struct BwdTile {
     }
 };
 
-#ifndef GS_BWD_WAVES
-#define GS_BWD_WAVES 1
-#endif
 // The backward pass, a workgroup walking one row's tiles from the last to the
 // first. The state entering a tile comes from the forward pass.
 template <int IO, int T, int W, bool GATED>
-__global__ __launch_bounds__(W* kWave, GS_BWD_WAVES) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
-                                                                               double* partial) {
+__global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
+                                                               double* partial) {
     typedef BwdTile<IO, T, W, GATED> Tile;
     __shared__ float2 sums[2][W][kGsChannels], backs[2][W][kGsChannels];
     __shared__ float enter[2][kGsChannels];
@@ -858,8 +852,8 @@ __global__ __launch_bounds__(W* kWave, GS_BWD_WAVES) void gated_scan_bwd_kernel(
 // last one with tokens. `partial` holds the decay's gradient of every (row, tile),
 // zeros for tiles without tokens.
 template <int IO, int T, int W, bool GATED>
-__global__ __launch_bounds__(W* kWave, GS_BWD_WAVES) void gated_scan_bwd_chain_kernel(GatedScanArgs a, Chain ch,
-                                                                                     float* partial) {
+__global__ __launch_bounds__(W* kWave) void gated_scan_bwd_chain_kernel(GatedScanArgs a, Chain ch,
+                                                                     float* partial) {
     typedef BwdTile<IO, T, W, GATED> Tile;
     typedef typename Tile::template In<false> AnyIn;
     __shared__ float2 sums[2][W][kGsChannels], backs[2][W][kGsChannels];   // by turns, as forward
@@ -905,31 +899,24 @@ __global__ __launch_bounds__(W* kWave, GS_BWD_WAVES) void gated_scan_bwd_chain_k
         uint32_t mine = kNoTicket;
         if (threadIdx.x == 0 && !ch.once) mine = take_ticket(ch.ticket);
         float* share = partial == nullptr || !place.in ? nullptr : partial + (b * ch.tiles + at.j) * a.dim + place.ch;
-        auto step = [&](auto full) {
-            constexpr bool FULL = decltype(full)::value;
-            typename Tile::template In<FULL> in(a, next_place, next.b, next_t0, next_left);
+        if (left > 0) {
+            AnyIn in(a, next_place, next.b, next_t0, next_left);
             float lam2[1];
             log2_decay(decays, lam2);
-            tile.template work<FULL>(place, lam2[0], left, in, sums[k & 1], backs[k & 1]);
+            tile.template work<false>(place, lam2[0], left, in, sums[k & 1], backs[k & 1]);
             __syncthreads();
-            put_share(place, k + 1);   // a wave that has not the chain's next word to find
+            put_share(place, k + 1);   // a wave that has not to look for what enters the tile
             if (place.wave == k % W) {
                 const float2 all = tile_sum<W>(backs[k & 1], place.lane);
                 float out;
-                enter[place.lane] =
-                    enter_tile(ch, at, place.ch, all.x, all.y, load_state(a.dhL, b, a.dim, place.ch), out);
+                enter[place.lane] = enter_tile(ch, at, a.dim, place.ch, all.x, all.y, a.dhL, out);
                 if (a.dh0 != nullptr && t0 == 0 && place.in) a.dh0[b * a.dim + place.ch] = out;
             }
             if (threadIdx.x == 0) taken[0] = mine;
             __syncthreads();
             shares[place.wave][place.lane] =
-                tile.template finish<FULL>(a, place, b, t0, left, in, sums[k & 1], backs[k & 1], enter);
+                tile.template finish<false>(a, place, b, t0, left, in, sums[k & 1], backs[k & 1], enter);
             due = share;
-        };
-        if (GS_CF && left >= Tile::TILE && next_left >= Tile::TILE) {
-            step(std::true_type());
-        } else if (left > 0) {
-            step(std::false_type());
         } else {
             tile.load_all(AnyIn(a, next_place, next.b, next_t0, next_left));
             Tile::none(a, place, b, static_cast<int64_t>(at.j) * Tile::TILE, 0);
@@ -1056,59 +1043,63 @@ bool divides(const GatedScanArgs& a, int64_t v) {
            (a.input_gate == nullptr || a.input_stride % v == 0);
 }
 
-#ifndef GS_GRID
-#define GS_GRID 256
-#endif
-#ifndef GS_BGRID
-#define GS_BGRID 256
-#endif
-#ifndef GS_ONCE
-#define GS_ONCE 1024
-#endif
-#ifndef GS_FT
-#define GS_FT 16
-#define GS_FW 8
-#endif
-#ifndef GS_FCV
-#define GS_FCV 2
-#define GS_FCT 16
-#define GS_FCW 8
-#endif
-#ifndef GS_BT
-#define GS_BT 8
-#define GS_BW 8
-#endif
-#ifndef GS_BCT
-#define GS_BCT 16
-#define GS_BCW 8
-#endif
-#ifndef GS_CHAIN
-#define GS_CHAIN 256
-#endif
 int64_t groups_of(const GatedScanArgs& a) { return (a.dim + kGsChannels - 1) / kGsChannels; }
 
-// The kernels' shapes: V channels to a lane, T tokens to a segment, W waves.
+// The kernels' shapes: V channels to a lane, T tokens to a segment, W waves. A
+// forward tile holds 2 values a token in registers, a backward tile 7, so segments
+// are of 16 and 8 tokens where a workgroup walks a row: 8 x 2048 x 4096 in bf16 118
+// us, of 8 (4 waves of 16) 126 (128); gradients 234, of 16 the same, 8 x 2048 x 5120
+// 308 against 328. A chain's tile has a fixed cost, the look for what enters it, and
+// waits are shorter the fewer tiles of a column are on their way, so its tiles are
+// longer: 256 tokens where two channels fit a lane (1 x 262144 x 2048 1022 us; of
+// 128 tokens by 128 channels 1230, by 64 channels 1490), 128 for the gradients (1 x
+// 65536 x 1536 448 us, of 64 553 to 640).
 template <int IO_, int V_, int T_, int W_>
 struct Shape {
     static constexpr int IO = IO_, V = V_, T = T_, W = W_, TILE = W * V * T;
 };
 
-template <int IO> using FwdWalk = Shape<IO, 1, GS_FT, GS_FW>;
-template <int IO, int V> using FwdChain = Shape<IO, V, V == 1 ? 16 : GS_FCT, V == 1 ? 8 : GS_FCW>;
-template <int IO> using BwdWalk = Shape<IO, 1, GS_BT, GS_BW>;
-template <int IO> using BwdChain = Shape<IO, 1, GS_BCT, GS_BCW>;
+template <int IO> using FwdWalk = Shape<IO, 1, 16, 8>;
+template <int IO, int V> using FwdChain = Shape<IO, V, 16, 8>;
+template <int IO> using BwdWalk = Shape<IO, 1, 8, 8>;
+template <int IO> using BwdChain = Shape<IO, 1, 16, 8>;
 
 // Channels to a lane of the forward chain.
-int fwd_chain_channels(const GatedScanArgs& a) { return a.io == kIoBF16 && divides(a, GS_FCV) ? GS_FCV : 1; }
+int fwd_chain_channels(const GatedScanArgs& a) { return a.io == kIoBF16 && divides(a, 2) ? 2 : 1; }
+
+constexpr int kFwdShortest = FwdChain<kIoF32, 1>::TILE;   // tokens of the shortest tile of a forward chain
 
 int chain_tile(const GatedScanArgs& a, bool bwd) {
-    if (bwd) return BwdChain<kIoF32>::TILE;
-    return fwd_chain_channels(a) == 1 ? FwdChain<kIoF32, 1>::TILE : FwdChain<kIoBF16, GS_FCV>::TILE;
+    return bwd ? BwdChain<kIoF32>::TILE : fwd_chain_channels(a) * kFwdShortest;
 }
 
-// Whether a call runs as a chain.
-bool chained(const GatedScanArgs& a, bool bwd) {
-    return a.seqlen > chain_tile(a, bwd) && a.batch * groups_of(a) < GS_CHAIN;
+// Whether a call runs as a chain: by the times that either takes on MI355X, in
+// microseconds. A walk's grows with the length of the sequences and, in bf16, where
+// it is bound by issue, with the rounds of one column (a row's 64 channels) to a
+// compute unit; in fp32, where it is bound by memory, with the columns. A chain's
+// grows with the tokens of all columns, from what clearing its words costs. Of
+// 2048 tokens in bf16, walk against chain: 32 columns 50 us against 17, 192 54
+// against 58, 256 61 against 72, 384 107 against 101, 512 117 against 128, 640 165
+// against 156; gradients 104 against 31, 116 against 114, 120 against 149, 198 against
+// 215, 234 against 276, 308 against 344. In fp32 32 columns 47 against 22, 128 74
+// against 60, 256 116 against 115, 512 217 against 202; gradients 99 against 36, 143
+// against 112, 211 against 200, 412 against 357. Sequences of fewer than 4 tiles of
+// 128 are walked (512 tokens of 192 columns: 16 us against 25).
+bool chained(const GatedScanArgs& a, bool bwd, int cu) {
+    const double columns = static_cast<double>(a.batch * groups_of(a)), len = static_cast<double>(a.seqlen);
+    if (a.seqlen < 512 || columns * (len / kFwdShortest + 1.0) >= 2147483648.0) return false;
+    const double each = columns * 256.0 / cu;   // as of 256 compute units
+    const double rounds = ceil(columns / cu);
+    double walk, chain;
+    if (a.io == kIoBF16) {
+        walk = bwd ? 8.0 + len * 0.048 * rounds : 2.0 + len * 0.0255 * rounds;
+        chain = 14.0 + len * each * (bwd ? 2.5e-4 : 1.1e-4);
+    } else {
+        walk = bwd ? 8.0 + len * fmax(0.04 + 1.9e-4 * each, 3.9e-4 * each)
+                   : 3.0 + len * fmax(0.021 + 1.1e-4 * each, 2.1e-4 * each);
+        chain = 14.0 + len * each * (bwd ? 3.3e-4 : 1.8e-4);
+    }
+    return chain < walk;
 }
 
 Chain chain_of(const GatedScanArgs& a, void* ws, bool bwd) {
@@ -1117,21 +1108,22 @@ Chain chain_of(const GatedScanArgs& a, void* ws, bool bwd) {
 
 size_t chain_bytes(const Chain& ch) { return 256 + static_cast<size_t>(ch.words()) * sizeof(Word); }
 
-// Clears the chain's words; sets its grid.
-hipError_t begin_chain(Chain& ch, unsigned resident, unsigned* grid, hipStream_t s) {
+// Clears the chain's words; sets its grid: a workgroup for every tile up to two
+// rounds of them (of 8 waves, one to a compute unit), else one for each unit.
+hipError_t begin_chain(Chain& ch, int cu, unsigned* grid, hipStream_t s) {
     const int64_t pairs = ch.words() / 2, total = static_cast<int64_t>(ch.columns) * ch.tiles;
-    ch.once = total <= GS_ONCE;
-    *grid = ch.once ? static_cast<unsigned>(total) : resident;
+    ch.once = total <= 2 * static_cast<int64_t>(cu);
+    *grid = static_cast<unsigned>(ch.once ? total : cu);
     hipLaunchKernelGGL(gated_scan_clear_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, s,
                        ch.ticket, ch.tile, pairs);
     return hipGetLastError();
 }
 
 template <typename S, bool GATED>
-hipError_t launch_fwd_chain(const GatedScanArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_fwd_chain(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     Chain ch = chain_of(a, ws, false);
     unsigned grid = 0;
-    const hipError_t e = begin_chain(ch, GS_GRID, &grid, s);
+    const hipError_t e = begin_chain(ch, cu, &grid, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<S::IO, S::V, S::T, S::W, GATED>), dim3(grid), dim3(S::W * kWave),
                        0, s, a, ch);
@@ -1139,11 +1131,11 @@ hipError_t launch_fwd_chain(const GatedScanArgs& a, void* ws, hipStream_t s) {
 }
 
 template <int IO, bool GATED>
-hipError_t launch_fwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
-    if (chained(a, false)) {
+hipError_t launch_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
+    if (chained(a, false, cu)) {
         if constexpr (IO == kIoBF16)
-            if (fwd_chain_channels(a) > 1) return launch_fwd_chain<FwdChain<IO, GS_FCV>, GATED>(a, ws, s);
-        return launch_fwd_chain<FwdChain<IO, 1>, GATED>(a, ws, s);
+            if (fwd_chain_channels(a) == 2) return launch_fwd_chain<FwdChain<IO, 2>, GATED>(a, cu, ws, s);
+        return launch_fwd_chain<FwdChain<IO, 1>, GATED>(a, cu, ws, s);
     }
     typedef FwdWalk<IO> S;
     const int64_t groups = groups_of(a);
@@ -1160,16 +1152,16 @@ hipError_t launch_sum(int64_t slots, int64_t dim, const F* partial, float* out, 
 }
 
 template <int IO, bool GATED>
-hipError_t launch_bwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     hipError_t e;
-    if (chained(a, true)) {
+    if (chained(a, true, cu)) {
         typedef BwdChain<IO> S;
         Chain ch = chain_of(a, ws, true);
         unsigned grid = 0;
         float* partial = a.dlog_decay == nullptr
                              ? nullptr
                              : reinterpret_cast<float*>(static_cast<char*>(ws) + chain_bytes(ch));
-        e = begin_chain(ch, GS_BGRID, &grid, s);
+        e = begin_chain(ch, cu, &grid, s);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<S::IO, S::T, S::W, GATED>), dim3(grid), dim3(S::W * kWave), 0,
                            s, a, ch, partial);
@@ -1197,25 +1189,23 @@ hipError_t launch_update(const GatedScanArgs& a, hipStream_t s) {
 
 // Without regard to the strides, which are not known when the scratch is asked for:
 // that of the shortest tiles a chain may take.
-size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a) {
-    constexpr int shortest = FwdChain<kIoF32, 1>::TILE;
-    static_assert(shortest <= FwdChain<kIoBF16, GS_FCV>::TILE, "shortest tiles of a chain");
-    return a.seqlen > shortest ? chain_bytes(Chain(nullptr, a.batch, a.seqlen, groups_of(a), shortest)) : 0;
+size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu) {
+    return chained(a, false, cu) ? chain_bytes(Chain(nullptr, a.batch, a.seqlen, groups_of(a), kFwdShortest)) : 0;
 }
 
-size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a) {
-    if (!chained(a, true)) return static_cast<size_t>(a.batch) * a.dim * sizeof(double);
+size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu) {
+    if (!chained(a, true, cu)) return static_cast<size_t>(a.batch) * a.dim * sizeof(double);
     const Chain ch = chain_of(a, nullptr, true);
     return chain_bytes(ch) + static_cast<size_t>(a.batch) * ch.tiles * a.dim * sizeof(float);
 }
 
-hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     if (a.io == kIoF32)
-        return a.input_gate != nullptr ? launch_fwd<kIoF32, true>(a, ws, s) : launch_fwd<kIoF32, false>(a, ws, s);
-    return a.input_gate != nullptr ? launch_fwd<kIoBF16, true>(a, ws, s) : launch_fwd<kIoBF16, false>(a, ws, s);
+        return a.input_gate != nullptr ? launch_fwd<kIoF32, true>(a, cu, ws, s) : launch_fwd<kIoF32, false>(a, cu, ws, s);
+    return a.input_gate != nullptr ? launch_fwd<kIoBF16, true>(a, cu, ws, s) : launch_fwd<kIoBF16, false>(a, cu, ws, s);
 }
 
-hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, void* ws, hipStream_t s) {
+hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     if (a.batch == 0 || a.seqlen == 0) {
         const int64_t state = a.batch * a.dim;
         hipLaunchKernelGGL(gated_scan_empty_kernel,
@@ -1224,8 +1214,8 @@ hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, void* ws, hipStream_t s
         return hipGetLastError();
     }
     if (a.io == kIoF32)
-        return a.input_gate != nullptr ? launch_bwd<kIoF32, true>(a, ws, s) : launch_bwd<kIoF32, false>(a, ws, s);
-    return a.input_gate != nullptr ? launch_bwd<kIoBF16, true>(a, ws, s) : launch_bwd<kIoBF16, false>(a, ws, s);
+        return a.input_gate != nullptr ? launch_bwd<kIoF32, true>(a, cu, ws, s) : launch_bwd<kIoF32, false>(a, cu, ws, s);
+    return a.input_gate != nullptr ? launch_bwd<kIoBF16, true>(a, cu, ws, s) : launch_bwd<kIoBF16, false>(a, cu, ws, s);
 }
 
 hipError_t launch_gated_scan_update(const GatedScanArgs& a, hipStream_t s) {

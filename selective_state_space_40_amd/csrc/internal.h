@@ -306,10 +306,10 @@ struct GatedScanArgs {
     float* h;            // the single token's state
 };
 
-size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a);
-size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a);
-hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, void* ws, hipStream_t s);
-hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, void* ws, hipStream_t s);
+size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu);
+size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu);
+hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s);
+hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s);
 hipError_t launch_gated_scan_update(const GatedScanArgs& a, hipStream_t s);
 
 // The norms around a block: gated (over parts of a row) and residual.

@@ -1,0 +1,279 @@
+"""The gated recurrence on the GPU over sequences whose tiles go to workgroups one
+by one, each learning from the others what enters it, against 64 bits (gated_ref.py):
+lengths around a tile (128 or 256 tokens), 8 of them and 64 of them; the same rows
+among many others, where a workgroup walks each; and what may go wrong between
+calls: captured ones, two at once, scratch with anything in it, aliased states."""
+import ctypes
+import sys
+
+import pytest
+import torch
+
+import gated_ref as ref
+import selective_state_space_40_amd as ms
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ms.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def _say(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+def _make(b, n, d, dtype, seed, gated=True, lengths=None):
+    g = torch.Generator(DEV).manual_seed(seed)
+    r = lambda *s, dt=dtype: torch.randn(*s, generator=g, device=DEV).to(dt)   # noqa: E731
+    lam = -torch.pow(10.0, 1.0 - 5.0 * torch.rand(d, generator=g, device=DEV))
+    return dict(x=r(b, n, d), decay_gate=r(b, n, d), log_decay=lam, input_gate=r(b, n, d) if gated else None,
+                h0=r(b, d, dt=F32), lengths=None if lengths is None else
+                torch.tensor(lengths, dtype=torch.int32, device=DEV), dy=r(b, n, d), dhL=r(b, d, dt=F32))
+
+
+def _forward(c, **kw):
+    y, hL, states = ms.gated_scan_fwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], c["h0"],
+                                      lengths=c["lengths"], return_block_states=True, **kw)
+    return dict(y=y, hL=hL, block_states=states)
+
+
+def _backward(c, states):
+    return ms.gated_scan_bwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], block_states=states,
+                             dy=c["dy"], dhL=c["dhL"], lengths=c["lengths"])
+
+
+def _live(c, states):
+    """The states of blocks with tokens; zeros for others, which are not written."""
+    if c["lengths"] is None:
+        return states
+    first = 64 * torch.arange(states.shape[1], device=states.device)
+    return torch.where((first < c["lengths"].to(states.device)[:, None])[..., None], states, 0.0)
+
+
+def _check(c, what, got=None, grads=None):
+    _say(f"case {what}")
+    got = got or _forward(c)
+    grads = grads or _backward(c, got["block_states"])
+    torch.cuda.synchronize()
+    want = ref.scan(**c)
+    for k in ("block_states", "block_states_size"):
+        want[k] = _live(c, want[k])
+    got["block_states"] = _live(c, got["block_states"])
+    ref.check_scan(got, want, what)
+    ref.check_scan(grads, want, what)
+    return got, grads
+
+
+@TYPES
+@pytest.mark.parametrize("n", [511, 512, 513, 640, 1023, 1024, 1025, 1153, 2049, 4100])
+def test_lengths(n, dtype):
+    for d in (70, 65):   # two channels to a lane in bf16, and one
+        _check(_make(1, n, d, dtype, n), f"1 x {n} x {d} {dtype}")
+
+
+@TYPES
+@pytest.mark.parametrize("n", [8191, 8193, 16385, 40000])
+def test_many_tiles(n, dtype):
+    # past 64 tiles of 128 tokens, and of 256
+    for d in (2, 1):
+        _check(_make(1, n, d, dtype, n, gated=d == 2), f"1 x {n} x {d} {dtype}")
+
+
+@TYPES
+@pytest.mark.parametrize("gated", [True, False], ids=["gates", "gate"])
+def test_ragged_rows(gated, dtype):
+    n = 2500
+    c = _make(9, n, 66, dtype, 1, gated, lengths=[n, 0, 1, 128, 129, 256, 257, 1024, 2048])
+    got, grads = _check(c, f"ragged {dtype} {gated}")
+    for k in ("x", "decay_gate", "input_gate", "dy"):   # what stands behind a row is not read
+        if c[k] is not None:
+            c[k] = torch.where((torch.arange(n, device=DEV) < c["lengths"][:, None])[..., None], c[k], float("nan"))
+    again = _forward(c)
+    more = _backward(c, again["block_states"])
+    for k, t in {**got, **grads}.items():
+        if t is not None:
+            assert torch.equal(_live(c, again[k]) if k == "block_states" else {**again, **more}[k], t), k
+
+
+@TYPES
+def test_blocks_behind_a_row_are_left(dtype):
+    # through the C ABI, as the binding hands out memory of its own
+    b, n, d = 2, 1500, 64
+    c = _make(b, n, d, dtype, 2, lengths=[n, 600])
+    lib, code = ms.load_library(), 1 if dtype == BF else 0
+    size = ctypes.c_size_t()
+    assert lib.gated_scan_fwd_workspace_size(b, n, d, code, ctypes.byref(size)) == 0
+    ws = torch.empty(max(size.value, 16), dtype=torch.uint8, device=DEV)
+    y, states = torch.empty_like(c["x"]), torch.full((b, 24, d), 7.0, device=DEV)
+    assert lib.gated_scan_fwd(b, n, d, code, c["x"].data_ptr(), d, c["decay_gate"].data_ptr(), d,
+                              c["log_decay"].data_ptr(), c["input_gate"].data_ptr(), d, c["lengths"].data_ptr(),
+                              c["h0"].data_ptr(), y.data_ptr(), None, states.data_ptr(), ws.data_ptr(), size.value,
+                              torch.cuda.current_stream(DEV).cuda_stream) == 0
+    torch.cuda.synchronize()
+    got = _forward(c)
+    assert torch.equal(y, got["y"]) and torch.equal(_live(c, states), _live(c, got["block_states"]))
+    assert (states[1, 10:] == 7.0).all()
+
+
+@TYPES
+@pytest.mark.parametrize("d", [64, 66, 63])
+def test_rows_alone_and_among_many(d, dtype):
+    # one row's tiles go to workgroups one by one; those of 200 groups of 64 channels
+    # are walked, in the forward pass at least
+    n, rows = 600, 200 // ((d + 63) // 64)
+    c = _make(1, n, d, dtype, d)
+    alone, alone_g = _check(c, f"alone {d} {dtype}")
+    many = {k: (v if v is None or k == "log_decay" else v.expand(rows, *v.shape[1:]).contiguous()) for k, v in c.items()}
+    got = _forward(many)
+    grads = _backward(many, got["block_states"])
+    grads["dlog_decay"] = grads["dlog_decay"] / rows
+    for k in ("y", "hL", "block_states"):
+        assert torch.equal(got[k][0], got[k][rows - 1]), k
+    for k in ("dx", "ddecay_gate", "dinput_gate", "dh0"):
+        assert torch.equal(grads[k][0], grads[k][rows - 1]), k
+    want = ref.scan(**c)
+    ref.check_scan({k: v[rows // 2:rows // 2 + 1] for k, v in got.items()}, want, "walked")
+    ref.check_scan({k: v[rows // 2:rows // 2 + 1] if k != "dlog_decay" else v for k, v in grads.items()}, want, "walked")
+
+
+def test_odd_strides():
+    for dtype in (BF, F32):
+        n, d, wide = 1300, 66, 201   # an odd row stride: one channel to a lane
+        c = _make(1, n, d, dtype, 5)
+        base = torch.zeros(1, n, wide, dtype=dtype, device=DEV)
+        base[..., :d] = c["x"]
+        c["x"] = base[..., :d]
+        _check(c, f"odd stride {dtype}")
+
+
+def test_results_repeat_whatever_the_scratch_holds():
+    for dtype in (BF, F32):
+        c = _make(2, 9000, 130, dtype, 6, lengths=[9000, 7001])
+        got = _forward(c)
+        grads = _backward(c, got["block_states"])
+        for fill in (0, 0xff, 0x7f):
+            junk = torch.full((64 << 20,), fill, dtype=torch.uint8, device=DEV)
+            del junk   # the next scratch is cut from this memory
+            again = _forward(c)
+            more = _backward(c, again["block_states"])
+            assert torch.equal(again["y"], got["y"]) and torch.equal(again["hL"], got["hL"])
+            for k, t in grads.items():
+                assert torch.equal(more[k], t), k
+
+
+def test_states_in_place():
+    # the last tile writes where the first one reads
+    for dtype in (BF, F32):
+        c = _make(3, 5000, 128, dtype, 7, lengths=[5000, 0, 300])
+        want = _forward(c)
+        for _ in range(5):
+            state = c["h0"].clone()
+            y, hL, _ = ms.gated_scan_fwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], state,
+                                         lengths=c["lengths"], state_out=state)
+            assert hL is state and torch.equal(y, want["y"]) and torch.equal(hL, want["hL"])
+
+
+def test_captured_calls_replay():
+    # graphs own their scratch; replayed by turns, and with eager calls between
+    graphs = []
+    for dtype, n in ((BF, 5000), (F32, 3000)):
+        c = _make(1, n, 192, dtype, n, lengths=[n - 77])
+        f = _forward(c)
+        want = [f["y"].clone(), f["hL"].clone(), *(t.clone() for t in _backward(c, f["block_states"]).values())]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            f = _forward(c)
+            got = [f["y"], f["hL"], *_backward(c, f["block_states"]).values()]
+        graphs.append((graph, got, want, c))
+    for r in range(4):
+        for graph, got, want, c in graphs:
+            for t in got:
+                t.fill_(float("nan"))
+            eager = _forward(c)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(eager["y"], want[0])
+            for a, e in zip(got, want):
+                assert torch.equal(a, e), f"replay {r}"
+
+
+def test_two_calls_at_once():
+    # each fills the chip by itself: workgroups of both wait for others of their own
+    cs = [_make(1, 30000, 512, BF, 8), _make(2, 17000, 320, F32, 9)]
+    want = []
+    for c in cs:
+        f = _forward(c)
+        want.append({**f, **_backward(c, f["block_states"])})
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in cs]
+    for _ in range(3):
+        got = []
+        for c, s in zip(cs, streams):
+            s.wait_stream(torch.cuda.current_stream(DEV))
+            with torch.cuda.stream(s):
+                f = _forward(c)
+                got.append({**f, **_backward(c, f["block_states"])})
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for k in w:
+                assert torch.equal(g[k], w[k]), k
+
+
+def test_nan_stays_in_its_channel_and_ends_no_wait_early():
+    # a NaN of all ones is what a word holds before it is written
+    for dtype in (BF, F32):
+        c = _make(1, 3000, 70, dtype, 10)
+        clean = _forward(c)
+        grads = _backward(c, clean["block_states"])
+        bits = torch.full((1,), -1, dtype=torch.int16 if dtype == BF else torch.int32, device=DEV).view(dtype)
+        others = [i for i in range(70) if i not in (5, 69)]
+        for k in ("x", "decay_gate"):
+            bad = dict(c)
+            bad[k] = c[k].clone()
+            bad[k][0, 700, 5] = bits[0]
+            bad[k][0, 1400, 69] = float("inf") if k == "x" else float("nan")
+            got = _forward(bad)
+            assert torch.equal(got["y"][..., others], clean["y"][..., others])
+            assert torch.equal(got["y"][0, :700, 5], clean["y"][0, :700, 5]) and torch.isnan(got["y"][0, 700:, 5]).all()
+            g = _backward(bad, got["block_states"])
+            for name in ("dx", "ddecay_gate", "dinput_gate", "dh0"):
+                assert torch.equal(g[name][..., others], grads[name][..., others]), name
+        states = clean["block_states"].clone()
+        states[0, :, 5] = torch.full((1,), -1, dtype=torch.int32, device=DEV).view(F32)
+        bad = dict(c)
+        bad["dhL"] = c["dhL"].clone()
+        bad["dhL"][0, 5] = torch.full((1,), -1, dtype=torch.int32, device=DEV).view(F32)[0]
+        g = _backward(bad, states)
+        assert torch.isnan(g["dh0"][0, 5]) and torch.equal(g["dx"][..., others], grads["dx"][..., others])
+
+
+def test_no_and_infinite_memory():
+    # log_decay 0: a = 1, nothing enters; and decays that leave nothing after a token
+    for dtype in (BF, F32):
+        c = _make(1, 2000, 64, dtype, 11)
+        c["log_decay"] = torch.zeros(64, device=DEV)
+        c["log_decay"][32:] = -1e4
+        got, grads = _forward(c), None
+        assert torch.equal(got["hL"][:, :32], c["h0"][:, :32])
+        assert torch.equal(got["y"][..., :32], c["h0"][:, None, :32].to(dtype).expand(1, 2000, 32))
+        grads = _backward(c, got["block_states"])
+        for k, t in grads.items():
+            assert torch.isfinite(t).all(), k
+        assert not grads["dx"][..., :32].any() and not grads["ddecay_gate"][..., :32].any()
+        half = {k: (v if v is None or k == "lengths" else v[..., 32:].contiguous()) for k, v in c.items()}
+        want = ref.scan(**half)
+        # a sigmoid's error reaches log a as |log a| times it, where a > 0 is left: |G|
+        # e^-|G| of it at most, as in the bounds; p below 2^-126 does not come up
+        ref.check_scan({k: got[k][..., 32:] for k in ("y", "hL")}, want, "short memory")
