@@ -671,7 +671,7 @@ __global__ __launch_bounds__(kThreads<TEAM>) void residual_norm_bwd_kernel(Resid
 // of `partial` goes to out[y].
 constexpr int kColumns = 16, kColumnThreads = 1024;
 
-__global__ __launch_bounds__(kColumnThreads) void norm_columns_kernel(int64_t dim, int slots, const float* partial,
+__global__ __launch_bounds__(kColumnThreads) void column_sums_kernel(int64_t dim, int64_t slots, const float* partial,
                                                                       float* out0, float* out1) {
     constexpr int ROWS = kColumnThreads / kColumns, WAVES = kColumnThreads / kWave, U = 8;
     __shared__ double red[WAVES][kColumns];
@@ -679,15 +679,15 @@ __global__ __launch_bounds__(kColumnThreads) void norm_columns_kernel(int64_t di
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kColumns + c;
     float* out = blockIdx.y ? out1 : out0;
     if (out == nullptr) return;
-    const float* p = partial + static_cast<int64_t>(blockIdx.y) * slots * dim;
+    const float* p = partial + blockIdx.y * slots * dim;
     double s = 0.0;
     if (col < dim) {
-        for (int k0 = r; k0 < slots; k0 += U * ROWS) {
+        for (int64_t k0 = r; k0 < slots; k0 += U * ROWS) {
             float x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = k0 + u * ROWS;
-                x[u] = k < slots ? p[static_cast<int64_t>(k) * dim + col] : 0.0f;
+                const int64_t k = k0 + u * ROWS;
+                x[u] = k < slots ? p[k * dim + col] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) s += static_cast<double>(x[u]);
@@ -838,13 +838,6 @@ hipError_t launch_residual_any(const ResidualNormArgs& a, const Shape& sh, bool 
               : launch_residual<kIoBF16, kIoBF16, false>(a, sh, bwd, lay, partial, s);
 }
 
-hipError_t launch_columns(int64_t dim, int slots, const float* partial, float* out0, float* out1, hipStream_t s) {
-    hipLaunchKernelGGL(norm_columns_kernel,
-                       dim3(static_cast<unsigned>((dim + kColumns - 1) / kColumns), out1 != nullptr ? 2 : 1),
-                       dim3(kColumnThreads), 0, s, dim, slots, partial, out0, out1);
-    return hipGetLastError();
-}
-
 hipError_t launch_zero(int64_t dim, float* out0, float* out1, hipStream_t s) {
     hipLaunchKernelGGL(norm_zero_kernel, dim3(static_cast<unsigned>((dim + 255) / 256)), dim3(256), 0, s, dim, out0,
                        out1);
@@ -852,6 +845,13 @@ hipError_t launch_zero(int64_t dim, float* out0, float* out1, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_column_sums(int64_t dim, int64_t slots, const float* partial, float* out0, float* out1, hipStream_t s) {
+    hipLaunchKernelGGL(column_sums_kernel,
+                       dim3(static_cast<unsigned>((dim + kColumns - 1) / kColumns), out1 != nullptr ? 2 : 1),
+                       dim3(kColumnThreads), 0, s, dim, slots, partial, out0, out1);
+    return hipGetLastError();
+}
 
 hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, int cu, hipStream_t s) {
     const Shape sh = shape_for(a.dim / a.groups, false);
@@ -870,7 +870,7 @@ hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, int cu, void* ws, hipSt
     float* partial = static_cast<float*>(ws);
     const hipError_t e = launch_gated_any(a, sh, true, lay, partial, s);
     if (e != hipSuccess || lay.slots == 1 || a.dweight == nullptr) return e;
-    return launch_columns(a.dim, lay.slots, partial, a.dweight, nullptr, s);
+    return launch_column_sums(a.dim, lay.slots, partial, a.dweight, nullptr, s);
 }
 
 hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a, int cu, hipStream_t s) {
@@ -890,7 +890,7 @@ hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, int cu, void* ws,
     float* partial = static_cast<float*>(ws);
     const hipError_t e = launch_residual_any(a, sh, true, lay, partial, s);
     if (e != hipSuccess || lay.slots == 1 || (a.dweight == nullptr && a.dscale == nullptr)) return e;
-    return launch_columns(a.dim, lay.slots, partial, a.dweight, a.dscale, s);
+    return launch_column_sums(a.dim, lay.slots, partial, a.dweight, a.dscale, s);
 }
 
 }  // namespace mamba

@@ -403,6 +403,7 @@ struct FwdTile {
     Token<IO, V> x[T], d[T], i[T];
     float ca[T][V], cu[T][V];
     float P0[V], h0[V];   // what precedes the lane's segment in its wave
+    float Gw[V], hw[V];   // and the wave in its tile
 
     // Where the inputs of a tile are; `left` <= 0: nowhere.
     struct In {
@@ -470,16 +471,20 @@ struct FwdTile {
             if (at.sub == 0) sums[at.wave][at.cl + v] = make_float2(G[v], hl[v]);
         }
     }
-    // The outputs, from the states entering the tile.
-    __device__ __forceinline__ void finish(const GatedScanArgs& a, const P& at, int64_t b, int64_t t0, int64_t len,
-                                           const float2 (&sums)[W][kGsChannels], const float (&enter)[kGsChannels]) {
-        float h[V];
+    // What needs the other waves' sums, and not yet what enters the tile.
+    __device__ __forceinline__ void gather(const P& at, const float2 (&sums)[W][kGsChannels]) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float G = 0.0f, s = 0.0f;
-            for (int w = 0; w < at.wave; ++w) append(G, s, sums[w][at.cl + v].x, sums[w][at.cl + v].y);
-            h[v] = fmaf(P0[v], carried(enter[at.cl + v], G, s), h0[v]);
+            Gw[v] = hw[v] = 0.0f;
+            for (int w = 0; w < at.wave; ++w) append(Gw[v], hw[v], sums[w][at.cl + v].x, sums[w][at.cl + v].y);
         }
+    }
+    // The outputs, from the states entering the tile.
+    __device__ __forceinline__ void finish(const GatedScanArgs& a, const P& at, int64_t b, int64_t t0, int64_t len,
+                                           const float (&enter)[kGsChannels]) {
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(P0[v], carried(enter[at.cl + v], Gw[v], hw[v]), h0[v]);
         const int64_t tseg = t0 + at.segment() * T;
         if (a.states != nullptr && at.segment() * T % kGatedBlock == 0 && tseg < len && at.in) {
             const int64_t blocks = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
@@ -562,7 +567,8 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs 
             const float2 all = tile_sum<W>(sums[odd], at.lane);
             enter[odd ^ 1][at.lane] = carried(enter[odd][at.lane], all.x, all.y);
         }
-        tile.finish(a, at, b, t0, len, sums[odd], enter[odd]);
+        tile.gather(at, sums[odd]);
+        tile.finish(a, at, b, t0, len, enter[odd]);
     }
     __syncthreads();
     if (a.hL != nullptr && at.wave == 0 && col < a.dim) a.hL[b * a.dim + col] = enter[k & 1][at.lane];
@@ -616,8 +622,10 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_chain_kernel(GatedSca
                 if (a.hL != nullptr && left <= Tile::TILE && col < a.dim) a.hL[b * a.dim + col] = out;
             }
             if (threadIdx.x == 0) taken[0] = mine;
+            if (!looks) tile.gather(place, sums[k & 1]);   // while the other looks
             __syncthreads();
-            tile.finish(a, place, b, t0, len, sums[k & 1], enter);
+            if (looks) tile.gather(place, sums[k & 1]);
+            tile.finish(a, place, b, t0, len, enter);
         } else {
             tile.load_all(in_of(next, next_left));
             Tile::none(a, place, b, t0, 0);
@@ -642,6 +650,7 @@ struct BwdTile {
     static_assert(TILE % kGatedBlock == 0, "tiles start at kept states");
     Token<IO, 1> x[T], d[T], i[T], dy[T];
     float state;   // entering the tile
+    float Gw, hw;  // what the later waves of the tile add to the adjoint
     float ca[T], cw[T], cu[T], cp[T], cgr[T], cir[T], ck[T];
 
     template <bool FULL>
@@ -732,28 +741,30 @@ struct BwdTile {
         sums[at.wave][at.lane] = make_float2(G, hl);
         backs[W - 1 - at.wave][at.lane] = make_float2(G, El);   // in the order of the walk back
     }
-    // The gradients, from the adjoints entering the tile from behind. Returns the
-    // wave's share of the decay's gradient.
-    template <bool FULL>
-    __device__ __forceinline__ float finish(const GatedScanArgs& a, const Place<1>& at, int64_t b, int64_t t0,
-                                            int64_t left, In<FULL>& next, const float2 (&sums)[W][kGsChannels],
-                                            const float2 (&backs)[W][kGsChannels],
-                                            const float (&enter)[kGsChannels]) {
-        typedef Rows<IO, 1, T, W, FULL> R;
-        const int64_t first = b * a.seqlen + t0;
+    // What needs the other waves' sums, and not yet what enters the tile from behind.
+    __device__ __forceinline__ void gather(const Place<1>& at, const float2 (&sums)[W][kGsChannels],
+                                           const float2 (&backs)[W][kGsChannels]) {
         float G = 0.0f, s = 0.0f;
         for (int w = 0; w < at.wave; ++w) append(G, s, sums[w][at.lane].x, sums[w][at.lane].y);
         float h = carried(state, G, s);
-        G = s = 0.0f;
-        for (int w = 0; w < W - 1 - at.wave; ++w) append(G, s, backs[w][at.lane].x, backs[w][at.lane].y);
-        float A = carried(enter[at.lane], G, s), sum = 0.0f;
-        state = next.state != nullptr ? *next.state : 0.0f;
+        Gw = hw = 0.0f;
+        for (int w = 0; w < W - 1 - at.wave; ++w) append(Gw, hw, backs[w][at.lane].x, backs[w][at.lane].y);
         // ck becomes h_{t-1} - q x a / b
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             ck[t] = h - ck[t];
             h = fmaf(ca[t], h, cu[t]);
         }
+    }
+    // The gradients, from the adjoints entering the tile from behind. Returns the
+    // wave's share of the decay's gradient.
+    template <bool FULL>
+    __device__ __forceinline__ float finish(const GatedScanArgs& a, const Place<1>& at, int64_t b, int64_t t0,
+                                            int64_t left, In<FULL>& next, const float (&enter)[kGsChannels]) {
+        typedef Rows<IO, 1, T, W, FULL> R;
+        const int64_t first = b * a.seqlen + t0;
+        float A = carried(enter[at.lane], Gw, hw), sum = 0.0f;
+        state = next.state != nullptr ? *next.state : 0.0f;
         R ox(at, a.dx, first, a.dim, a.dim, a.seqlen - t0), od(at, a.ddecay, first, a.dim, a.dim, a.seqlen - t0),
             oi(at, a.dinput, first, a.dim, a.dim, a.seqlen - t0);
         ox.go(T - 1);
@@ -797,7 +808,7 @@ struct BwdTile {
 // first. The state entering a tile comes from the forward pass.
 template <int IO, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
-                                                               double* partial) {
+                                                               float* partial) {
     typedef BwdTile<IO, T, W, GATED> Tile;
     __shared__ float2 sums[2][W][kGsChannels], backs[2][W][kGsChannels];
     __shared__ float enter[2][kGsChannels];
@@ -824,8 +835,8 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs 
             const float2 all = tile_sum<W>(backs[odd], at.lane);
             enter[odd ^ 1][at.lane] = carried(enter[odd][at.lane], all.x, all.y);
         }
-        dl += static_cast<double>(
-            tile.template finish<FULL>(a, at, b, t0, len - t0, next, sums[odd], backs[odd], enter[odd]));
+        tile.gather(at, sums[odd], backs[odd]);
+        dl += static_cast<double>(tile.template finish<FULL>(a, at, b, t0, len - t0, next, enter[odd]));
         t0 -= Tile::TILE;
         ++k;
     };
@@ -842,7 +853,7 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs 
             double s = 0.0;
 #pragma unroll
             for (int q = 0; q < W; ++q) s += all[q][at.lane];
-            partial[b * a.dim + at.ch] = s;
+            partial[b * a.dim + at.ch] = static_cast<float>(s);
         }
     }
     for (t0 = live * Tile::TILE; t0 < a.seqlen; t0 += Tile::TILE) Tile::none(a, at, b, t0, 0);
@@ -906,16 +917,18 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_chain_kernel(GatedSca
             tile.template work<false>(place, lam2[0], left, in, sums[k & 1], backs[k & 1]);
             __syncthreads();
             put_share(place, k + 1);   // a wave that has not to look for what enters the tile
-            if (place.wave == k % W) {
+            const bool looks = place.wave == k % W;
+            if (looks) {
                 const float2 all = tile_sum<W>(backs[k & 1], place.lane);
                 float out;
                 enter[place.lane] = enter_tile(ch, at, a.dim, place.ch, all.x, all.y, a.dhL, out);
                 if (a.dh0 != nullptr && t0 == 0 && place.in) a.dh0[b * a.dim + place.ch] = out;
             }
             if (threadIdx.x == 0) taken[0] = mine;
+            if (!looks) tile.gather(place, sums[k & 1], backs[k & 1]);   // while the other looks
             __syncthreads();
-            shares[place.wave][place.lane] =
-                tile.template finish<false>(a, place, b, t0, left, in, sums[k & 1], backs[k & 1], enter);
+            if (looks) tile.gather(place, sums[k & 1], backs[k & 1]);
+            shares[place.wave][place.lane] = tile.template finish<false>(a, place, b, t0, left, in, enter);
             due = share;
         } else {
             tile.load_all(AnyIn(a, next_place, next.b, next_t0, next_left));
@@ -935,41 +948,6 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_chain_kernel(GatedSca
     }
     __syncthreads();
     put_share(Place<1>(a.dim, 0), 0);
-}
-
-// The sums of d(log_decay) over `slots` partial ones, in 64 bits and a fixed
-// order: 64 channels per workgroup, its 16 waves a sixteenth of the slots each, 4
-// loads in flight.
-constexpr int kSumWaves = 16;
-
-template <typename F>
-__global__ __launch_bounds__(kSumWaves* kWave) void gated_scan_sum_kernel(int64_t slots, int64_t dim, const F* partial,
-                                                                         float* out) {
-    __shared__ double red[kSumWaves][kWave];
-    const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
-    const int64_t ch = static_cast<int64_t>(blockIdx.x) * kWave + lane;
-    double s = 0.0;
-    if (ch < dim) {
-        constexpr int U = 4;
-        for (int64_t k0 = w; k0 < slots; k0 += U * kSumWaves) {
-            F x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t k = k0 + u * kSumWaves;
-                x[u] = k < slots ? partial[k * dim + ch] : F(0);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) s += static_cast<double>(x[u]);
-        }
-    }
-    red[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && ch < dim) {
-        double t = 0.0;
-#pragma unroll
-        for (int k = 0; k < kSumWaves; ++k) t += red[k][lane];
-        out[ch] = static_cast<float>(t);
-    }
 }
 
 // Without tokens: dh0 = dhL, no gradient of the decay.
@@ -1051,9 +1029,9 @@ int64_t groups_of(const GatedScanArgs& a) { return (a.dim + kGsChannels - 1) / k
 // us, of 8 (4 waves of 16) 126 (128); gradients 234, of 16 the same, 8 x 2048 x 5120
 // 308 against 328. A chain's tile has a fixed cost, the look for what enters it, and
 // waits are shorter the fewer tiles of a column are on their way, so its tiles are
-// longer: 256 tokens where two channels fit a lane (1 x 262144 x 2048 1022 us; of
-// 128 tokens by 128 channels 1230, by 64 channels 1490), 128 for the gradients (1 x
-// 65536 x 1536 448 us, of 64 553 to 640).
+// longer: 256 tokens where two channels fit a lane (1 x 262144 x 2048 956 us; of
+// 128 tokens by 128 channels 1351, by 64 channels 1490), 128 for the gradients (1 x
+// 65536 x 1536 411 us, of 64 540 to 615).
 template <int IO_, int V_, int T_, int W_>
 struct Shape {
     static constexpr int IO = IO_, V = V_, T = T_, W = W_, TILE = W * V * T;
@@ -1144,13 +1122,6 @@ hipError_t launch_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename F>
-hipError_t launch_sum(int64_t slots, int64_t dim, const F* partial, float* out, hipStream_t s) {
-    hipLaunchKernelGGL((gated_scan_sum_kernel<F>), dim3(static_cast<unsigned>((dim + kWave - 1) / kWave)),
-                       dim3(kSumWaves * kWave), 0, s, slots, dim, partial, out);
-    return hipGetLastError();
-}
-
 template <int IO, bool GATED>
 hipError_t launch_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     hipError_t e;
@@ -1167,15 +1138,15 @@ hipError_t launch_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
                            s, a, ch, partial);
         e = hipGetLastError();
         if (e != hipSuccess || partial == nullptr) return e;
-        return launch_sum(a.batch * ch.tiles, a.dim, partial, a.dlog_decay, s);
+        return launch_column_sums(a.dim, a.batch * ch.tiles, partial, a.dlog_decay, nullptr, s);
     }
     typedef BwdWalk<IO> S;
     const int64_t groups = groups_of(a);
-    double* partial = a.dlog_decay != nullptr ? static_cast<double*>(ws) : nullptr;
+    float* partial = a.dlog_decay != nullptr ? static_cast<float*>(ws) : nullptr;
     hipLaunchKernelGGL((gated_scan_bwd_kernel<S::IO, S::T, S::W, GATED>),
                        dim3(static_cast<unsigned>(a.batch * groups)), dim3(S::W * kWave), 0, s, a, groups, partial);
     e = hipGetLastError();
-    return e != hipSuccess || partial == nullptr ? e : launch_sum(a.batch, a.dim, partial, a.dlog_decay, s);
+    return e != hipSuccess || partial == nullptr ? e : launch_column_sums(a.dim, a.batch, partial, a.dlog_decay, nullptr, s);
 }
 
 template <int IO, int V>
@@ -1194,7 +1165,7 @@ size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu) {
 }
 
 size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu) {
-    if (!chained(a, true, cu)) return static_cast<size_t>(a.batch) * a.dim * sizeof(double);
+    if (!chained(a, true, cu)) return static_cast<size_t>(a.batch) * a.dim * sizeof(float);
     const Chain ch = chain_of(a, nullptr, true);
     return chain_bytes(ch) + static_cast<size_t>(a.batch) * ch.tiles * a.dim * sizeof(float);
 }

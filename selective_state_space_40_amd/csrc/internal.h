@@ -349,6 +349,10 @@ hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, int cu, void* ws, hipSt
 hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a, int cu, hipStream_t s);
 size_t residual_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int cu);
 hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, int cu, void* ws, hipStream_t s);
+// out0[c] = the sum over `slots` rows of partial (slots, dim), in 64 bits and a fixed
+// order; with out1 of a second such plane behind it too. Either may be null.
+hipError_t launch_column_sums(int64_t dim, int64_t slots, const float* partial, float* out0, float* out1,
+                              hipStream_t s);
 
 // Compute units of the current device, cached per device; a mamba_status.
 int current_cu_count(int* cu);
