@@ -600,6 +600,15 @@ def _output(t, name, shape, dtype, dev):
     return t, _require(t, name, shape, dtype, dev)
 
 
+def _output_like(t, name, x, dtype, dev):
+    """_output for one of an input's shape and dtype: dense, and quicker made from an
+    input that is."""
+    if t is None and x.is_contiguous():
+        t = torch.empty_like(x)
+        return t, t.data_ptr()
+    return _output(t, name, x.shape, dtype, dev)
+
+
 class _Stay:
     """The device that is current already."""
 
@@ -937,7 +946,7 @@ def gated_scan_fwd(x, decay_gate, log_decay, input_gate=None, h0=None, *, length
     gates = _gates(x, decay_gate, log_decay, input_gate, shape, dt, dev)
     pl = _require(lengths, "lengths", (batch,), torch.int32, dev)
     p0 = _require(h0, "h0", (batch, dim), torch.float32, dev)
-    y, py = _output(out, "out", shape, dt, dev)
+    y, py = _output_like(out, "out", x, dt, dev)
     hL = ph = states = ps = None
     if return_state:
         hL, ph = _output(state_out, "state_out", (batch, dim), torch.float32, dev)
@@ -999,7 +1008,7 @@ def gated_scan_update(h, x, decay_gate, log_decay, input_gate=None, *, out=None)
     dev, dt = x.device, x.dtype
     gates = _gates(x, decay_gate, log_decay, input_gate, shape, dt, dev)
     ph = _must(h, "h", shape, torch.float32, dev)
-    y, py = _output(out, "out", shape, dt, dev)
+    y, py = _output_like(out, "out", x, dt, dev)
     with _on(dev):
         st = lib.gated_scan_update(*shape, _DTYPES[dt], ph, *gates, py, _raw_stream(dev))
     if st:
@@ -1040,7 +1049,7 @@ def gated_norm_fwd(x, z=None, weight=None, *, groups=1, eps=1e-5, gate_first=Tru
     px = _rows(x, "x", shape, dt, dev)
     pz = (None, 0) if z is None else _rows(z, "z", shape, dt, dev)
     pw = _require(weight, "weight", (dim,), torch.float32, dev)
-    y, py = _output(out, "out", shape, dt, dev)
+    y, py = _output_like(out, "out", x, dt, dev)
     rstd = torch.empty((*shape[:-1], groups), dtype=torch.float32, device=dev)
     with _on(dev):
         st = lib.gated_norm_fwd(rows, dim, groups, _DTYPES[dt], _gate_code(z, gate_first), *px, *pz,
@@ -1062,9 +1071,9 @@ def gated_norm_bwd(x, z, weight, rstd, *, dy, groups=1, gate_first=True, out=Non
     pw = _require(weight, "weight", (dim,), torch.float32, dev)
     pr = _must(rstd, "rstd", (*shape[:-1], groups), torch.float32, dev)
     pdy = _must(dy, "dy", shape, dt, dev)
-    dx, pdx = _output(out, "out", shape, dt, dev)
-    dz = None if z is None else torch.empty(shape, dtype=dt, device=dev)
-    dw = None if weight is None else torch.empty(dim, dtype=torch.float32, device=dev)
+    dx, pdx = _output_like(out, "out", x, dt, dev)
+    dz = None if z is None else torch.empty_like(dy)   # dense, as dy is
+    dw = None if weight is None else torch.empty_like(weight)
     code = _DTYPES[dt]
     with _on(dev):
         nbytes = 0
@@ -1104,8 +1113,8 @@ def residual_norm_fwd(x, residual, scale=None, weight=None, *, eps=1e-5, out=Non
     pres = _must(residual, "residual", shape, rt, dev)
     psc = _require(scale, "scale", (dim,), torch.float32, dev)
     pw = _require(weight, "weight", (dim,), torch.float32, dev)
-    y, py = _output(out, "out", shape, dt, dev)
-    total, pt = _output(total_out, "total_out", shape, rt, dev)
+    y, py = _output_like(out, "out", x, dt, dev)
+    total, pt = _output_like(total_out, "total_out", residual, rt, dev)
     rstd = torch.empty((*shape[:-1], 1), dtype=torch.float32, device=dev)
     with _on(dev):
         st = lib.residual_norm_fwd(rows, dim, _DTYPES[dt], _DTYPES[rt], px, pres, psc, pw, eps, py, pt,
@@ -1132,10 +1141,10 @@ def residual_norm_bwd(total, weight, rstd, x=None, scale=None, *, dy, dtotal=Non
     psc = _require(scale, "scale", (dim,), torch.float32, dev)
     px = None if scale is None else _must(x, "x", shape, dt, dev)
     pdt = _require(dtotal, "dtotal", shape, rt, dev)
-    dres = torch.empty(shape, dtype=rt, device=dev)
-    dx = dres if scale is None and rt is dt else torch.empty(shape, dtype=dt, device=dev)
-    dsc = None if scale is None else torch.empty(dim, dtype=torch.float32, device=dev)
-    dw = None if weight is None else torch.empty(dim, dtype=torch.float32, device=dev)
+    dres = torch.empty_like(total)   # dense, as total is
+    dx = dres if scale is None and rt is dt else torch.empty_like(dy)
+    dsc = None if scale is None else torch.empty_like(scale)
+    dw = None if weight is None else torch.empty_like(weight)
     codes = _DTYPES[dt], _DTYPES[rt]
     with _on(dev):
         nbytes = 0
