@@ -7,9 +7,11 @@
 //
 // All are bound by memory: every tensor is read or written once. A lane holds 8
 // consecutive values of a part (16 above 8192 of them), so that a part of n values
-// takes as many lanes as it has eights - 16 or 64 of a wave, or as many waves as
-// they fill - and few registers; weights and the sums over rows stay in registers
-// while a workgroup walks rows, with the next row's loads out.
+// takes as many lanes as it has eights - some of a wave's, or several waves' - and few
+// registers; weights and the sums over rows stay in registers while a workgroup walks
+// rows, with the next row's loads out. In bf16 on MI355X, 16384 x 5120: gated forward
+// 90 us (5.6 TB/s), gradients 155 to 164 (5.1 to 5.4), with the residual sum in fp32
+// 178 (5.6), its gradients 192 (5.2); a large copy reaches 4.9 to 5.6 by machine.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -316,6 +318,7 @@ __device__ __forceinline__ void end_run() {
     typedef Cells<IO, CH, AL, SHORT> C;                         \
     typedef Params<CH, AL, SHORT> P
 
+// One sum a row, of the squares: 16384 x 5120 in bf16 90 us, 80 parts of 64 a row 88.
 template <int IO, int TEAM, int CH, bool AL, int GATE>
 __global__ __launch_bounds__(kThreads<TEAM>) void gated_norm_fwd_kernel(GatedNormArgs a, Layout lay) {
     MAMBA_NORM_TYPES;
@@ -432,6 +435,11 @@ struct GatedTerms {
     }
 };
 
+// One sum a row, of u n; rstd comes from the forward pass. The terms behind the sum
+// are formed before it and kept (asm statements hold them in place: left alone, the
+// compiler moves their forming behind the sum, where it takes more registers and half
+// the workgroups find room). 16384 x 5120 in bf16: gate behind 155 us, gate first in 8
+// groups 164; 4000 x 16384 159 (with its column sums in registers, spilling, 709).
 template <int IO, int TEAM, int CH, bool AL, int GATE>
 __global__ __launch_bounds__(kThreads<TEAM>) void gated_norm_bwd_kernel(GatedNormArgs a, Layout lay,
                                                                              float* partial) {
@@ -511,6 +519,8 @@ __global__ __launch_bounds__(kThreads<TEAM>) void gated_norm_bwd_kernel(GatedNor
     put_columns<TEAM, CH>(tm, walk, span, cols, out, dw);
 }
 
+// As the gated norm, of the sum before its rounding: 16384 x 5120 in bf16 with an fp32
+// stream 178 us.
 template <int IO, int RIO, int TEAM, int CH, bool AL>
 __global__ __launch_bounds__(kThreads<TEAM>) void residual_norm_fwd_kernel(ResidualNormArgs a, Layout lay) {
     MAMBA_NORM_TYPES;
@@ -567,7 +577,9 @@ __global__ __launch_bounds__(kThreads<TEAM>) void residual_norm_fwd_kernel(Resid
     }
 }
 
-// SCALE: x is read and dscale formed.
+// SCALE: x is read and dscale formed. What is read behind the sum is loaded behind the
+// row before, which leaves no second copy of it in registers: 16384 x 5120 in bf16 192
+// us, 4000 x 16384 186, 1000 x 1531 in fp32 18.
 template <int IO, int RIO, int TEAM, int CH, bool AL, bool SCALE>
 __global__ __launch_bounds__(kThreads<TEAM>) void residual_norm_bwd_kernel(ResidualNormArgs a, Layout lay,
                                                                                 float* partial) {
@@ -849,7 +861,8 @@ hipError_t launch_zero(int64_t dim, float* out0, float* out1, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_column_sums(int64_t dim, int64_t slots, const float* partial, float* out0, float* out1, hipStream_t s) {
+hipError_t launch_column_sums(int64_t dim, int64_t slots, const float* partial, float* out0, float* out1,
+                              hipStream_t s) {
     hipLaunchKernelGGL(column_sums_kernel,
                        dim3(static_cast<unsigned>((dim + kColumns - 1) / kColumns), out1 != nullptr ? 2 : 1),
                        dim3(kColumnThreads), 0, s, dim, slots, partial, out0, out1);

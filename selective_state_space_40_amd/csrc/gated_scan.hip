@@ -540,7 +540,9 @@ __device__ __forceinline__ float2 tile_sum(const float2 (&sums)[W][kGsChannels],
 }
 
 // The forward pass, a workgroup walking one row's tiles. The waves take turns in
-// carrying the state over a tile, a lane for each channel.
+// carrying the state over a tile, a lane for each channel. About 42 vector
+// instructions a value, 7 of them transcendental, keep the vector units busy for 60% of
+// the time beside 80% of the memory's rate: 8 x 2048 x 4096 in bf16 121 us (4.4 TB/s).
 template <int IO, int V, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs a, int64_t groups) {
     typedef FwdTile<IO, V, T, W, GATED> Tile;
@@ -576,7 +578,10 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs 
 }
 
 // The forward pass as a chain. A workgroup takes tickets until none is left, one
-// ahead of the tile whose inputs are being loaded.
+// ahead of the tile whose inputs are being loaded. 1 x 262144 x 2048 in bf16 957 us
+// (4.5 TB/s), of which the look for what enters a tile, a trip to memory in each, costs
+// 150: a wave that does nothing but look, and looking while the next tile is worked
+// through, were no faster (981 and 1491 us).
 template <int IO, int V, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_chain_kernel(GatedScanArgs a, Chain ch) {
     typedef FwdTile<IO, V, T, W, GATED> Tile;
@@ -805,7 +810,10 @@ struct BwdTile {
 };
 
 // The backward pass, a workgroup walking one row's tiles from the last to the
-// first. The state entering a tile comes from the forward pass.
+// first. The state entering a tile comes from the forward pass, a block's start at a
+// time, so that nothing is walked twice. About 70 vector instructions a value keep the
+// vector units busy for 59% of the time at 4 waves a SIMD: 8 x 2048 x 5120 in bf16 308
+// us (3.8 TB/s), 8 x 2048 x 4096, where all columns run at once, 234 (4.0).
 template <int IO, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
                                                                float* partial) {
@@ -859,8 +867,9 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs 
     for (t0 = live * Tile::TILE; t0 < a.seqlen; t0 += Tile::TILE) Tile::none(a, at, b, t0, 0);
 }
 
-// The backward pass as a chain: position j of a row is its j-th tile from the
-// last one with tokens. `partial` holds the decay's gradient of every (row, tile),
+// The backward pass as a chain (1 x 65536 x 1536 in bf16 411 us, of which the looks
+// cost 60): position j of a row is its j-th tile from the last one with tokens.
+// `partial` holds the decay's gradient of every (row, tile),
 // zeros for tiles without tokens.
 template <int IO, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_chain_kernel(GatedScanArgs a, Chain ch,
@@ -962,7 +971,8 @@ __global__ __launch_bounds__(256) void gated_scan_empty_kernel(int64_t state, in
 
 constexpr int words_of(int io, int v) { return io == kIoF32 ? v : (v + 1) / 2; }
 
-// One token: V channels to a lane.
+// One token: V channels to a lane, all loads out at once. 256 x 5120 in bf16 takes 5.9
+// us, of the call's 9.1.
 template <int IO, int V>
 __global__ __launch_bounds__(256) void gated_scan_update_kernel(GatedScanArgs a) {
     constexpr int SIZE = IO == kIoF32 ? 4 : 2;
@@ -1146,7 +1156,8 @@ hipError_t launch_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
     hipLaunchKernelGGL((gated_scan_bwd_kernel<S::IO, S::T, S::W, GATED>),
                        dim3(static_cast<unsigned>(a.batch * groups)), dim3(S::W * kWave), 0, s, a, groups, partial);
     e = hipGetLastError();
-    return e != hipSuccess || partial == nullptr ? e : launch_column_sums(a.dim, a.batch, partial, a.dlog_decay, nullptr, s);
+    if (e != hipSuccess || partial == nullptr) return e;
+    return launch_column_sums(a.dim, a.batch, partial, a.dlog_decay, nullptr, s);
 }
 
 template <int IO, int V>
