@@ -54,7 +54,8 @@ extern "C" {
  *                                        that start behind a row's length are left
  *                                        as they were
  *
- * dim and the strides are at most MAMBA_GATED_SCAN_MAX_DIM (else
+ * dim and the strides are at most MAMBA_GATED_SCAN_MAX_DIM, batch * seqlen at
+ * most 2^28 and batch * ceil(dim / 64) below 2^23 (else
  * MAMBA_ERR_UNSUPPORTED). What stands behind a row's length is never read. A NaN
  * or infinite value stays in its channel and reaches no earlier output; where the
  * definition has an infinity, NaN may come out. Sums and states are fp32, and the
@@ -108,6 +109,7 @@ int gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
  * x, decay_gate, input_gate (batch, dim)       rows x_stride, decay_stride,
  *                                              input_stride elements apart
  * y                         (batch, dim)       written
+ * batch * ceil(dim / 64) is below 2^23 (else MAMBA_ERR_UNSUPPORTED).
  */
 int gated_scan_update(int64_t batch, int64_t dim, int dtype, float* h, const void* x,
                       int64_t x_stride, const void* decay_gate, int64_t decay_stride,

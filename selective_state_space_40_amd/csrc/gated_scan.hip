@@ -1072,10 +1072,11 @@ int chain_tile(const GatedScanArgs& a, bool bwd) {
 // 215, 234 against 276, 308 against 344. In fp32 32 columns 47 against 22, 128 74
 // against 60, 256 116 against 115, 512 217 against 202; gradients 99 against 36, 143
 // against 112, 211 against 200, 412 against 357. Sequences of fewer than 4 tiles of
-// 128 are walked (512 tokens of 192 columns: 16 us against 25).
+// 128 are walked (512 tokens of 192 columns: 16 us against 25), and so would be 2^26
+// tiles, for which clearing the words would count 2^32 threads.
 bool chained(const GatedScanArgs& a, bool bwd, int cu) {
     const double columns = static_cast<double>(a.batch * groups_of(a)), len = static_cast<double>(a.seqlen);
-    if (a.seqlen < 512 || columns * (len / kFwdShortest + 1.0) >= 2147483648.0) return false;
+    if (a.seqlen < 512 || columns * (len / kFwdShortest + 1.0) >= 67108864.0) return false;
     const double each = columns * 256.0 / cu;   // as of 256 compute units
     const double rounds = ceil(columns / cu);
     double walk, chain;

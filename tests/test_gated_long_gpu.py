@@ -184,6 +184,42 @@ def test_states_in_place():
             assert hL is state and torch.equal(y, want["y"]) and torch.equal(hL, want["hL"])
 
 
+def _bwd(c, states, g, dhL, ws):
+    """gated_scan_bwd through the C ABI, outputs as in the dict g (None: not wanted)."""
+    b, n, d = c["x"].shape
+    p = lambda t: None if t is None else t.data_ptr()   # noqa: E731
+    return ms.load_library().gated_scan_bwd(
+        b, n, d, 1 if c["x"].dtype == BF else 0, p(c["x"]), d, p(c["decay_gate"]), d, p(c["log_decay"]),
+        p(c["input_gate"]), d, p(c["lengths"]), p(states), p(c["dy"]), p(dhL),
+        *(p(g[k]) for k in ("dx", "ddecay_gate", "dinput_gate", "dlog_decay", "dh0")), p(ws), ws.numel(),
+        torch.cuda.current_stream(DEV).cuda_stream)
+
+
+@TYPES
+def test_adjoints_in_place_and_outputs_not_wanted(dtype):
+    c = _make(3, 5000, 130, dtype, 12, lengths=[5000, 0, 300])
+    states = _forward(c)["block_states"]
+    want = _backward(c, states)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        g = {k: None if t is None else torch.full_like(t, 7.0) for k, t in want.items()}
+        g["dh0"] = c["dhL"].clone()   # the last tile writes where the first one reads
+        assert _bwd(c, states, g, g["dh0"], ws) == 0
+        torch.cuda.synchronize()
+        for k, t in want.items():
+            assert torch.equal(g[k], t), k
+    for missing in ("dlog_decay", "dh0"):
+        g = {k: torch.full_like(t, 7.0) for k, t in want.items()}
+        g[missing] = None
+        assert _bwd(c, states, g, c["dhL"], ws) == 0
+        torch.cuda.synchronize()
+        for k, t in want.items():
+            assert g[k] is None or torch.equal(g[k], t), k
+    c["dhL"] = None
+    assert _bwd(c, states, g | dict(dh0=None), None, ws) == 0
+    assert _bwd(c, states, g, None, ws[:256]) == -4   # scratch too small: nothing is queued
+
+
 def test_captured_calls_replay():
     # graphs own their scratch; replayed by turns, and with eager calls between
     graphs = []
