@@ -981,12 +981,10 @@ def gated_scan_bwd(x, decay_gate, log_decay, input_gate=None, *, block_states, d
     pdy = _must(dy, "dy", shape, dt, dev)
     pdh = _require(dhL, "dhL", (batch, dim), torch.float32, dev)
 
-    def new(*size, dtype=torch.float32, wanted=True):
-        return torch.empty(size, dtype=dtype, device=dev) if wanted else None
-
-    g = dict(dx=new(*shape, dtype=dt), ddecay_gate=new(*shape, dtype=dt),
-             dinput_gate=new(*shape, dtype=dt, wanted=input_gate is not None),
-             dlog_decay=new(dim, wanted=want_dlog_decay), dh0=new(batch, dim, wanted=want_dh0))
+    like = torch.empty_like   # dense, as dy and log_decay are
+    g = dict(dx=like(dy), ddecay_gate=like(dy), dinput_gate=None if input_gate is None else like(dy),
+             dlog_decay=like(log_decay) if want_dlog_decay else None,
+             dh0=torch.empty((batch, dim), dtype=torch.float32, device=dev) if want_dh0 else None)
     code = _DTYPES[dt]
     with _on(dev):
         nbytes = _scratch_bytes("gated_scan_bwd_workspace_size", dev.index, batch, seqlen, dim, code)

@@ -755,18 +755,20 @@ constexpr int kFwdWaves = 320, kBwdWaves = 8;   // to a compute unit, at least
 // forward about 320 waves to a compute unit (16384 rows of 5120: 91 us, of 80 waves 99;
 // 2048 x 80 parts of 64 118 and 126); backward 8 (16384 x 2048 71 us, of 16 75, of 4
 // 85; 16384 x 5120 155 and of 16 167), as fewer rows at once are read in longer
-// stretches and every workgroup leaves its columns' sums, and no more than a quarter of
+// stretches and every workgroup leaves its columns' sums; no more than a quarter of
 // the rows have one (1000 x 1531 in fp32 18 us, a workgroup each 23; 3000 x 1024 22 and
-// 25).
+// 25), unless compute units would have none (243 x 12400 37 us, a quarter 40; 8 x 14966 in fp32 27
+// and 43).
 Layout layout_for(int64_t rows, int64_t groups, const Shape& sh, int cu, bool bwd) {
     const int teams = sh.threads / sh.lanes;
     int across = 1;
     while (across * 2 <= teams && teams % (across * 2) == 0 && groups % (across * 2) == 0) across *= 2;
     const int64_t down = teams / across, most = (rows + down - 1) / down;
     const int64_t each = ((bwd ? kBwdWaves : kFwdWaves) * kWave + sh.threads - 1) / sh.threads;
-    int64_t slots = each * cu / (groups / across);
-    const int64_t cap = bwd ? most / 4 : most;
-    if (slots > cap) slots = cap;
+    const int64_t blocks = groups / across, few = (cu + blocks - 1) / blocks;
+    int64_t slots = each * cu / blocks;
+    if (bwd && slots > most / 4) slots = most / 4 > few ? most / 4 : few;
+    if (slots > most) slots = most;
     return {sh.lanes, across, static_cast<int>(slots < 1 ? 1 : slots)};
 }
 

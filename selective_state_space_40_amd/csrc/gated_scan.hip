@@ -239,7 +239,10 @@ __device__ __forceinline__ void append(float& G, float& h, float nextG, float ne
 // How a tile learns the state that enters it. A workgroup that walks a row knows
 // it; where rows and channels are too few to fill the chip, tiles go to the
 // workgroups one by one (a chain), in the order of tickets taken from a counter:
-// all rows' and groups' first tiles, then all second ones. A tile's sum over its
+// all rows' and groups' first tiles, then all second ones; tiles without tokens, which
+// nothing waits for, come last. (In between, they would let some workgroups run ahead
+// to tiles that wait for ones which others hold for later: 11 rows of up to 30893 x 240
+// took 412 us for their gradients, all rows full 336.) A tile's sum over its
 // tokens (G, h) is published at once, and what enters it is folded, always in the
 // same order, from the sums of the up to 7 tiles before it in its run of 8, of the
 // up to 7 runs before that in their stretch of 8 runs, and the state that enters
@@ -281,37 +284,64 @@ __device__ __forceinline__ Word await(const Word* at, Word w) {
     return w;
 }
 
-// The chain's scratch: a counter (256 bytes), then words for every (row, tile),
-// (row, run) and (row, stretch) of all channels.
+// The chain's scratch: a counter (256 bytes), words for every (row, tile), (row, run)
+// and (row, stretch) of all channels, and the order of the (tile, row) pairs where rows
+// are of different lengths.
 struct Chain {
     uint32_t* ticket;
     Word *tile, *run, *stretch;
-    uint32_t groups, columns, tiles, runs, stretches;
-    bool once;   // a workgroup for every tile
+    uint32_t* order;
+    const int32_t* lengths;
+    int64_t seqlen;
+    uint32_t groups, batch, tiles, runs, stretches, pairs;
+    int tokens;   // of a tile
+    bool once;    // a workgroup for every tile
     int64_t width;
 
-    __host__ __device__ Chain(void* ws, int64_t batch, int64_t seqlen, int64_t channel_groups, int tile_tokens) {
+    // Of more rows than this, a pair's place takes longer to count than it saves.
+    static constexpr uint32_t kOrdered = 512;
+
+    __host__ __device__ Chain(void* ws, int64_t rows, int64_t length, const int32_t* lens, int64_t channel_groups,
+                              int tile_tokens)
+        : seqlen(length), tokens(tile_tokens), once(false) {
         groups = static_cast<uint32_t>(channel_groups);
-        columns = static_cast<uint32_t>(batch * channel_groups);
-        tiles = static_cast<uint32_t>((seqlen + tile_tokens - 1) / tile_tokens);
+        batch = static_cast<uint32_t>(rows);
+        tiles = static_cast<uint32_t>((length + tile_tokens - 1) / tile_tokens);
         runs = (tiles + kRun - 1) / kRun;
         stretches = (tiles + kStretch - 1) / kStretch;
-        once = false;
+        pairs = batch * tiles;
         width = channel_groups * kGsChannels;
+        lengths = batch <= kOrdered ? lens : nullptr;
         ticket = static_cast<uint32_t*>(ws);
         tile = reinterpret_cast<Word*>(static_cast<char*>(ws) + 256);
-        run = tile + batch * tiles * width;
-        stretch = run + batch * runs * width;
+        run = tile + rows * tiles * width;
+        stretch = run + rows * runs * width;
+        order = reinterpret_cast<uint32_t*>(tile + words());
     }
     __host__ __device__ int64_t words() const {
-        return static_cast<int64_t>(columns / groups) * (static_cast<int64_t>(tiles) + runs + stretches) * width;
+        return batch * (static_cast<int64_t>(tiles) + runs + stretches) * width;
     }
 };
 
-__global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint32_t* ticket, Word* words, int64_t pairs) {
+// Clears the words and the counter, two words to a thread, and sets the order: a pair
+// with tokens comes behind all such of smaller tiles, and of its own tile and smaller
+// rows; one without behind all with.
+__global__ __launch_bounds__(256) void gated_scan_clear_kernel(Chain ch) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i == 0) *ticket = 0;
-    if (i < pairs) reinterpret_cast<ulonglong2*>(words)[i] = make_ulonglong2(kNoWord, kNoWord);
+    if (i == 0) *ch.ticket = 0;
+    if (i < ch.words() / 2) reinterpret_cast<ulonglong2*>(ch.tile)[i] = make_ulonglong2(kNoWord, kNoWord);
+    if (ch.lengths == nullptr || i >= ch.pairs) return;
+    const uint32_t p = static_cast<uint32_t>(i), j = p / ch.batch, b = p - j * ch.batch;
+    uint32_t before = 0, all = 0;
+    bool live = false;
+    for (uint32_t r = 0; r < ch.batch; ++r) {
+        const int64_t len = row_length(ch.lengths, r, ch.seqlen);
+        const uint32_t n = static_cast<uint32_t>((len + ch.tokens - 1) / ch.tokens);
+        all += n;
+        before += (n < j ? n : j) + (r < b && n > j ? 1 : 0);
+        if (r == b) live = n > j;
+    }
+    ch.order[live ? before : all + (p - before)] = p;
 }
 
 // The next ticket. (Through an address that the compiler takes for a lane's own: for
@@ -331,11 +361,13 @@ struct Link {
     bool any;
 
     __device__ __forceinline__ Link(const Chain& ch, uint32_t n) {
-        j = n / ch.columns;
-        const uint32_t r = n - j * ch.columns;
-        b = r / ch.groups;
-        group = r - b * ch.groups;
-        any = n != kNoTicket && j < ch.tiles;
+        uint32_t p = n / ch.groups;
+        group = n - p * ch.groups;
+        any = n != kNoTicket && p < ch.pairs;
+        p = any ? p : 0;
+        if (ch.lengths != nullptr) p = ((const __attribute__((address_space(4))) uint32_t*)ch.order)[p];
+        j = p / ch.batch;
+        b = p - j * ch.batch;
     }
 };
 
@@ -1092,19 +1124,21 @@ bool chained(const GatedScanArgs& a, bool bwd, int cu) {
 }
 
 Chain chain_of(const GatedScanArgs& a, void* ws, bool bwd) {
-    return Chain(ws, a.batch, a.seqlen, groups_of(a), chain_tile(a, bwd));
+    return Chain(ws, a.batch, a.seqlen, a.lengths, groups_of(a), chain_tile(a, bwd));
 }
 
-size_t chain_bytes(const Chain& ch) { return 256 + static_cast<size_t>(ch.words()) * sizeof(Word); }
+size_t chain_bytes(const Chain& ch) {
+    return 256 + static_cast<size_t>(ch.words()) * sizeof(Word) + (static_cast<size_t>(ch.pairs) * 4 + 15) / 16 * 16;
+}
 
 // Clears the chain's words; sets its grid: a workgroup for every tile up to two
 // rounds of them (of 8 waves, one to a compute unit), else one for each unit.
 hipError_t begin_chain(Chain& ch, int cu, unsigned* grid, hipStream_t s) {
-    const int64_t pairs = ch.words() / 2, total = static_cast<int64_t>(ch.columns) * ch.tiles;
+    const int64_t total = static_cast<int64_t>(ch.pairs) * ch.groups;
     ch.once = total <= 2 * static_cast<int64_t>(cu);
     *grid = static_cast<unsigned>(ch.once ? total : cu);
-    hipLaunchKernelGGL(gated_scan_clear_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, s,
-                       ch.ticket, ch.tile, pairs);
+    hipLaunchKernelGGL(gated_scan_clear_kernel, dim3(static_cast<unsigned>((ch.words() / 2 + 255) / 256)), dim3(256), 0,
+                       s, ch);
     return hipGetLastError();
 }
 
@@ -1173,7 +1207,7 @@ hipError_t launch_update(const GatedScanArgs& a, hipStream_t s) {
 // Without regard to the strides, which are not known when the scratch is asked for:
 // that of the shortest tiles a chain may take.
 size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu) {
-    return chained(a, false, cu) ? chain_bytes(Chain(nullptr, a.batch, a.seqlen, groups_of(a), kFwdShortest)) : 0;
+    return chained(a, false, cu) ? chain_bytes(Chain(nullptr, a.batch, a.seqlen, nullptr, groups_of(a), kFwdShortest)) : 0;
 }
 
 size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu) {

@@ -107,6 +107,19 @@ def test_ragged_rows(gated, dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("kind", ["even", "none", "one", "many"])
+def test_order_of_ragged_tiles(kind, dtype):
+    # tiles with tokens come first, whatever the lengths; above 512 rows in the rows' order
+    n, b, d = 4000, 23, 70
+    if kind == "many":
+        n, b, d = 520, 513, 8
+    g = torch.Generator().manual_seed(b)
+    lens = dict(even=torch.arange(b) * n // (b - 1), none=torch.zeros(b), one=(torch.arange(b) == 7) * n,
+                many=torch.randint(0, n + 1, (b,), generator=g))[kind].to(torch.int32).tolist()
+    _check(_make(b, n, d, dtype, 13, lengths=lens), f"order {kind} {dtype}")
+
+
+@TYPES
 def test_blocks_behind_a_row_are_left(dtype):
     # through the C ABI, as the binding hands out memory of its own
     b, n, d = 2, 1500, 64
