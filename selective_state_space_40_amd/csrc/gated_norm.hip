@@ -757,8 +757,8 @@ constexpr int kFwdWaves = 320, kBwdWaves = 8;   // to a compute unit, at least
 // 85; 16384 x 5120 155 and of 16 167), as fewer rows at once are read in longer
 // stretches and every workgroup leaves its columns' sums; no more than a quarter of
 // the rows have one (1000 x 1531 in fp32 18 us, a workgroup each 23; 3000 x 1024 22 and
-// 25), unless compute units would have none (243 x 12400 37 us, a quarter 40; 8 x 14966 in fp32 27
-// and 43).
+// 25), unless compute units would have none (243 x 12400 37 us, a quarter 40; 8 x 14966
+// in fp32 27 and 43).
 Layout layout_for(int64_t rows, int64_t groups, const Shape& sh, int cu, bool bwd) {
     const int teams = sh.threads / sh.lanes;
     int across = 1;

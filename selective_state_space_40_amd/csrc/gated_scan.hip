@@ -1103,24 +1103,35 @@ int chain_tile(const GatedScanArgs& a, bool bwd) {
 // against 156; gradients 104 against 31, 116 against 114, 120 against 149, 198 against
 // 215, 234 against 276, 308 against 344. In fp32 32 columns 47 against 22, 128 74
 // against 60, 256 116 against 115, 512 217 against 202; gradients 99 against 36, 143
-// against 112, 211 against 200, 412 against 357. Sequences of fewer than 4 tiles of
+// against 112, 211 against 200, 412 against 357. Rows of different lengths are taken
+// to hold three quarters of the longest, which a walk gains nothing from while all
+// columns run at once (12 rows up to 3000 x 640 in bf16 74 us against 45, gradients 155
+// against 81; all full 74 and 55, 156 and 111). Sequences of fewer than 4 tiles of
 // 128 are walked (512 tokens of 192 columns: 16 us against 25), and so would be 2^26
 // tiles, for which clearing the words would count 2^32 threads.
-bool chained(const GatedScanArgs& a, bool bwd, int cu) {
+bool chained(const GatedScanArgs& a, bool bwd, bool ragged, int cu) {
     const double columns = static_cast<double>(a.batch * groups_of(a)), len = static_cast<double>(a.seqlen);
     if (a.seqlen < 512 || columns * (len / kFwdShortest + 1.0) >= 67108864.0) return false;
-    const double each = columns * 256.0 / cu;   // as of 256 compute units
-    const double rounds = ceil(columns / cu);
+    const double part = ragged ? 0.75 : 1.0;
+    const double each = columns * 256.0 / cu * part;   // as of 256 compute units
     double walk, chain;
     if (a.io == kIoBF16) {
-        walk = bwd ? 8.0 + len * 0.048 * rounds : 2.0 + len * 0.0255 * rounds;
-        chain = 14.0 + len * each * (bwd ? 2.5e-4 : 1.1e-4);
+        const double rounds = bwd ? fmax(1.0, columns / cu) : ceil(columns / cu);
+        walk = (bwd ? 6.0 : 2.0) + len * (bwd ? 0.053 : 0.0255) * (1.0 + (rounds - 1.0) * part);
+        chain = bwd ? 14.0 + len * each * 2.6e-4 : 14.0 + len * each * 1.1e-4;
     } else {
         walk = bwd ? 8.0 + len * fmax(0.04 + 1.9e-4 * each, 3.9e-4 * each)
                    : 3.0 + len * fmax(0.021 + 1.1e-4 * each, 2.1e-4 * each);
-        chain = 14.0 + len * each * (bwd ? 3.3e-4 : 1.8e-4);
+        chain = bwd ? 18.0 + len * each * 3.4e-4 : 12.0 + len * each * 1.9e-4;
     }
     return chain < walk;
+}
+
+bool chained(const GatedScanArgs& a, bool bwd, int cu) { return chained(a, bwd, a.lengths != nullptr, cu); }
+
+// Whether any call of these sizes does.
+bool may_chain(const GatedScanArgs& a, bool bwd, int cu) {
+    return chained(a, bwd, false, cu) || chained(a, bwd, true, cu);
 }
 
 Chain chain_of(const GatedScanArgs& a, void* ws, bool bwd) {
@@ -1204,16 +1215,18 @@ hipError_t launch_update(const GatedScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Without regard to the strides, which are not known when the scratch is asked for:
-// that of the shortest tiles a chain may take.
+// Without regard to the strides and to whether rows differ in length, which are not
+// known when the scratch is asked for: that of the shortest tiles a chain may take.
 size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu) {
-    return chained(a, false, cu) ? chain_bytes(Chain(nullptr, a.batch, a.seqlen, nullptr, groups_of(a), kFwdShortest)) : 0;
+    if (!may_chain(a, false, cu)) return 0;
+    return chain_bytes(Chain(nullptr, a.batch, a.seqlen, nullptr, groups_of(a), kFwdShortest));
 }
 
 size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu) {
-    if (!chained(a, true, cu)) return static_cast<size_t>(a.batch) * a.dim * sizeof(float);
+    const size_t walk = static_cast<size_t>(a.batch) * a.dim * sizeof(float);
+    if (!may_chain(a, true, cu)) return walk;
     const Chain ch = chain_of(a, nullptr, true);
-    return chain_bytes(ch) + static_cast<size_t>(a.batch) * ch.tiles * a.dim * sizeof(float);
+    return chain_bytes(ch) + ch.tiles * walk;   // a share of the decay's gradient for each tile
 }
 
 hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
