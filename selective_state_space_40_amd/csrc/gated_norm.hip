@@ -416,9 +416,11 @@ struct GatedTerms {
         float v = x;
         up = dy;
         if constexpr (GATE != kGateNone) {
-            // sigmoid and 1 - sigmoid, each to its own accuracy
-            const float e = fast_exp2(fminf(-z * kLog2e, 126.0f));
-            const float sg = fast_rcp(1.0f + e), rest = z == z ? e * sg : z;
+            // sigmoid and 1 - sigmoid, each to its own accuracy. Far down the sigmoid is 0,
+            // as forward: a z of the type's lowest value is what masks close a gate with,
+            // and times 2^-126 it would still be -4.
+            const float t = -z * kLog2e, e = fast_exp2(t);
+            const float sg = fast_rcp(1.0f + e), rest = t > 126.0f ? 1.0f : e * sg;
             const float sl = z * sg, dsl = sg * fmaf(z, rest, 1.0f);
             if constexpr (GATE == kGateFirst) {
                 v = x * sl;
