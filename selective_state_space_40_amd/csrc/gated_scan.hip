@@ -60,12 +60,13 @@ __device__ __forceinline__ float sigmoid(float v) {
     return fast_rcp(1.0f + fast_exp2(-v * kLog2e));
 }
 
-// sigmoid(v) and 1 - sigmoid(v), each to its own accuracy.
+// sigmoid(v) and 1 - sigmoid(v), each to its own accuracy. Far down p is 0, as
+// forward: what a gate closed by the type's lowest value lets through is nothing,
+// behind which a masked x may be as large as the type goes.
 __device__ __forceinline__ void sigmoid_both(float v, float& p, float& rest) {
-    const float x = -v * kLog2e;
-    const float e = fast_exp2(x > 126.0f ? 126.0f : x);   // a NaN stays one
+    const float x = -v * kLog2e, e = fast_exp2(x);
     p = fast_rcp(1.0f + e);
-    rest = e * p;
+    rest = x > 126.0f ? 1.0f : e * p;   // a NaN stays one
 }
 
 // A value that is formed here and not later from what it is made of, which is

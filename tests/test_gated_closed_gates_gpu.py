@@ -51,3 +51,45 @@ def test_norm_gate_of_the_lowest_value(dim, groups, first, dtype):
     shut = shut.to(DEV)
     assert not bool(y[shut].any()) and not bool(grads["dz"][shut].any())
     assert not first or not bool(grads["dx"][shut].any())
+
+
+def _sequences(b, n, d, dtype, seed, gated=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s, dt=dtype: torch.randn(*s, generator=g).to(dt).to(DEV)   # noqa: E731
+    return dict(x=r(b, n, d), decay_gate=r(b, n, d), log_decay=-torch.logspace(-3, 1, d).to(DEV),
+                input_gate=r(b, n, d) if gated else None, h0=r(b, d, dt=F32), dy=r(b, n, d),
+                dhL=r(b, d, dt=F32)), (torch.rand(b, n, d, generator=g) < 0.3).to(DEV)
+
+
+def _results(c):
+    y, hL, states = ms.gated_scan_fwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], c["h0"],
+                                      return_block_states=True)
+    g = ms.gated_scan_bwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], block_states=states,
+                          dy=c["dy"], dhL=c["dhL"])
+    return dict(y=y, hL=hL, block_states=states, **g)
+
+
+@TYPES
+@pytest.mark.parametrize("n", [100, 1300])   # walked, and in bf16 and fp32 a chain
+@pytest.mark.parametrize("which,gate", [("input_gate", -2000.0), ("input_gate", "lowest"), ("input_gate", "infinite"),
+                                        ("decay_gate", -2000.0), ("decay_gate", "lowest"), ("decay_gate", "infinite")])
+def test_nothing_enters_through_a_closed_gate(which, gate, n, dtype):
+    # exp(-2000) is 0 in 64 bits: the token's weight w is 0 by either gate, so x counts
+    # as 0 there, the type's lowest value as well, and it has no gradient
+    c, shut = _sequences(2, n, 66, dtype, n, gated=True)
+    low = torch.finfo(dtype).min
+    value = dict(lowest=low, infinite=float("-inf")).get(gate, gate)
+    c[which] = torch.where(shut, torch.tensor(value, dtype=dtype, device=DEV), c[which])
+    _say(f"case {which} {gate} {n} {dtype}")
+    c["x"] = torch.where(shut, torch.tensor(0, dtype=dtype, device=DEV), c["x"])
+    want = _results(c)
+    if which == "input_gate" and gate == -2000.0:
+        exact = ref.scan(**c)
+        # 2000 2^-25 log2(e) more of a sigmoid that is 0 all the same
+        ref.check_scan({k: t for k, t in want.items() if k != "block_states"}, exact, "closed")
+    c["x"] = torch.where(shut, torch.tensor(low, dtype=dtype, device=DEV), c["x"])
+    got = _results(c)
+    for k, t in got.items():
+        assert bool(torch.isfinite(t).all()), k
+        assert bool((t == want[k]).all()), k
+    assert not bool(got["dx"][shut].any())
