@@ -56,7 +56,9 @@ extern "C" {
  *
  * dim and the strides are at most MAMBA_GATED_SCAN_MAX_DIM, batch * seqlen at
  * most 2^28 and batch * ceil(dim / 64) below 2^23 (else
- * MAMBA_ERR_UNSUPPORTED). What stands behind a row's length is never read. A NaN
+ * MAMBA_ERR_UNSUPPORTED). batch == 0 or dim == 0 is a no-op; seqlen == 0 writes hL =
+ * h0 (or zeros) and reads nothing else, whose pointers may be NULL. What stands
+ * behind a row's length is never read. A NaN
  * or infinite value stays in its channel and reaches no earlier output; where the
  * definition has an infinity, NaN may come out. Sums and states are fp32, and the
  * decay over many tokens is carried by its logarithm, so that slow channels keep
@@ -87,7 +89,7 @@ int gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
  * dh0             (batch, dim) fp32     optional; may alias dhL
  * Sums are taken in a fixed order: results are reproducible bit for bit on one
  * kind of device. batch == 0 or seqlen == 0 writes zero dlog_decay and dh0 =
- * dhL. Where nothing enters the state (a_t = 1) the derivative of w_t by
+ * dhL, and reads nothing else. Where nothing enters the state (a_t = 1) the derivative of w_t by
  * log_decay counts as zero.
  */
 int gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int dtype,

@@ -152,12 +152,15 @@ int gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
     const void* const ptrs[] = {x, decay_gate, log_decay, input_gate, lengths, h0, y, hL, block_states, workspace};
     st = check_aligned(ptrs);
     if (st != MAMBA_OK) return st;
-    if (seqlen == 0 && hL == nullptr) return MAMBA_OK;
-    int cu = 0;
-    st = mamba::current_cu_count(&cu);
-    if (st != MAMBA_OK) return st;
-    const size_t need = seqlen > 0 ? mamba::gated_scan_fwd_workspace_bytes(a, cu) : 0;
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+    int cu = 1;
+    if (seqlen > 0) {
+        st = mamba::current_cu_count(&cu);
+        if (st != MAMBA_OK) return st;
+        const size_t need = mamba::gated_scan_fwd_workspace_bytes(a, cu);
+        if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
+    } else if (hL == nullptr) {
+        return MAMBA_OK;
+    }
     set_inputs(&a, x, x_stride, decay_gate, decay_stride, log_decay, input_gate, input_stride);
     a.lengths = lengths;
     a.h0 = h0;

@@ -992,7 +992,8 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_chain_kernel(GatedSca
     put_share(Place<1>(a.dim, 0), 0);
 }
 
-// Without tokens: dh0 = dhL, no gradient of the decay.
+// Without tokens: hL = h0, dh0 = dhL, no gradient of the decay. No other input is
+// looked at, as none need be there.
 __global__ __launch_bounds__(256) void gated_scan_empty_kernel(int64_t state, int64_t dim, const float* from,
                                                                float* to, float* zero) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
@@ -1214,6 +1215,12 @@ hipError_t launch_update(const GatedScanArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+hipError_t launch_empty(int64_t state, int64_t dim, const float* from, float* to, float* zero, hipStream_t s) {
+    hipLaunchKernelGGL(gated_scan_empty_kernel, dim3(static_cast<unsigned>(stride_blocks(state > dim ? state : dim))),
+                       dim3(256), 0, s, state, dim, from, to, zero);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 // Without regard to the strides and to whether rows differ in length, which are not
@@ -1231,19 +1238,14 @@ size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu) {
 }
 
 hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
+    if (a.seqlen == 0) return launch_empty(a.batch * a.dim, a.dim, a.h0, a.hL, nullptr, s);
     if (a.io == kIoF32)
         return a.input_gate != nullptr ? launch_fwd<kIoF32, true>(a, cu, ws, s) : launch_fwd<kIoF32, false>(a, cu, ws, s);
     return a.input_gate != nullptr ? launch_fwd<kIoBF16, true>(a, cu, ws, s) : launch_fwd<kIoBF16, false>(a, cu, ws, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {
-    if (a.batch == 0 || a.seqlen == 0) {
-        const int64_t state = a.batch * a.dim;
-        hipLaunchKernelGGL(gated_scan_empty_kernel,
-                           dim3(static_cast<unsigned>(stride_blocks(state > a.dim ? state : a.dim))), dim3(256), 0, s,
-                           state, a.dim, a.dhL, a.dh0, a.dlog_decay);
-        return hipGetLastError();
-    }
+    if (a.batch == 0 || a.seqlen == 0) return launch_empty(a.batch * a.dim, a.dim, a.dhL, a.dh0, a.dlog_decay, s);
     if (a.io == kIoF32)
         return a.input_gate != nullptr ? launch_bwd<kIoF32, true>(a, cu, ws, s) : launch_bwd<kIoF32, false>(a, cu, ws, s);
     return a.input_gate != nullptr ? launch_bwd<kIoBF16, true>(a, cu, ws, s) : launch_bwd<kIoBF16, false>(a, cu, ws, s);
