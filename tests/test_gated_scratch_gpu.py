@@ -92,3 +92,32 @@ def test_no_tokens_read_nothing(b, d):
     assert lib.gated_scan_fwd(b, 0, d, 0, *none, None, _p(same), None, _p(same), None, None, 0, _stream()) == OK
     torch.cuda.synchronize()
     assert torch.equal(same, state)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16-f32", "f32"])
+@pytest.mark.parametrize("rows,dim", [(5, 7), (900, 333), (3001, 645), (2003, 1531), (1501, 2560), (701, 5001),
+                                      (401, 9001), (301, 16383), (301, 12288)])
+def test_residual_gradients_in_place(rows, dim, kind):
+    # dresidual over dtotal and dx over dy. At odd widths the last 8 values overlap the
+    # run before, in a lane of another wave where a part takes more than one: both read
+    # before the barrier of the row's sum and write behind it
+    g = torch.Generator().manual_seed(dim)
+    dtype = F32 if kind == "f32" else BF
+    wide = F32 if kind == "bf16-f32" else dtype
+    r = lambda *s, dt=dtype: torch.randn(*s, generator=g).to(dt).to(DEV)   # noqa: E731
+    total, dtotal = r(rows, dim, dt=wide), r(rows, dim, dt=wide)
+    x, dy, scale, weight = r(rows, dim), r(rows, dim), r(dim, dt=F32), r(dim, dt=F32)
+    rstd = (total.float().square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    print(f"case {rows} x {dim} {kind}", flush=True)
+    want = ms.residual_norm_bwd(total, weight, rstd, x, scale, dy=dy, dtotal=dtotal)
+    need = _size("residual_norm_bwd_workspace_size", rows, dim, _code(dtype), _code(wide))
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    dscale, dweight = torch.empty(dim, device=DEV), torch.empty(dim, device=DEV)
+    for _ in range(3):
+        d, dx = dtotal.clone(), dy.clone()
+        assert ms.load_library().residual_norm_bwd(
+            rows, dim, _code(dtype), _code(wide), _p(total), _p(weight), _p(rstd), _p(x), _p(scale), _p(dx), _p(d),
+            _p(dx), _p(d), _p(dscale), _p(dweight), _p(ws), need, _stream()) == OK
+        torch.cuda.synchronize()
+        for name, t in dict(dresidual=d, dx=dx, dscale=dscale, dweight=dweight).items():
+            assert torch.equal(t, want[name]), name
