@@ -752,6 +752,7 @@ constexpr Shape shape_for(int64_t n, bool bwd) {
 static_assert(shape_for(kGatedNormMaxDim, true).threads <= kNormMaxWaves * kWave, "the widest part has a workgroup");
 
 constexpr int kFwdWaves = 320, kBwdWaves = 8;   // to a compute unit, at least
+constexpr int64_t kSumRows = 1024;              // rows of a sum in fp32, at most
 
 // Teams stand on so many groups side by side as divide both. Workgroups for a group:
 // forward about 320 waves to a compute unit (16384 rows of 5120: 91 us, of 80 waves 99;
@@ -760,7 +761,11 @@ constexpr int kFwdWaves = 320, kBwdWaves = 8;   // to a compute unit, at least
 // stretches and every workgroup leaves its columns' sums; no more than a quarter of
 // the rows have one (1000 x 1531 in fp32 18 us, a workgroup each 23; 3000 x 1024 22 and
 // 25), unless compute units would have none (243 x 12400 37 us, a quarter 40; 8 x 14966
-// in fp32 27 and 43).
+// in fp32 27 and 43). A team adds up its rows in fp32, no more than 1024 of them: their
+// roundings come to 2^-14 of the terms at worst, and what is above, over workgroups, is
+// summed in 64 bits (262144 rows of 521 groups of 8 were 8192 each, off by 1.2e-4 where
+// rows are alike, and took 17.1 ms, now 12.4). Fewer would have more workgroups at once than the
+// memory likes: 524288 x 2048 2.2 ms, 256 rows each 2.5.
 Layout layout_for(int64_t rows, int64_t groups, const Shape& sh, int cu, bool bwd) {
     const int teams = sh.threads / sh.lanes;
     int across = 1;
@@ -771,6 +776,8 @@ Layout layout_for(int64_t rows, int64_t groups, const Shape& sh, int cu, bool bw
     int64_t slots = each * cu / blocks;
     if (bwd && slots > most / 4) slots = most / 4 > few ? most / 4 : few;
     if (slots > most) slots = most;
+    const int64_t least = (most + kSumRows - 1) / kSumRows;
+    if (bwd && slots < least) slots = least;
     return {sh.lanes, across, static_cast<int>(slots < 1 ? 1 : slots)};
 }
 
@@ -865,6 +872,8 @@ hipError_t launch_zero(int64_t dim, float* out0, float* out1, hipStream_t s) {
 
 }  // namespace
 
+// (2^26 columns, more than a launch's threads count, have one slot in all tensors that
+// fit the memory.)
 hipError_t launch_column_sums(int64_t dim, int64_t slots, const float* partial, float* out0, float* out1,
                               hipStream_t s) {
     hipLaunchKernelGGL(column_sums_kernel,
