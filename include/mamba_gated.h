@@ -85,7 +85,9 @@ int gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
  * dx, ddecay_gate (batch, seqlen, dim)  I/O dtype, dense; written; zeros behind a
  *                                       row's length
  * dinput_gate     the same; required with input_gate, else not written
- * dlog_decay      (dim) fp32            optional, summed over rows and tokens
+ * dlog_decay      (dim) fp32            optional, summed over rows and tokens; without
+ *                                       it sequences of fewer than 512 tokens need no
+ *                                       workspace
  * dh0             (batch, dim) fp32     optional; may alias dhL
  * Sums are taken in a fixed order: results are reproducible bit for bit on one
  * kind of device. batch == 0 or seqlen == 0 writes zero dlog_decay and dh0 =

@@ -193,24 +193,24 @@ int gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
                                 dhL, dx,          ddecay_gate, dinput_gate, dlog_decay, dh0,      workspace};
     st = check_aligned(ptrs);
     if (st != MAMBA_OK) return st;
+    a.lengths = lengths;
+    a.dlog_decay = dlog_decay;
     int cu = 1;
     if (tokens) {
         st = mamba::current_cu_count(&cu);
         if (st != MAMBA_OK) return st;
-        const size_t need = mamba::gated_scan_bwd_workspace_bytes(a, cu);
+        const size_t need = mamba::gated_scan_bwd_needed_bytes(a, cu);
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
     } else if (dlog_decay == nullptr && dh0 == nullptr) {
         return MAMBA_OK;
     }
     set_inputs(&a, x, x_stride, decay_gate, decay_stride, log_decay, input_gate, input_stride);
-    a.lengths = lengths;
     a.states = const_cast<float*>(block_states);
     a.dy = dy;
     a.dhL = dhL;
     a.dx = dx;
     a.ddecay = ddecay_gate;
     a.dinput = dinput_gate;
-    a.dlog_decay = dlog_decay;
     a.dh0 = dh0;
     return mamba::launch_gated_scan_bwd(a, cu, workspace, stream) == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }

@@ -1144,6 +1144,14 @@ size_t chain_bytes(const Chain& ch) {
     return 256 + static_cast<size_t>(ch.words()) * sizeof(Word) + (static_cast<size_t>(ch.pairs) * 4 + 15) / 16 * 16;
 }
 
+// Of the backward pass, with a share of the decay's gradient for each row, or tile.
+size_t bwd_bytes(const GatedScanArgs& a, bool chain, bool shares) {
+    const size_t row = shares ? static_cast<size_t>(a.batch) * a.dim * sizeof(float) : 0;
+    if (!chain) return row;
+    const Chain ch = chain_of(a, nullptr, true);
+    return chain_bytes(ch) + ch.tiles * row;
+}
+
 // Clears the chain's words; sets its grid: a workgroup for every tile up to two
 // rounds of them (of 8 waves, one to a compute unit), else one for each unit.
 hipError_t begin_chain(Chain& ch, int cu, unsigned* grid, hipStream_t s) {
@@ -1231,10 +1239,12 @@ size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu) {
 }
 
 size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu) {
-    const size_t walk = static_cast<size_t>(a.batch) * a.dim * sizeof(float);
-    if (!may_chain(a, true, cu)) return walk;
-    const Chain ch = chain_of(a, nullptr, true);
-    return chain_bytes(ch) + ch.tiles * walk;   // a share of the decay's gradient for each tile
+    return bwd_bytes(a, may_chain(a, true, cu), true);
+}
+
+// What a call uses of it.
+size_t gated_scan_bwd_needed_bytes(const GatedScanArgs& a, int cu) {
+    return bwd_bytes(a, chained(a, true, cu), a.dlog_decay != nullptr);
 }
 
 hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s) {

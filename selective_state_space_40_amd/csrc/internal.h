@@ -308,6 +308,7 @@ struct GatedScanArgs {
 
 size_t gated_scan_fwd_workspace_bytes(const GatedScanArgs& a, int cu);
 size_t gated_scan_bwd_workspace_bytes(const GatedScanArgs& a, int cu);
+size_t gated_scan_bwd_needed_bytes(const GatedScanArgs& a, int cu);   // with lengths and dlog_decay set
 hipError_t launch_gated_scan_fwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s);
 hipError_t launch_gated_scan_bwd(const GatedScanArgs& a, int cu, void* ws, hipStream_t s);
 hipError_t launch_gated_scan_update(const GatedScanArgs& a, hipStream_t s);

@@ -121,3 +121,27 @@ def test_residual_gradients_in_place(rows, dim, kind):
         torch.cuda.synchronize()
         for name, t in dict(dresidual=d, dx=dx, dscale=dscale, dweight=dweight).items():
             assert torch.equal(t, want[name]), name
+
+
+@TYPES
+def test_no_scratch_where_none_is_used(dtype):
+    # a row walked keeps its share of the decay's gradient in scratch, and nothing else
+    c = _sequences(3, 200, 70, dtype, 1, [200, 0, 77])
+    st, _, _, states = _forward(c, None)
+    assert st == OK and _size("gated_scan_fwd_workspace_size", 3, 200, 70, _code(dtype)) == 0
+    need = _size("gated_scan_bwd_workspace_size", 3, 200, 70, _code(dtype))
+    assert need > 0
+    st, want = _backward(c, states, torch.empty(need, dtype=torch.uint8, device=DEV))
+    assert st == OK
+    assert _backward(c, states, None)[0] == WORKSPACE
+    assert _backward(c, states, torch.empty(need - 4, dtype=torch.uint8, device=DEV))[0] == WORKSPACE
+    st, got = _backward(c, states, None, dlog=False)
+    assert st == OK
+    torch.cuda.synchronize()
+    for k, t in got.items():
+        assert t is None or torch.equal(t, want[k]), k
+    # a chain's tiles learn from each other through it in any case
+    c = _sequences(1, 4000, 70, dtype, 2)
+    need = _size("gated_scan_bwd_workspace_size", 1, 4000, 70, _code(dtype))
+    states = _forward(c, torch.empty(need, dtype=torch.uint8, device=DEV))[3]
+    assert _backward(c, states, None, dlog=False)[0] == WORKSPACE
