@@ -145,3 +145,39 @@ def test_no_scratch_where_none_is_used(dtype):
     need = _size("gated_scan_bwd_workspace_size", 1, 4000, 70, _code(dtype))
     states = _forward(c, torch.empty(need, dtype=torch.uint8, device=DEV))[3]
     assert _backward(c, states, None, dlog=False)[0] == WORKSPACE
+
+
+@TYPES
+@pytest.mark.parametrize("b,n,d,lens", [(2, 9000, 130, [9000, 7001]), (1, 4100, 65, None), (513, 1500, 8, "many")], ids=str)
+def test_results_whatever_the_scratch_holds(b, n, d, lens, dtype):
+    # each call's scratch filled by the test: zeros (states and sums of nothing), all
+    # ones (a word that is not there yet), 0x7f, what the call before left, and what one
+    # of other sizes left
+    if lens == "many":
+        lens = torch.randint(0, n + 1, (b,), generator=torch.Generator().manual_seed(b)).tolist()
+    c, other = _sequences(b, n, d, dtype, 6, lens), _sequences(1, 7777, 192, dtype, 7)
+    sizes = [_size(f"gated_scan_{w}_workspace_size", *s, _code(dtype)) for w in ("fwd", "bwd")
+             for s in ((b, n, d), (1, 7777, 192))]
+    assert min(sizes) > 0
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device=DEV)
+    print(f"case {b} x {n} x {d} {dtype}", flush=True)
+    want = None
+    for fill in (0, 0xff, 0x7f, "left", "other"):
+        for call in ("forward", "backward"):
+            if fill == "other":
+                st, _, _, s = _forward(other, ws)
+                assert st == OK and _backward(other, s, ws)[0] == OK
+            elif fill != "left":
+                ws.fill_(fill)
+            if call == "forward":
+                st, *got = _forward(c, ws)
+            else:
+                st, g = _backward(c, got[2], ws)
+                got += g.values()
+            assert st == OK
+        torch.cuda.synchronize()
+        want = want or [t.clone() for t in got]
+        for i, (t, e) in enumerate(zip(got, want)):
+            assert torch.equal(t, e), (fill, i)
+    f = ms.gated_scan_fwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], c["h0"], lengths=c["lengths"])
+    assert torch.equal(f[0], want[0]) and torch.equal(f[1], want[1])
