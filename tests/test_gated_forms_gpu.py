@@ -109,3 +109,50 @@ def test_forms_that_other_tests_mean(b, n, d, ragged, want, dtype):
     assert chain == (want == "chain")
     if want != "walk forward":
         assert _chained(lambda: _backward(c, got["block_states"]))[0] == chain
+
+
+def _slice(t, wide):
+    """The same values in a wider tensor of its own, whose rows are `wide` apart."""
+    base = torch.full((*t.shape[:-1], wide), float("nan"), dtype=t.dtype, device=DEV)
+    base[..., :t.shape[-1]] = t
+    assert base.data_ptr() % 16 == 0
+    return base[..., :t.shape[-1]]
+
+
+# two channels to a lane forward; the odd stride at each input by turns; all unlike;
+# the single token's four channels a lane, and not
+STRIDES = [(200, 208, 216), (201, 200, 200), (200, 203, 200), (200, 200, 207), (201, 203, 207), (202, 206, 210)]
+
+
+@TYPES
+@pytest.mark.parametrize("strides", STRIDES, ids=str)
+@pytest.mark.parametrize("n,lens", [(90, None), (1300, None), (1300, [1300, 801])], ids=["walk", "chain", "ragged"])
+def test_inputs_of_unlike_strides(strides, n, lens, dtype):
+    for d in (64, 66):
+        c = _make(2, n, d, dtype, d, lengths=lens)
+        want = ref.scan(**c)
+        for k in ("block_states", "block_states_size"):
+            want[k] = _live(c, want[k])
+        for k, wide in zip(("x", "decay_gate", "input_gate"), strides):
+            c[k] = _slice(c[k], wide)
+        _say(f"case {strides} {n} x {d} {dtype}")
+        chain, got = _chained(lambda: _forward(c))
+        assert chain == (n > 1000)
+        grads = _backward(c, got["block_states"])
+        got["block_states"] = _live(c, got["block_states"])
+        ref.check_scan(got, want, f"{strides}")
+        ref.check_scan(grads, want, f"{strides}")
+
+
+@TYPES
+@pytest.mark.parametrize("strides", STRIDES, ids=str)
+def test_single_tokens_of_unlike_strides(strides, dtype):
+    for d in (64, 66, 63):
+        c = _make(5, 1, d, dtype, d)
+        want = ref.scan(**{k: v for k, v in c.items() if k not in ("dy", "dhL")})
+        h = c["h0"].clone()
+        x, dg, ig = (_slice(c[k][:, 0], wide) for k, wide in zip(("x", "decay_gate", "input_gate"), strides))
+        _say(f"case token {strides} {d} {dtype}")
+        y = ms.gated_scan_update(h, x, dg, c["log_decay"], ig)
+        ref.within(y, want["y"][:, 0], ref.STATE * want["y_size"][:, 0], "y")
+        ref.within(h, want["hL"], ref.STATE * want["hL_size"], "state")
