@@ -46,7 +46,10 @@ fp32, mean and rstd (..., groups) fp32. The gated recurrence takes x, gates and 
 norm x, z, y (..., dim), weight (dim,) fp32, rstd (..., groups) fp32; the residual
 norm x, y (..., dim), the residual stream (..., dim) in the dtype of x or fp32,
 scale and weight (dim,) fp32. x, z and the gates of the gated operators may be
-slices of a wider tensor's channels (rows a fixed stride apart).
+slices of a wider tensor's channels (rows a fixed stride apart) that start on 16
+bytes: the second half of a tensor of 2 dim channels does where dim is a multiple of
+8 in bfloat16, of 4 in float32; other slices raise MambaScanError and are copied
+first (contiguous()).
 """
 import collections
 import ctypes

@@ -156,3 +156,30 @@ def test_single_tokens_of_unlike_strides(strides, dtype):
         y = ms.gated_scan_update(h, x, dg, c["log_decay"], ig)
         ref.within(y, want["y"][:, 0], ref.STATE * want["y_size"][:, 0], "y")
         ref.within(h, want["hL"], ref.STATE * want["hL_size"], "state")
+
+
+@TYPES
+def test_slices_that_start_off_16_bytes_are_refused(dtype):
+    # halves of one projection start on 16 bytes where a half is a multiple of that
+    size = 16 // (2 if dtype == BF else 4)
+    for d, fits in ((8 * size, True), (8 * size + 1, False), (8 * size + size // 2, False)):
+        both = torch.randn(3, 5, 2 * d, device=DEV).to(dtype)
+        x, z = both.split(d, -1)
+        lam = -torch.rand(d, device=DEV)
+        h = torch.zeros(3, d, device=DEV)
+        dy = torch.randn(3, 5, d, device=DEV).to(dtype)
+        rstd = torch.ones(3, 5, 1, device=DEV)
+        states = torch.zeros(3, 1, d, device=DEV)
+        calls = [lambda x, z: ms.gated_scan_fwd(x, z, lam)[0],
+                 lambda x, z: ms.gated_scan_bwd(x, z, lam, block_states=states, dy=dy)["dx"],
+                 lambda x, z: ms.gated_scan_update(h.clone(), x[:, 0], z[:, 0], lam),
+                 lambda x, z: ms.gated_norm_fwd(x, z)[0],
+                 lambda x, z: ms.gated_norm_bwd(x, z, None, rstd, dy=dy)["dx"]]
+        for i, call in enumerate(calls):
+            if fits:
+                assert torch.equal(call(x, z), call(x.contiguous(), z.contiguous())), i
+            else:
+                with pytest.raises(ms.MambaScanError) as e:
+                    call(x, z)
+                assert e.value.status == -3, i
+                call(x, z.contiguous())
