@@ -38,6 +38,14 @@ __device__ __forceinline__ float carried(float c, float G, float h) {
     return G > -1.0f ? near : far;
 }
 
+// The base-2 logarithm of a channel's decay, finite for the lowest natural one as
+// well: its product with a closed gate's 0 is 0.
+__device__ __forceinline__ float log2_of(float log_decay) {
+    constexpr float LOWEST = -3.4028235e38f;
+    const float v = log_decay * kLog2e;
+    return v < LOWEST ? LOWEST : v;   // a NaN stays one
+}
+
 // The gates of one value. s = 1 - a^2 = -2 a sinh(g): for a > 1/2 by the series,
 // whose last coefficient takes up the terms left out (1e-8 of s), as 1 - a^2
 // would lose what is left of it next to 1.
@@ -560,7 +568,7 @@ __device__ __forceinline__ void load_log_decay(const GatedScanArgs& a, const Pla
 template <int V>
 __device__ __forceinline__ void log2_decay(const uint32_t (&w)[V], float (&lam2)[V]) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) lam2[v] = __uint_as_float(w[v]) * kLog2e;
+    for (int v = 0; v < V; ++v) lam2[v] = log2_of(__uint_as_float(w[v]));
 }
 
 // A tile's whole sum for one of the workgroup's channels.
@@ -1037,7 +1045,7 @@ __global__ __launch_bounds__(256) void gated_scan_update_kernel(GatedScanArgs a)
         float o[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const Decay1 e(sigmoid(d[v]), lam.f[v] * kLog2e);
+            const Decay1 e(sigmoid(d[v]), log2_of(lam.f[v]));
             float w = __builtin_amdgcn_sqrtf(e.s);
             if (a.input_gate != nullptr) w *= sigmoid(i[v]);
             o[v] = h.f[v] = carried(h.f[v], e.g2, w * x[v]);

@@ -93,3 +93,30 @@ def test_nothing_enters_through_a_closed_gate(which, gate, n, dtype):
         assert bool(torch.isfinite(t).all()), k
         assert bool((t == want[k]).all()), k
     assert not bool(got["dx"][shut].any())
+
+
+@TYPES
+@pytest.mark.parametrize("n", [100, 1300])
+def test_decays_of_the_lowest_value(n, dtype):
+    # log_decay may be any finite number: next to -1e30, where a is 0 behind any gate
+    # that is not closed (exp(-1e30 sigmoid(-40)) is), the lowest one gives the same; behind
+    # a closed one a is 1 and nothing enters
+    c, shut = _sequences(2, n, 66, dtype, n)
+    c["decay_gate"] = torch.where(shut, torch.tensor(float("-inf"), dtype=dtype, device=DEV),
+                                  c["decay_gate"].clamp(min=-40))
+    low = torch.finfo(F32).min
+    _say(f"case {n} {dtype}")
+    c["log_decay"][1::2] = -1e30
+    want = _results(c)
+    h = c["h0"].clone()
+    token = ms.gated_scan_update(h, c["x"][:, 0], c["decay_gate"][:, 0], c["log_decay"], c["input_gate"][:, 0])
+    for k, t in want.items():
+        assert bool(torch.isfinite(t).all()), k
+    for value in (low, 0.75 * low):
+        c["log_decay"][1::2] = value
+        got = _results(c)
+        for k, t in got.items():
+            assert bool((t == want[k]).all()), (k, value)
+        h2 = c["h0"].clone()
+        again = ms.gated_scan_update(h2, c["x"][:, 0], c["decay_gate"][:, 0], c["log_decay"], c["input_gate"][:, 0])
+        assert bool((again == token).all()) and bool((h2 == h).all())
