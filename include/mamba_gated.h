@@ -138,8 +138,9 @@ typedef enum mamba_norm_gate {
  *     MAMBA_GATE_NONE     v = x            y = v rstd weight
  *     rstd = 1 / sqrt(mean(v^2) + eps)
  *
- * the mean taken over a part's dim / groups values. Sums are fp32; sigmoids of z
- * below 2^-126, the least normal fp32 number, may count as zero.
+ * the mean taken over a part's dim / groups values. Sums are fp32 (where squares of v
+ * add up past its range rstd is 0); sigmoids of z below 2^-126, the least normal fp32
+ * number, may count as zero, here and in the gradients.
  *
  * x, z     (rows, dim) I/O dtype       a row's channels are contiguous, rows
  *                                      x_stride (z_stride) >= dim elements apart

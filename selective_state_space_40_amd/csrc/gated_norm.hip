@@ -145,8 +145,9 @@ __device__ __forceinline__ char* part(void* p, int64_t row, int64_t stride, int6
 }
 
 // The parameters of a lane's values, ones where there are none. They stay in
-// registers, but for lanes of two runs, which read them for every row (KEEP false):
-// else a kernel of 1024 threads, of which 128 registers are a lane's, would spill.
+// registers, but for lanes of two runs, which read them for every row (KEEP false), as
+// a kernel of 1024 threads has 128 registers to a lane: the gradients take 88 to 128
+// without them, the forward kernels 48 to 72.
 template <int CH, bool AL, bool SHORT>
 struct Params {
     static constexpr bool KEEP = CH == 1;
@@ -269,8 +270,9 @@ struct Walk {
     __device__ __forceinline__ bool more() const { return row + step < rows; }
 };
 
-// Sums over rows of a lane's columns: in registers, or for lanes of two runs, which
-// have none left, in LDS (without them 20 to 90 registers would spill).
+// Sums over rows of a lane's columns: in registers, or for lanes of two runs in LDS
+// (in registers 20 to 90 others would spill; with an fp32 stream, or with a scale in
+// fp32, the residual gradients spill 4 to 17 all the same).
 template <int CH>
 struct Columns {
     float v[8];
@@ -301,9 +303,9 @@ struct Columns {
 
 __device__ __forceinline__ float sigmoid(float v) { return fast_rcp(1.0f + fast_exp2(-v * kLog2e)); }
 
-// Lanes of two runs load a row when they come to it: what a workgroup of that many
-// lanes loads at once is enough, and the registers of a row ahead would spill. They
-// take their runs one after the other.
+// Lanes of two runs load a row when they come to it, and take their runs one after the
+// other. In the gradients a row ahead was slower (gated, 4000 x 16384 in bf16 167 us
+// against 159); forward, where its registers would find room, it has not been tried.
 template <int CH>
 constexpr bool kAhead = CH == 1;
 
@@ -581,7 +583,8 @@ __global__ __launch_bounds__(kThreads<TEAM>) void residual_norm_fwd_kernel(Resid
 
 // SCALE: x is read and dscale formed. What is read behind the sum is loaded behind the
 // row before, which leaves no second copy of it in registers: 16384 x 5120 in bf16 192
-// us, 4000 x 16384 186, 1000 x 1531 in fp32 18.
+// us, with an fp32 stream 279; 4000 x 16384 186 and 285, in fp32 2000 x 16384 185 (4.2
+// TB/s); 1000 x 1531 in fp32 18.
 template <int IO, int RIO, int TEAM, int CH, bool AL, bool SCALE>
 __global__ __launch_bounds__(kThreads<TEAM>) void residual_norm_bwd_kernel(ResidualNormArgs a, Layout lay,
                                                                                 float* partial) {
@@ -764,8 +767,8 @@ constexpr int64_t kSumRows = 1024;              // rows of a sum in fp32, at mos
 // in fp32 27 and 43). A team adds up its rows in fp32, no more than 1024 of them: their
 // roundings come to 2^-14 of the terms at worst, and what is above, over workgroups, is
 // summed in 64 bits (262144 rows of 521 groups of 8 were 8192 each, off by 1.2e-4 where
-// rows are alike, and took 17.1 ms, now 12.4). Fewer would have more workgroups at once than the
-// memory likes: 524288 x 2048 2.2 ms, 256 rows each 2.5.
+// rows are alike, and took 17.1 ms, now 1.6e-5 and 12.4). Fewer would have more
+// workgroups at once than the memory likes: 524288 x 2048 2.2 ms, 256 rows each 2.5.
 Layout layout_for(int64_t rows, int64_t groups, const Shape& sh, int cu, bool bwd) {
     const int teams = sh.threads / sh.lanes;
     int across = 1;

@@ -581,9 +581,12 @@ __device__ __forceinline__ float2 tile_sum(const float2 (&sums)[W][kGsChannels],
 }
 
 // The forward pass, a workgroup walking one row's tiles. The waves take turns in
-// carrying the state over a tile, a lane for each channel. About 42 vector
-// instructions a value, 7 of them transcendental, keep the vector units busy for 60% of
-// the time beside 80% of the memory's rate: 8 x 2048 x 4096 in bf16 121 us (4.4 TB/s).
+// carrying the state over a tile, a lane for each channel. About 38 vector
+// instructions a value, 7 of them transcendental, keep the vector units busy for 67% of
+// the time: 8 x 2048 x 4096 in bf16 118 us (4.5 TB/s). With an input gate a lane takes
+// 139 registers, so that 3 waves find room on a SIMD and one workgroup (2 on each) on a
+// unit; narrower, what a row takes is the latency of its tiles, about 3.3 us each (8 x
+// 2048 x 1536 53 us).
 template <int IO, int V, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs a, int64_t groups) {
     typedef FwdTile<IO, V, T, W, GATED> Tile;
@@ -619,7 +622,7 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_fwd_kernel(GatedScanArgs 
 }
 
 // The forward pass as a chain. A workgroup takes tickets until none is left, one
-// ahead of the tile whose inputs are being loaded. 1 x 262144 x 2048 in bf16 957 us
+// ahead of the tile whose inputs are being loaded. 1 x 262144 x 2048 in bf16 960 us
 // (4.5 TB/s), of which the look for what enters a tile, a trip to memory in each, costs
 // 150: a wave that does nothing but look, and looking while the next tile is worked
 // through, were no faster (981 and 1491 us).
@@ -854,7 +857,7 @@ struct BwdTile {
 // first. The state entering a tile comes from the forward pass, a block's start at a
 // time, so that nothing is walked twice. About 70 vector instructions a value keep the
 // vector units busy for 59% of the time at 4 waves a SIMD: 8 x 2048 x 5120 in bf16 308
-// us (3.8 TB/s), 8 x 2048 x 4096, where all columns run at once, 234 (4.0).
+// us (3.8 TB/s), 8 x 2048 x 4096, where all columns run at once, 233 (4.1).
 template <int IO, int T, int W, bool GATED>
 __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs a, int64_t groups,
                                                                float* partial) {
@@ -908,7 +911,7 @@ __global__ __launch_bounds__(W* kWave) void gated_scan_bwd_kernel(GatedScanArgs 
     for (t0 = live * Tile::TILE; t0 < a.seqlen; t0 += Tile::TILE) Tile::none(a, at, b, t0, 0);
 }
 
-// The backward pass as a chain (1 x 65536 x 1536 in bf16 411 us, of which the looks
+// The backward pass as a chain (1 x 65536 x 1536 in bf16 415 us, of which the looks
 // cost 60): position j of a row is its j-th tile from the last one with tokens.
 // `partial` holds the decay's gradient of every (row, tile),
 // zeros for tiles without tokens.
@@ -1078,12 +1081,12 @@ int64_t groups_of(const GatedScanArgs& a) { return (a.dim + kGsChannels - 1) / k
 // The kernels' shapes: V channels to a lane, T tokens to a segment, W waves. A
 // forward tile holds 2 values a token in registers, a backward tile 7, so segments
 // are of 16 and 8 tokens where a workgroup walks a row: 8 x 2048 x 4096 in bf16 118
-// us, of 8 (4 waves of 16) 126 (128); gradients 234, of 16 the same, 8 x 2048 x 5120
+// us, of 8 (4 waves of 16) 126 (128); gradients 233, of 16 the same, 8 x 2048 x 5120
 // 308 against 328. A chain's tile has a fixed cost, the look for what enters it, and
 // waits are shorter the fewer tiles of a column are on their way, so its tiles are
-// longer: 256 tokens where two channels fit a lane (1 x 262144 x 2048 956 us; of
+// longer: 256 tokens where two channels fit a lane (1 x 262144 x 2048 960 us; of
 // 128 tokens by 128 channels 1351, by 64 channels 1490), 128 for the gradients (1 x
-// 65536 x 1536 411 us, of 64 540 to 615).
+// 65536 x 1536 415 us, of 64 540 to 615).
 template <int IO_, int V_, int T_, int W_>
 struct Shape {
     static constexpr int IO = IO_, V = V_, T = T_, W = W_, TILE = W * V * T;
@@ -1109,9 +1112,9 @@ int chain_tile(const GatedScanArgs& a, bool bwd) {
 // compute unit; in fp32, where it is bound by memory, with the columns. A chain's
 // grows with the tokens of all columns, from what clearing its words costs. Of
 // 2048 tokens in bf16, walk against chain: 32 columns 50 us against 17, 192 54
-// against 58, 256 61 against 72, 384 107 against 101, 512 117 against 128, 640 165
+// against 58, 256 61 against 72, 384 107 against 101, 512 118 against 128, 640 165
 // against 156; gradients 104 against 31, 116 against 114, 120 against 149, 198 against
-// 215, 234 against 276, 308 against 344. In fp32 32 columns 47 against 22, 128 74
+// 215, 233 against 276, 308 against 344. In fp32 32 columns 47 against 22, 128 74
 // against 60, 256 116 against 115, 512 217 against 202; gradients 99 against 36, 143
 // against 112, 211 against 200, 412 against 357. Rows of different lengths are taken
 // to hold three quarters of the longest, which a walk gains nothing from while all
