@@ -181,3 +181,28 @@ def test_results_whatever_the_scratch_holds(b, n, d, lens, dtype):
             assert torch.equal(t, e), (fill, i)
     f = ms.gated_scan_fwd(c["x"], c["decay_gate"], c["log_decay"], c["input_gate"], c["h0"], lengths=c["lengths"])
     assert torch.equal(f[0], want[0]) and torch.equal(f[1], want[1])
+
+
+@TYPES
+@pytest.mark.parametrize("rows,dim", [(900, 333), (3001, 645), (2003, 1531), (701, 5001), (401, 9001), (301, 16383)])
+def test_norms_in_place_at_odd_widths(rows, dim, dtype):
+    # outputs over inputs, where runs of neighbouring lanes and waves overlap
+    g = torch.Generator().manual_seed(dim)
+    r = lambda *s, dt=dtype: torch.randn(*s, generator=g).to(dt).to(DEV)   # noqa: E731
+    x, z, dy, w, sc = r(rows, dim), r(rows, dim), r(rows, dim), r(dim, dt=F32), r(dim, dt=F32)
+    print(f"case {rows} x {dim} {dtype}", flush=True)
+    for first in (True, False):
+        y, rstd = ms.gated_norm_fwd(x, z, w, gate_first=first)
+        grads = ms.gated_norm_bwd(x, z, w, rstd, dy=dy, gate_first=first)
+        for which in (0, 1):
+            a = [x.clone(), z.clone()]
+            assert torch.equal(ms.gated_norm_fwd(*a, w, gate_first=first, out=a[which])[0], y)
+        d = dy.clone()
+        more = ms.gated_norm_bwd(x, z, w, rstd, dy=d, gate_first=first, out=d)
+        for k, t in grads.items():
+            assert torch.equal(more[k], t), k
+    for res in (r(rows, dim), r(rows, dim, dt=F32)):
+        want = ms.residual_norm_fwd(x, res, sc, w)
+        a, b = x.clone(), res.clone()
+        for t, e in zip(ms.residual_norm_fwd(a, b, sc, w, out=a, total_out=b), want):
+            assert torch.equal(t, e)
