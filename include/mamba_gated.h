@@ -58,12 +58,12 @@ extern "C" {
  * most 2^28 and batch * ceil(dim / 64) below 2^23 (else
  * MAMBA_ERR_UNSUPPORTED). batch == 0 or dim == 0 is a no-op; seqlen == 0 writes hL =
  * h0 (or zeros) and reads nothing else, whose pointers may be NULL. What stands
- * behind a row's length is never read. A NaN
- * or infinite value stays in its channel and reaches no earlier output; where the
- * definition has an infinity, NaN may come out. Sums and states are fp32, and the
- * decay over many tokens is carried by its logarithm, so that slow channels keep
- * fp32's accuracy over long sequences. Decays and sigmoids
- * below 2^-126, the least normal fp32 number, may count as zero.
+ * behind a row's length is never read. A NaN or infinite value stays in its channel
+ * and reaches no earlier output; where the definition has an infinity, NaN may come
+ * out. Sums and states are fp32, and the decay over many tokens is carried by its
+ * logarithm, so that slow channels keep fp32's accuracy over long sequences. Decays
+ * and sigmoids below 2^-126, the least normal fp32 number, may count as zero, here and
+ * in the gradients.
  */
 int gated_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int dtype,
                                   size_t* bytes);
@@ -90,9 +90,9 @@ int gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const 
  *                                       workspace
  * dh0             (batch, dim) fp32     optional; may alias dhL
  * Sums are taken in a fixed order: results are reproducible bit for bit on one
- * kind of device. batch == 0 or seqlen == 0 writes zero dlog_decay and dh0 =
- * dhL, and reads nothing else. Where nothing enters the state (a_t = 1) the derivative of w_t by
- * log_decay counts as zero.
+ * kind of device. batch == 0 or seqlen == 0 writes zero dlog_decay and dh0 = dhL,
+ * and reads nothing else. Where nothing enters the state (a_t = 1) the derivative of
+ * w_t by log_decay counts as zero.
  */
 int gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int dtype,
                                   size_t* bytes);
